@@ -311,3 +311,8 @@ def tiles(model, dtype, A, B, C=None, D=None, xorsum=False, stream=None):
     if rc != 0:
         raise MmaEmuError(rc, "mma_emulate_tiles")
     return D, X
+
+
+# ------------------------------------- native training operators (mmaops.h)
+from .ops import (Checkpoint, MmaOpsError, checkpoint, layer_norm,  # noqa: E402
+                  layer_norm_backward, linear, linear_backward, restore)

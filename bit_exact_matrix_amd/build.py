@@ -10,13 +10,19 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libmmaemu.so")
 
+# the native training operators (include/mmaops.h), linked into the library
+OPS_CSRC = os.path.join(HERE, "ops_csrc")
+OPS_SOURCES = ("ops.hip", "linear_fp16.hip", "linear_bf16.hip")
+
 HIPCC_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-shared", "-fPIC",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # no packed-FP32 instruction selection anywhere in this library
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     # all packed 16-bit arithmetic in the kernels is explicit; the SLP
@@ -37,22 +43,37 @@ PROBE_SRC = os.path.join(HERE, "probe", "valu_rate.hip")
 PROBE_OUT = os.path.join(HERE, "probe", "libvalurate.so")
 
 
-def _hipcc(src: str, out: str, verbose: bool) -> str:
-    tmp = out + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, src, "-o", tmp]
+def _run(cmd, what: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError(f"hipcc failed building {os.path.basename(out)}")
+        raise RuntimeError(f"hipcc failed building {what}")
+
+
+def _hipcc(src: str, out: str, verbose: bool) -> str:
+    tmp = out + ".tmp"
+    _run([hipcc(), *HIPCC_FLAGS, "-shared", src, "-o", tmp], os.path.basename(out), verbose)
     os.replace(tmp, out)
     return out
 
 
 def build(out: str = OUT, verbose: bool = False) -> str:
-    """libmmaemu.so, the library."""
-    return _hipcc(os.path.join(CSRC, "mmaemu.hip"), out, verbose)
+    """libmmaemu.so, the library: each source compiled on its own, a few at
+    a time, then linked."""
+    srcs = [os.path.join(CSRC, "mmaemu.hip")] + [os.path.join(OPS_CSRC, f) for f in OPS_SOURCES]
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, os.path.basename(s) + ".o") for s in srcs]
+        with ThreadPoolExecutor(min(len(srcs), os.cpu_count() or 1)) as pool:
+            for f in [pool.submit(_run, [hipcc(), *HIPCC_FLAGS, "-c", s, "-o", o],
+                                  os.path.basename(s), verbose) for s, o in zip(srcs, objs)]:
+                f.result()
+        tmp = out + ".tmp"
+        _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp],
+             os.path.basename(out), verbose)
+    os.replace(tmp, out)
+    return out
 
 
 def build_probe(verbose: bool = False) -> str:

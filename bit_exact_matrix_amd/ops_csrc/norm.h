@@ -1,0 +1,473 @@
+// norm.h -- layer norm of the rows of a matrix, forward and backward, and
+// the reduction of the weight's and the bias's gradient.
+//
+// Mathematics.  mu = sum x / n, r = 1 / sqrt(sum (x - mu)^2 / n + eps), the
+// second sum over the centred values (a difference of two large sums would
+// lose what the row's offset holds).  Backward, with xh = (x - mu) r and
+// h = dy w: dx = r (h - sum h / n - xh sum(h xh) / n), dw = sum over rows of
+// dy xh, db = sum over rows of dy.  All in FP32.
+//
+// What bounds both is memory: each element is read once and written once,
+// and a row stays in registers between its sums and its output.  A row is
+// held by GT lanes, NV vectors of 16 bytes each; a workgroup of GT * G
+// lanes works on G rows at a time and walks the matrix, so weight and bias
+// are loaded once and the weight gradient's sums stay in registers until
+// the workgroup's last row.  Each workgroup then writes one row of partial
+// sums, and a second kernel adds those in workgroup order: the result does
+// not depend on which workgroup ran first.
+#ifndef MMAOPS_NORM_H
+#define MMAOPS_NORM_H
+
+#include "ops_common.h"
+
+namespace mmaops {
+
+template <int DT>
+constexpr int kVec = 16 / (DT == kFP32 ? 4 : 2);  // elements of a 16-byte vector
+
+// Sums of N values over the GT lanes of a row, the same in each of them.
+// `lds` has 2 * 16 * N floats: two buffers that calls use in turn, so that
+// one barrier a call is enough (a lane can write a buffer again only after
+// the barrier of the call between, which every reader of it has reached).
+template <int GT, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* lds, int& turn) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (GT > 64) {
+    constexpr int W = GT / 64;
+    float* const buf = lds + turn * 16 * N;
+    turn ^= 1;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) buf[wave * N + i] = v[i];
+    }
+    __syncthreads();
+    const int first = wave / W * W;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) s += buf[(first + w) * N + i];
+      v[i] = s;
+    }
+  }
+}
+
+struct NormArgs {
+  const void* x;
+  int64_t ldx;
+  const uint8_t* codes;  // backward: the checkpoint in x's place
+  const uint8_t* scales;
+  const void* weight;
+  const void* bias;
+  void* y;
+  int64_t ldy;
+  float* mean;
+  float* rstd;
+  uint8_t* codes_out;
+  uint8_t* scales_out;
+  int64_t rows;
+  int cols;
+  float eps;
+  // backward
+  const void* dy;
+  int64_t lddy;
+  float* partial;  // [gridDim.x][2][cols]
+};
+
+// weight or bias of a lane's vectors, `fill` where there is none
+template <int PDT, int V, int NV, int GT>
+__device__ __forceinline__ void load_param(const void* p, int lane, int cols, float fill,
+                                           float (&v)[NV][V]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * GT + lane) * V;
+    const int n = cols - c;
+    if (p && n > 0) {
+      unpack(load_pack<PDT, V>((const elem_t<PDT>*)p + c, n), v[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[j][i] = fill;
+    }
+  }
+}
+
+template <int DT, int PDT, int GT, int NV, int G, bool SAVE>
+__global__ __launch_bounds__(GT* G) void norm_kernel(NormArgs a) {
+  constexpr int V = kVec<DT>;
+  using E = elem_t<DT>;
+  __shared__ float lds[2 * 16];
+  const int lane = threadIdx.x % GT, g = threadIdx.x / GT;
+  int turn = 0;
+  float w[NV][V], b[NV][V];
+  load_param<PDT, V, NV, GT>(a.weight, lane, a.cols, 1.0f, w);
+  load_param<PDT, V, NV, GT>(a.bias, lane, a.cols, 0.0f, b);
+  const float inv_n = 1.0f / (float)a.cols;
+  const float limit = save_limit(DT);
+  for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < a.rows; r0 += (int64_t)gridDim.x * G) {
+    const int64_t row = r0 + g;
+    const bool live = row < a.rows;
+    const E* const x = (const E*)a.x + (live ? row : 0) * a.ldx;
+    float v[NV][V];
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * GT + lane) * V;
+      unpack(load_pack<DT, V>(x + c, live ? a.cols - c : 0), v[j]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[0] += v[j][i];
+    }
+    if constexpr (SAVE) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * GT + lane) * V;
+        const int n = live ? a.cols - c : 0;
+        Codes<V> q;
+        const int sc = encode<V>(v[j], n, limit, q);
+        if (n > 0) {
+          store_codes<V>(a.codes_out + row * a.cols + c, q, n);
+          if (c % kBlock == 0)
+            a.scales_out[row * ((a.cols + kBlock - 1) / kBlock) + c / kBlock] = (uint8_t)sc;
+        }
+      }
+    }
+    row_sum<GT, 1>(s, lds, turn);
+    const float mu = s[0] * inv_n;
+    s[0] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int n = a.cols - (j * GT + lane) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[j][i] = i < n ? v[j][i] - mu : 0.0f;
+        s[0] += v[j][i] * v[j][i];
+      }
+    }
+    row_sum<GT, 1>(s, lds, turn);
+    const float r = 1.0f / sqrtf(s[0] * inv_n + a.eps);
+    if (!live) continue;
+    E* const y = (E*)a.y + row * a.ldy;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * GT + lane) * V;
+      float o[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = v[j][i] * r * w[j][i] + b[j][i];
+      store_pack<DT, V>(y + c, pack<DT, V>(o), a.cols - c);
+    }
+    if (lane == 0 && a.mean) {
+      a.mean[row] = mu;
+      a.rstd[row] = r;
+    }
+  }
+}
+
+// x of a row's vector, from the matrix or the checkpoint
+template <int DT, bool SAVED, int V>
+struct Raw;
+template <int DT, int V>
+struct Raw<DT, false, V> {
+  Pack<DT, V> q;
+  __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int c, int n) {
+    q = load_pack<DT, V>((const elem_t<DT>*)a.x + row * a.ldx + c, n);
+  }
+  __device__ __forceinline__ void values(float (&v)[V]) const { unpack(q, v); }
+};
+template <int DT, int V>
+struct Raw<DT, true, V> {
+  Codes<V> q;
+  int s;
+  __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int c, int n) {
+    q = load_codes<V>(a.codes + row * a.cols + c, n);
+    s = n > 0 ? a.scales[row * ((a.cols + kBlock - 1) / kBlock) + c / kBlock] : 0;
+  }
+  __device__ __forceinline__ void values(float (&v)[V]) const { decode<V>(q, s, v); }
+};
+
+// dx of every row, and the workgroup's partial sums of dw and db.
+template <int DT, int PDT, int GT, int NV, int G, bool SAVED>
+__global__ __launch_bounds__(GT* G) void norm_backward_kernel(NormArgs a) {
+  constexpr int V = kVec<DT>;
+  using E = elem_t<DT>;
+  __shared__ float lds[2 * 16 * 2];
+  const int lane = threadIdx.x % GT, g = threadIdx.x / GT;
+  int turn = 0;
+  float w[NV][V], dw[NV][V], db[NV][V];
+  load_param<PDT, V, NV, GT>(a.weight, lane, a.cols, 1.0f, w);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[j][i] = db[j][i] = 0.0f;
+  const float inv_n = 1.0f / (float)a.cols;
+  const int64_t step = (int64_t)gridDim.x * G;
+
+  // the next rows' loads are in flight while this row's sums meet
+  Raw<DT, SAVED, V> xr[NV];
+  Pack<DT, V> dr[NV];
+  float mu = 0.0f, r = 0.0f;
+  auto fetch = [&](int64_t row) {
+    const bool live = row < a.rows;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * GT + lane) * V;
+      const int n = live ? a.cols - c : 0;
+      xr[j].load(a, live ? row : 0, c, n);
+      dr[j] = load_pack<DT, V>((const E*)a.dy + (live ? row : 0) * a.lddy + c, n);
+    }
+    mu = live ? a.mean[row] : 0.0f;
+    r = live ? a.rstd[row] : 0.0f;
+  };
+  int64_t r0 = (int64_t)blockIdx.x * G;
+  fetch(r0 + g);
+  for (; r0 < a.rows; r0 += step) {
+    const int64_t row = r0 + g;
+    float xh[NV][V], h[NV][V];
+    float s[2] = {0.0f, 0.0f};
+    const float rr = r, m = mu;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int n = a.cols - (j * GT + lane) * V;
+      float x[V], d[V];
+      xr[j].values(x);
+      unpack(dr[j], d);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        // a lane past the row's end holds dy = 0, which its sums take as
+        // it is; its xh must be 0, not -mu r (which may be NaN)
+        xh[j][i] = i < n ? (x[i] - m) * rr : 0.0f;
+        h[j][i] = d[i] * w[j][i];
+        s[0] += h[j][i];
+        s[1] += h[j][i] * xh[j][i];
+        dw[j][i] += d[i] * xh[j][i];
+        db[j][i] += d[i];
+      }
+    }
+    if (r0 + step < a.rows) fetch(row + step);
+    row_sum<GT, 2>(s, lds, turn);
+    if (row < a.rows && a.y) {
+      const float m0 = s[0] * inv_n, m1 = s[1] * inv_n;
+      E* const dx = (E*)a.y + row * a.ldy;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * GT + lane) * V;
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = rr * (h[j][i] - m0 - xh[j][i] * m1);
+        store_pack<DT, V>(dx + c, pack<DT, V>(o), a.cols - c);
+      }
+    }
+  }
+  if (!a.partial) return;
+  // the G rows' sums meet in LDS, in group order, one vector a time
+  float* const out = a.partial + (int64_t)blockIdx.x * 2 * a.cols;
+  if constexpr (G == 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * GT + lane) * V;
+      store_pack<kFP32, V>(out + c, pack<kFP32, V>(dw[j]), a.cols - c);
+      store_pack<kFP32, V>(out + a.cols + c, pack<kFP32, V>(db[j]), a.cols - c);
+    }
+  } else {
+    __shared__ float meet[G][GT * V];
+#pragma unroll
+    for (int k = 0; k < 2 * NV; ++k) {
+      const int j = k >> 1;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < V; ++i) meet[g][i * GT + lane] = (k & 1) ? db[j][i] : dw[j][i];
+      __syncthreads();
+      for (int t = threadIdx.x; t < GT * V; t += GT * G) {
+        const int c = j * GT * V + t;  // column, of lane t / V, element t % V
+        float s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < G; ++q) s += meet[q][(t % V) * GT + t / V];
+        if (c < a.cols) out[(k & 1) * a.cols + c] = s;
+      }
+    }
+  }
+}
+
+// Rows too long for registers: one workgroup a row, the row read again for
+// each pass (from L2, as a row is at most a few hundred KB).
+template <int DT, bool SAVE>
+__global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a, int pdt) {
+  constexpr int V = kVec<DT>, GT = 1024;
+  using E = elem_t<DT>;
+  __shared__ float lds[2 * 16];
+  int turn = 0;
+  const float inv_n = 1.0f / (float)a.cols, limit = save_limit(DT);
+  // whole waves walk the row together, so that a block's lanes are all there
+  const int end = (a.cols + 64 * V - 1) / (64 * V) * 64 * V;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const E* const x = (const E*)a.x + row * a.ldx;
+    float s[1] = {0.0f};
+    for (int c = threadIdx.x * V; c < end; c += GT * V) {
+      const int n = a.cols - c;
+      float v[V];
+      unpack(load_pack<DT, V>(x + c, n), v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[0] += v[i];
+      if constexpr (SAVE) {
+        Codes<V> q;
+        const int sc = encode<V>(v, n, limit, q);
+        if (n > 0) {
+          store_codes<V>(a.codes_out + row * a.cols + c, q, n);
+          if (c % kBlock == 0)
+            a.scales_out[row * ((a.cols + kBlock - 1) / kBlock) + c / kBlock] = (uint8_t)sc;
+        }
+      }
+    }
+    row_sum<GT, 1>(s, lds, turn);
+    const float mu = s[0] * inv_n;
+    s[0] = 0.0f;
+    for (int c = threadIdx.x * V; c < a.cols; c += GT * V) {
+      float v[V];
+      unpack(load_pack<DT, V>(x + c, a.cols - c), v);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c + i < a.cols) s[0] += (v[i] - mu) * (v[i] - mu);
+    }
+    row_sum<GT, 1>(s, lds, turn);
+    const float r = 1.0f / sqrtf(s[0] * inv_n + a.eps);
+    E* const y = (E*)a.y + row * a.ldy;
+    for (int c = threadIdx.x * V; c < a.cols; c += GT * V) {
+      float v[V];
+      unpack(load_pack<DT, V>(x + c, a.cols - c), v);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c + i < a.cols) {
+          const float w = a.weight ? load_any(a.weight, c + i, pdt) : 1.0f;
+          const float b = a.bias ? load_any(a.bias, c + i, pdt) : 0.0f;
+          v[i] = (v[i] - mu) * r * w + b;
+        }
+      store_pack<DT, V>(y + c, pack<DT, V>(v), a.cols - c);
+    }
+    if (threadIdx.x == 0 && a.mean) {
+      a.mean[row] = mu;
+      a.rstd[row] = r;
+    }
+  }
+}
+
+template <int DT, bool SAVED>
+__global__ __launch_bounds__(1024) void norm_long_dx_kernel(NormArgs a, int pdt) {
+  constexpr int V = kVec<DT>, GT = 1024;
+  using E = elem_t<DT>;
+  __shared__ float lds[2 * 16 * 2];
+  int turn = 0;
+  const float inv_n = 1.0f / (float)a.cols;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const float r = a.rstd[row], mu = a.mean[row];
+    const E* const dy = (const E*)a.dy + row * a.lddy;
+    E* const dx = (E*)a.y + row * a.ldy;
+    float s[2] = {0.0f, 0.0f};
+    float m0 = 0.0f, m1 = 0.0f;
+    for (int pass = 0; pass < 2; ++pass) {
+      for (int c = threadIdx.x * V; c < a.cols; c += GT * V) {
+        const int n = a.cols - c;
+        Raw<DT, SAVED, V> xr;
+        float x[V], d[V];
+        xr.load(a, row, c, n);
+        xr.values(x);
+        unpack(load_pack<DT, V>(dy + c, n), d);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (i >= n) break;
+          const float w = a.weight ? load_any(a.weight, c + i, pdt) : 1.0f;
+          const float xh = (x[i] - mu) * r, h = d[i] * w;
+          if (pass == 0) {
+            s[0] += h;
+            s[1] += h * xh;
+          } else {
+            d[i] = r * (h - m0 - xh * m1);
+          }
+        }
+        if (pass == 1) store_pack<DT, V>(dx + c, pack<DT, V>(d), n);
+      }
+      if (pass == 0) {
+        row_sum<GT, 2>(s, lds, turn);
+        m0 = s[0] * inv_n;
+        m1 = s[1] * inv_n;
+      }
+    }
+  }
+}
+
+// Partial sums of dw and db over a run of rows, for the columns of one
+// workgroup (64 lanes of V columns each, four waves over the rows).
+template <int DT, bool SAVED>
+__global__ __launch_bounds__(256) void norm_long_dw_kernel(NormArgs a, int64_t run) {
+  constexpr int V = kVec<DT>;
+  using E = elem_t<DT>;
+  __shared__ float meet[2][4][64 * V];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = (blockIdx.x * 64 + lane) * V, n = a.cols - c;
+  const int64_t r0 = blockIdx.y * run, r1 = r0 + run < a.rows ? r0 + run : a.rows;
+  float dw[V], db[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) dw[i] = db[i] = 0.0f;
+  if (n > 0)
+    for (int64_t row = r0 + wave; row < r1; row += 4) {
+      const float r = a.rstd[row], mu = a.mean[row];
+      Raw<DT, SAVED, V> xr;
+      float x[V], d[V];
+      xr.load(a, row, c, n);
+      xr.values(x);
+      unpack(load_pack<DT, V>((const E*)a.dy + row * a.lddy + c, n), d);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        dw[i] += d[i] * ((x[i] - mu) * r);
+        db[i] += d[i];
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    meet[0][wave][i * 64 + lane] = dw[i];
+    meet[1][wave][i * 64 + lane] = db[i];
+  }
+  __syncthreads();
+  if (wave < 2) {
+    float* const out = a.partial + ((int64_t)blockIdx.y * 2 + wave) * a.cols;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float s = 0.0f;
+      for (int q = 0; q < 4; ++q) s += meet[wave][q][i * 64 + lane];
+      if (i < n) out[c + i] = s;
+    }
+  }
+}
+
+// Column sums of `count` rows of partial sums, in row order within each of
+// 16 runs and then in run order.  lane = column; blockIdx.y picks one of
+// the interleaved matrices (row p of matrix y starts at (p * gridDim.y + y)
+// * cols).
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, int count,
+                                                          int64_t cols, void* out0, void* out1,
+                                                          int dt) {
+  __shared__ float meet[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  void* const out = blockIdx.y ? out1 : out0;
+  if (!out) return;  // the whole workgroup
+  const int run = (count + 15) / 16;
+  const int p0 = wave * run, p1 = p0 + run < count ? p0 + run : count;
+  float s = 0.0f;
+  if (c < cols) {
+    const float* p = partial + blockIdx.y * cols + c;
+    const int64_t stride = (int64_t)gridDim.y * cols;
+#pragma unroll 4
+    for (int q = p0; q < p1; ++q) s += p[q * stride];
+  }
+  meet[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < cols) {
+    s = meet[0][lane];
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += meet[w][lane];
+    store_any(out, c, s, dt);
+  }
+}
+
+}  // namespace mmaops
+#endif

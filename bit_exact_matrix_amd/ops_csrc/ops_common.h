@@ -1,0 +1,290 @@
+// ops_common.h -- what the native operators share: element types, vector
+// loads, reductions, activations and the 8-bit checkpoint format.  The
+// operators themselves are stated in include/mmaops.h.
+#ifndef MMAOPS_COMMON_H
+#define MMAOPS_COMMON_H
+
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mmaops {
+
+// element types: the values of include/mmaops.h
+constexpr int kFP16 = 0, kBF16 = 1, kFP32 = 3;
+
+using half8 = __attribute__((ext_vector_type(8))) _Float16;
+using bf8 = __attribute__((ext_vector_type(8))) __bf16;
+using half4 = __attribute__((ext_vector_type(4))) _Float16;
+using f32x4 = __attribute__((ext_vector_type(4))) float;
+using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
+using u32x2 = __attribute__((ext_vector_type(2))) uint32_t;
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<kFP16> {
+  using type = _Float16;
+};
+template <>
+struct Elem<kBF16> {
+  using type = __bf16;
+};
+template <>
+struct Elem<kFP32> {
+  using type = float;
+};
+template <int DT>
+using elem_t = typename Elem<DT>::type;
+
+__host__ __device__ constexpr int elem_bytes(int dt) { return dt == kFP32 ? 4 : 2; }
+
+// One element of a type known at run time (a wave-uniform branch).
+__device__ __forceinline__ float load_any(const void* p, int64_t i, int dt) {
+  if (dt == kFP32) return ((const float*)p)[i];
+  if (dt == kFP16) return (float)((const _Float16*)p)[i];
+  return (float)((const __bf16*)p)[i];
+}
+
+__device__ __forceinline__ void store_any(void* p, int64_t i, float v, int dt) {
+  if (dt == kFP32)
+    ((float*)p)[i] = v;
+  else if (dt == kFP16)
+    ((_Float16*)p)[i] = (_Float16)v;
+  else
+    ((__bf16*)p)[i] = (__bf16)v;
+}
+
+// V consecutive elements, in registers as they are in memory.  Global loads
+// and stores of 16 bytes need no more than the element's alignment on
+// gfx950, so rows of odd lengths and strides take the same wide accesses.
+template <int DT, int V>
+struct Pack {
+  elem_t<DT> e[V];
+};
+
+template <int DT, int V>
+__device__ __forceinline__ Pack<DT, V> load_pack(const elem_t<DT>* p) {
+  Pack<DT, V> q;
+  __builtin_memcpy(&q, p, sizeof q);
+  return q;
+}
+
+// the first n (0 to V) of them; the others are 0
+template <int DT, int V>
+__device__ __forceinline__ Pack<DT, V> load_pack(const elem_t<DT>* p, int n) {
+  if (n >= V) return load_pack<DT, V>(p);
+  Pack<DT, V> q;
+#pragma unroll
+  for (int i = 0; i < V; ++i) q.e[i] = i < n ? p[i] : (elem_t<DT>)0.0f;
+  return q;
+}
+
+template <int DT, int V>
+__device__ __forceinline__ void store_pack(elem_t<DT>* p, const Pack<DT, V>& q, int n) {
+  if (n >= V) {
+    __builtin_memcpy(p, &q, sizeof q);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < n) p[i] = q.e[i];
+}
+
+template <int DT, int V>
+__device__ __forceinline__ void unpack(const Pack<DT, V>& q, float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = (float)q.e[i];
+}
+
+template <int DT, int V>
+__device__ __forceinline__ Pack<DT, V> pack(const float (&v)[V]) {
+  Pack<DT, V> q;
+#pragma unroll
+  for (int i = 0; i < V; ++i) q.e[i] = (elem_t<DT>)v[i];
+  return q;
+}
+
+// ---------------------------------------------------------- reductions
+// Sum over the 64 lanes of a wave, the same in every lane.  The pairs are
+// the same in every lane (each step adds two values that both lanes hold),
+// so the result does not depend on the lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+// ---------------------------------------------------------- activations
+enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kSqrt2OverPi = 0.79788456080286536f;
+
+__device__ __forceinline__ float logistic(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+__device__ __forceinline__ float act_apply(float z, int act) {
+  switch (act) {
+    case kActRelu: return z < 0.0f ? 0.0f : z;  // keeps NaN
+    case kActGelu: return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    case kActGeluTanh: {
+      // 0.5 (1 + tanh(u)) = logistic(2u)
+      const float u = kSqrt2OverPi * (z + 0.044715f * z * z * z);
+      return z * logistic(2.0f * u);
+    }
+    case kActSilu: return z * logistic(z);
+    default: return z;
+  }
+}
+
+// d act / d z
+__device__ __forceinline__ float act_slope(float z, int act) {
+  switch (act) {
+    case kActRelu: return z > 0.0f ? 1.0f : 0.0f;
+    case kActGelu:
+      return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
+    case kActGeluTanh: {
+      // 0 or 1 beyond 12, where the product of a zero and a large power
+      // of z must not become NaN
+      z = z > 12.0f ? 12.0f : z < -12.0f ? -12.0f : z;
+      const float z2 = z * z;
+      const float s = logistic(2.0f * kSqrt2OverPi * (z + 0.044715f * z2 * z));
+      return s + z * s * (1.0f - s) * 2.0f * kSqrt2OverPi * (1.0f + 3.0f * 0.044715f * z2);
+    }
+    case kActSilu: {
+      const float s = logistic(z);
+      return s * (1.0f + z * (1.0f - s));
+    }
+    default: return 1.0f;
+  }
+}
+
+// -------------------------------------------------- 8-bit checkpoints
+// E4M3 codes with one power of two for each block of 32 elements of a row.
+// A power of two makes x / s exact, so the only rounding is the one to
+// E4M3 (nearest, ties to even), and a restored value is exact in the
+// element type that was saved: the codes do not depend on the order or
+// precision of anything computed here.
+constexpr int kBlock = 32;
+
+// The largest magnitude that a checkpoint keeps, so that a code never
+// restores to an infinity of the element type: 1.875 times its largest
+// power of two (61440 for FP16).
+__device__ __forceinline__ float save_limit(int dt) {
+  return dt == kFP16 ? 61440.0f : __uint_as_float(0x7F700000u);
+}
+
+// |x| as it enters a block's maximum: 0 for NaN and infinities.
+__device__ __forceinline__ float save_mag(float x, float limit) {
+  const float m = __builtin_fabsf(x);
+  return m < __builtin_inff() ? __builtin_fminf(m, limit) : 0.0f;
+}
+
+// The scale's exponent + 127 from the block's largest magnitude: the
+// smallest e with amax <= 448 * 2^e = 1.75 * 2^(e+8).  Adding 0x1FFFFF to
+// the pattern carries into the exponent exactly when the fraction is above
+// .75.  e is at least -117, where 448 * 2^e still covers every smaller
+// block and 2^-9 * 2^e, the smallest value, is a normal BF16 number.
+__device__ __forceinline__ int save_scale(float amax) {
+  const int e = (int)((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 127 - 8;
+  return (e < -117 ? -117 : e) + 127;
+}
+
+// 2^(s - 127), 2^(127 - s) for s in [10, 247]
+__device__ __forceinline__ float scale_up(int s) { return __uint_as_float((uint32_t)s << 23); }
+__device__ __forceinline__ float scale_down(int s) {
+  return __uint_as_float((uint32_t)(254 - s) << 23);
+}
+
+// x as it is handed to the E4M3 conversion: its limited magnitude times
+// 2^-e, or NaN where x is not finite (E4M3 has no infinity, and an
+// overflow must not come back as a number).
+__device__ __forceinline__ float save_scaled(float x, float limit, float down) {
+  const float m = __builtin_fabsf(x);
+  const float v = __builtin_copysignf(__builtin_fminf(m, limit) * down, x);
+  return m < __builtin_inff() ? v : __builtin_copysignf(__builtin_nanf(""), x);
+}
+
+// Four E4M3 codes of four scaled values (|v| <= 448 or NaN).
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+  return (uint32_t)r;
+}
+
+__device__ __forceinline__ void decode4(uint32_t w, float (&v)[4]) {
+  v[0] = __builtin_amdgcn_cvt_f32_fp8((int)w, 0);
+  v[1] = __builtin_amdgcn_cvt_f32_fp8((int)w, 1);
+  v[2] = __builtin_amdgcn_cvt_f32_fp8((int)w, 2);
+  v[3] = __builtin_amdgcn_cvt_f32_fp8((int)w, 3);
+}
+
+// V codes (4 or 8) as they are in memory, and the first n of them.
+template <int V>
+struct Codes {
+  uint32_t w[V / 4];
+};
+
+template <int V>
+__device__ __forceinline__ Codes<V> load_codes(const uint8_t* p, int n) {
+  Codes<V> c;
+  if (n >= V) {
+    __builtin_memcpy(&c, p, V);
+    return c;
+  }
+#pragma unroll
+  for (int j = 0; j < V / 4; ++j) c.w[j] = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < n) c.w[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
+  return c;
+}
+
+template <int V>
+__device__ __forceinline__ void store_codes(uint8_t* p, const Codes<V>& c, int n) {
+  if (n >= V) {
+    __builtin_memcpy(p, &c, V);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < n) p[i] = (uint8_t)(c.w[i / 4] >> (8 * (i & 3)));
+}
+
+template <int V>
+__device__ __forceinline__ void decode(const Codes<V>& c, int scale, float (&v)[V]) {
+  const float up = scale_up(scale);
+#pragma unroll
+  for (int j = 0; j < V / 4; ++j) {
+    float t[4];
+    decode4(c.w[j], t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * j + i] = t[i] * up;
+  }
+}
+
+// The codes of V consecutive elements held by each lane, where 32 / V
+// neighbouring lanes hold a block; elements past n do not count.  Returns
+// the block's scale, the same in its lanes.
+template <int V>
+__device__ __forceinline__ int encode(const float (&v)[V], int n, float limit, Codes<V>& c) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < n) amax = __builtin_fmaxf(amax, save_mag(v[i], limit));
+#pragma unroll
+  for (int m = 1; m < kBlock / V; m <<= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, m));
+  const int s = save_scale(amax);
+  const float down = scale_down(s);
+#pragma unroll
+  for (int j = 0; j < V / 4; ++j)
+    c.w[j] = encode4(save_scaled(v[4 * j], limit, down), save_scaled(v[4 * j + 1], limit, down),
+                     save_scaled(v[4 * j + 2], limit, down),
+                     save_scaled(v[4 * j + 3], limit, down));
+  return s;
+}
+
+}  // namespace mmaops
+#endif
