@@ -1,7 +1,8 @@
 // norm.h -- layer norm of the rows of a matrix, forward and backward, and
 // the reduction of the weight's and the bias's gradient.
 //
-// Mathematics.  mu = sum x / n, r = 1 / sqrt(sum (x - mu)^2 / n + eps), the
+// Mathematics.  mu = sum x / n (divided, not times 1 / n: a row of equal
+// values has no spread), r = 1 / sqrt(sum (x - mu)^2 / n + eps), the
 // second sum over the centred values (a difference of two large sums would
 // lose what the row's offset holds).  Backward, with xh = (x - mu) r and
 // h = dy w: dx = r (h - sum h / n - xh sum(h xh) / n), dw = sum over rows of
@@ -103,7 +104,7 @@ __global__ __launch_bounds__(GT* G) void norm_kernel(NormArgs a) {
   float w[NV][V], b[NV][V];
   load_param<PDT, V, NV, GT>(a.weight, lane, a.cols, 1.0f, w);
   load_param<PDT, V, NV, GT>(a.bias, lane, a.cols, 0.0f, b);
-  const float inv_n = 1.0f / (float)a.cols;
+  const float n_f = (float)a.cols;
   const float limit = save_limit(DT);
   for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < a.rows; r0 += (int64_t)gridDim.x * G) {
     const int64_t row = r0 + g;
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(GT* G) void norm_kernel(NormArgs a) {
       }
     }
     row_sum<GT, 1>(s, lds, turn);
-    const float mu = s[0] * inv_n;
+    const float mu = s[0] / n_f;
     s[0] = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(GT* G) void norm_kernel(NormArgs a) {
       }
     }
     row_sum<GT, 1>(s, lds, turn);
-    const float r = 1.0f / sqrtf(s[0] * inv_n + a.eps);
+    const float r = 1.0f / sqrtf(s[0] / n_f + a.eps);
     if (!live) continue;
     E* const y = (E*)a.y + row * a.ldy;
 #pragma unroll
@@ -199,7 +200,7 @@ __global__ __launch_bounds__(GT* G) void norm_backward_kernel(NormArgs a) {
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < V; ++i) dw[j][i] = db[j][i] = 0.0f;
-  const float inv_n = 1.0f / (float)a.cols;
+  const float n_f = (float)a.cols;
   const int64_t step = (int64_t)gridDim.x * G;
 
   // the next rows' loads are in flight while this row's sums meet
@@ -246,7 +247,7 @@ __global__ __launch_bounds__(GT* G) void norm_backward_kernel(NormArgs a) {
     if (r0 + step < a.rows) fetch(row + step);
     row_sum<GT, 2>(s, lds, turn);
     if (row < a.rows && a.y) {
-      const float m0 = s[0] * inv_n, m1 = s[1] * inv_n;
+      const float m0 = s[0] / n_f, m1 = s[1] / n_f;
       E* const dx = (E*)a.y + row * a.ldy;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -296,7 +297,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a, int pdt) {
   using E = elem_t<DT>;
   __shared__ float lds[2 * 16];
   int turn = 0;
-  const float inv_n = 1.0f / (float)a.cols, limit = save_limit(DT);
+  const float n_f = (float)a.cols, limit = save_limit(DT);
   // whole waves walk the row together, so that a block's lanes are all there
   const int end = (a.cols + 64 * V - 1) / (64 * V) * 64 * V;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -319,7 +320,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a, int pdt) {
       }
     }
     row_sum<GT, 1>(s, lds, turn);
-    const float mu = s[0] * inv_n;
+    const float mu = s[0] / n_f;
     s[0] = 0.0f;
     for (int c = threadIdx.x * V; c < a.cols; c += GT * V) {
       float v[V];
@@ -329,7 +330,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a, int pdt) {
         if (c + i < a.cols) s[0] += (v[i] - mu) * (v[i] - mu);
     }
     row_sum<GT, 1>(s, lds, turn);
-    const float r = 1.0f / sqrtf(s[0] * inv_n + a.eps);
+    const float r = 1.0f / sqrtf(s[0] / n_f + a.eps);
     E* const y = (E*)a.y + row * a.ldy;
     for (int c = threadIdx.x * V; c < a.cols; c += GT * V) {
       float v[V];
@@ -356,7 +357,7 @@ __global__ __launch_bounds__(1024) void norm_long_dx_kernel(NormArgs a, int pdt)
   using E = elem_t<DT>;
   __shared__ float lds[2 * 16 * 2];
   int turn = 0;
-  const float inv_n = 1.0f / (float)a.cols;
+  const float n_f = (float)a.cols;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const float r = a.rstd[row], mu = a.mean[row];
     const E* const dy = (const E*)a.dy + row * a.lddy;
@@ -387,8 +388,8 @@ __global__ __launch_bounds__(1024) void norm_long_dx_kernel(NormArgs a, int pdt)
       }
       if (pass == 0) {
         row_sum<GT, 2>(s, lds, turn);
-        m0 = s[0] * inv_n;
-        m1 = s[1] * inv_n;
+        m0 = s[0] / n_f;
+        m1 = s[1] / n_f;
       }
     }
   }

@@ -204,7 +204,7 @@ __device__ __forceinline__ float scale_down(int s) {
 __device__ __forceinline__ float save_scaled(float x, float limit, float down) {
   const float m = __builtin_fabsf(x);
   const float v = __builtin_copysignf(__builtin_fminf(m, limit) * down, x);
-  return m < __builtin_inff() ? v : __builtin_copysignf(__builtin_nanf(""), x);
+  return m < __builtin_inff() ? v : __builtin_nanf("");
 }
 
 // Four E4M3 codes of four scaled values (|v| <= 448 or NaN).

@@ -32,8 +32,8 @@
  *   A code is x / 2^e rounded to nearest, ties to even; a code restores to
  *   code * 2^e, which every element type here holds exactly.  Magnitudes
  *   above 61440 (FP16) or 1.875 * 2^127 are saved as that bound, so that
- *   no code restores to an infinity.  NaN and infinities are saved as NaN
- *   (E4M3 has no infinity) and do not enter the block's maximum.  Where an
+ *   no code restores to an infinity.  NaN and infinities are saved as the
+ *   code 0xFF, NaN (E4M3 has no infinity), and do not enter the block's maximum.  Where an
  *   operator reads a checkpoint, codes and scales stand in the place of
  *   the matrix, which is then NULL.  codes are read and written in whole
  *   words where they and the row length allow it; no alignment is asked.
