@@ -27,6 +27,8 @@
 #ifndef MMAOPS_LINEAR_H
 #define MMAOPS_LINEAR_H
 
+#include <type_traits>
+
 #include "ops_common.h"
 
 namespace mmaops {
@@ -168,14 +170,26 @@ struct Tile {
                                                   lane * 16) = v[i];
   }
 
-  // fragment of rows r0 .. r0 + 15 for k in [32 kk, 32 kk + 32): the lane
-  // has row r0 + (lane & 15) and 8 k from 8 (lane >> 4)
-  template <typename F>
-  static __device__ __forceinline__ F frag(const lds_char* tile, int r0, int kk, int lane) {
+  // Fragment i, rows r0 + 16 i .. + 15, for k in [32 kk, 32 kk + 32): the
+  // lane has row r0 + 16 i + (lane & 15) and 8 k from 8 (lane >> 4).  The
+  // swaps depend on the lane alone, so an address is one per-lane base, an
+  // exclusive or and constants (r0 is a multiple of the rows that the
+  // wave's fragments span, a power of two, so r0 / 16 and i share no bit).
+  static __device__ __forceinline__ uint32_t base(int r0, int lane) {
     if constexpr (LAYOUT == 0) {
-      const int row = r0 + (lane & 15), c = kk * 4 + (lane >> 4);
-      return *(const __attribute__((address_space(3))) F*)(tile + row * (BK * 2) +
-                                                           ((c ^ swap_of(row)) * 16));
+      const int row = r0 + (lane & 15);
+      return row * (BK * 2) + (((lane >> 4) ^ swap_of(row)) * 16);
+    } else {
+      const int k = (lane >> 4) * 8 + ((lane & 15) >> 2);
+      return k * (R * 2) + (((r0 / 16) ^ swap_of(k)) * 32) + (lane & 3) * 8;
+    }
+  }
+  template <typename F>
+  static __device__ __forceinline__ F frag(const lds_char* tile, uint32_t base, int kk, int i) {
+    if constexpr (LAYOUT == 0) {
+      // kk > 1 (BK > 64): chunk bits above the three that are swapped
+      return *(const __attribute__((address_space(3))) F*)(tile + (base ^ ((kk & 1) * 64)) +
+                                                           (kk >> 1) * 128 + i * 16 * BK * 2);
     } else {
       using s4 = __attribute__((ext_vector_type(4))) short;
       union {
@@ -183,52 +197,107 @@ struct Tile {
         F f;
       } u;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = kk * 32 + (lane >> 4) * 8 + h * 4 + ((lane & 15) >> 2);
+      for (int h = 0; h < 2; ++h)
         u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s4*)(tile + k * (R * 2) +
-                                                    (((r0 / 16) ^ swap_of(k)) * 32) +
-                                                    (lane & 3) * 8));
-      }
+            (__attribute__((address_space(3))) s4*)(tile + (base ^ (i * 32)) +
+                                                    (kk * 32 + h * 4) * (R * 2)));
       return u.f;
     }
   }
 };
 
 // ------------------------------------------------------------ epilogue
-// Bias, pre-activation, activation, residual and store of four columns of
-// one row; n of them are there.
-template <int DT>
-__device__ __forceinline__ void finish4(const LinearArgs& g, int64_t m, int64_t c, int n,
-                                        float (&v)[4]) {
+// Bias, pre-activation, activation, residual and store of V columns of one
+// row; n of them are there.
+template <int DT, int V>
+__device__ __forceinline__ void finish(const LinearArgs& g, int64_t m, int64_t c, int n,
+                                       float (&v)[V]) {
   using E = elem_t<DT>;
-  if (g.z) store_pack<DT, 4>((E*)g.z + m * g.ldz + c, pack<DT, 4>(v), n);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = act_apply(v[i], g.act);
+  if (g.z) store_pack<DT, V>((E*)g.z + m * g.ldz + c, pack<DT, V>(v), n);
+  act_apply_all(v, g.act);
   if (g.out_dt == kFP32) {
     if (g.residual) {
-      float r[4];
-      unpack(load_pack<kFP32, 4>((const float*)g.residual + m * g.ldr + c, n), r);
+      float r[V];
+      unpack(load_pack<kFP32, V>((const float*)g.residual + m * g.ldr + c, n), r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += r[i];
+      for (int i = 0; i < V; ++i) v[i] += r[i];
     }
-    store_pack<kFP32, 4>((float*)g.y + m * g.ldy + c, pack<kFP32, 4>(v), n);
+    store_pack<kFP32, V>((float*)g.y + m * g.ldy + c, pack<kFP32, V>(v), n);
   } else {
     if (g.residual) {
-      float r[4];
-      unpack(load_pack<DT, 4>((const E*)g.residual + m * g.ldr + c, n), r);
+      float r[V];
+      unpack(load_pack<DT, V>((const E*)g.residual + m * g.ldr + c, n), r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += r[i];
+      for (int i = 0; i < V; ++i) v[i] += r[i];
     }
-    store_pack<DT, 4>((E*)g.y + m * g.ldy + c, pack<DT, 4>(v), n);
+    store_pack<DT, V>((E*)g.y + m * g.ldy + c, pack<DT, V>(v), n);
   }
 }
 
-__device__ __forceinline__ void add_bias4(const LinearArgs& g, int64_t c, int n, float (&v)[4]) {
-  if (!g.bias) return;
+template <int V>
+__device__ __forceinline__ void load_bias(const LinearArgs& g, int64_t c, int n, float (&v)[V]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < n) v[i] += load_any(g.bias, c + i, g.bias_dt);
+  for (int i = 0; i < V; ++i)
+    v[i] = g.bias && i < n ? load_any(g.bias, c + i, g.bias_dt) : 0.0f;
+}
+
+// A wave's FM x FN fragments of sums, whose first element is C's (m0, n0),
+// to their place: the partial sums of a split product, or the output.  They
+// go through LDS (the wave's own part of it, no barrier), 32 rows at a
+// time, so that a lane then has 8 neighbouring columns and neighbouring
+// lanes a row: whole 16-byte stores, and 4 lanes for a checkpoint block.
+// A row's 16 bytes of padding spread the 16 rows of a fragment over the
+// banks.
+template <int FM, int FN>
+constexpr int kStoreBytes = (FM > 1 ? 32 : 16) * (FN * 64 + 16);
+
+template <int DT, int FM, int FN>
+__device__ __forceinline__ void store_tile(const LinearArgs& g, const f32x4 (&acc)[FM][FN],
+                                           lds_char* mem, int64_t m0, int64_t n0, int lane) {
+  constexpr int kRow = FN * 64 + 16, kPass = FM > 1 ? 2 : 1;
+  constexpr int kLanes = FN * 2, kRows = 64 / kLanes;  // lanes a row, rows at once
+  const int64_t c = n0 + (lane % kLanes) * 8;
+  const int n = g.N - c < 8 ? (int)(g.N - c) : 8;
+  const float limit = save_limit(DT);
+  float bias[8];
+  if (!g.partial) load_bias<8>(g, c, n, bias);
+#pragma unroll
+  for (int i = 0; i < FM; i += kPass) {
+#pragma unroll
+    for (int h = 0; h < kPass; ++h)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        *(__attribute__((address_space(3))) f32x4*)(mem + (h * 16 + (lane & 15)) * kRow + j * 64 +
+                                                    (lane >> 4) * 16) = acc[i + h][j];
+#pragma unroll 1
+    for (int r = lane / kLanes; r < kPass * 16; r += kRows) {
+      const int64_t m = m0 + i * 16 + r;
+      const __attribute__((address_space(3))) f32x4* const p =
+          (const __attribute__((address_space(3))) f32x4*)(mem + r * kRow + (lane % kLanes) * 32);
+      const f32x4 lo = p[0], hi = p[1];
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      if (g.partial) {
+        if (m < g.M && n > 0)
+          store_pack<kFP32, 8>(g.partial + ((int64_t)blockIdx.y * g.M + m) * g.N + c,
+                               pack<kFP32, 8>(v), n);
+        continue;
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] += bias[q];
+      if constexpr (FN % 2 == 0) {
+        if (g.codes) {  // a row's lanes are here together
+          Codes<8> q;
+          const int s = encode<8>(v, n, limit, q);
+          if (m < g.M && n > 0) {
+            store_codes<8>(g.codes + m * g.N + c, q, n);
+            if (c % kBlock == 0)
+              g.scales[m * ((g.N + kBlock - 1) / kBlock) + c / kBlock] = (uint8_t)s;
+          }
+        }
+      }
+      if (m < g.M && n > 0) finish<DT, 8>(g, m, c, n, v);
+    }
+  }
 }
 
 // Which tile a workgroup takes.  Workgroups go to the 8 XCDs in turn, so
@@ -284,6 +353,7 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const uint32_t base_a = TA::base(wm * (BM / WM), lane), base_b = TB::base(wn * (BN / WN), lane);
 
   auto compute = [&](int stage) {
     const lds_char* const ta = lds + stage * kStage;
@@ -292,11 +362,9 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
     for (int kk = 0; kk < BK / 32; ++kk) {
       F fa[FM], fb[FN];
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-        fb[j] = TB::template frag<F>(tb, wn * (BN / WN) + j * 16, kk, lane);
+      for (int j = 0; j < FN; ++j) fb[j] = TB::template frag<F>(tb, base_b, kk, j);
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-        fa[i] = TA::template frag<F>(ta, wm * (BM / WM) + i * 16, kk, lane);
+      for (int i = 0; i < FM; ++i) fa[i] = TA::template frag<F>(ta, base_a, kk, i);
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -375,80 +443,147 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
     }
   }
 
-  // lane: row lane & 15 of each 16 x 16 tile, columns 4 (lane >> 4) .. + 3
-  const int64_t row0 = m0 + wm * (BM / WM) + (lane & 15);
-  const int64_t col0 = n0 + wn * (BN / WN) + (lane >> 4) * 4;
-  if (g.partial) {
-    float* const out = g.partial + (int64_t)blockIdx.y * g.M * g.N;
+  static_assert(NW * kStoreBytes<FM, FN> <= STAGES * kStage, "the epilogue's LDS");
+  __syncthreads();
+  store_tile<DT, FM, FN>(g, acc, lds + wave * kStoreBytes<FM, FN>, m0 + wm * (BM / WM),
+                         n0 + wn * (BN / WN), lane);
+}
+
+// The largest tile, 256 x 256: four waves, one for each SIMD, with 128 x
+// 128 each. A wave of that size reads 1 KiB of LDS for 16 matrix
+// instructions, where 128 x 64 reads 1.5 KiB: with eight waves LDS reads
+// and the tile's arrival would take as many cycles as the products.  With
+// one wave a SIMD nothing else hides a wait, so the loop is laid out by
+// hand.  A step of BK = 64 has two halves of K; while one half's products
+// run, the fragments of the next half are read, two for every eight
+// products, and the loads of the step after next are issued.  One wait and
+// one barrier a step, half a step after the loads it waits for were needed
+// at the earliest and a step after they were issued.
+template <int DT, int LA, int LB>
+__global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
+  constexpr int BM = 256, BN = 256, BK = 64, NW = 4, FM = 8, FN = 8;
+  using TA = Tile<BM, BK, LA, NW>;
+  using TB = Tile<BN, BK, LB, NW>;
+  using F = typename Mfma<DT>::frag;
+  constexpr int kStage = TA::kBytes + TB::kBytes;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
+  lds_char* const lds = (lds_char*)smem;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  int tm, tn;
+  tile_of(g.tiles_m, g.tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int have_m = g.M - m0 < BM ? (int)(g.M - m0) : BM;
+  const int have_n = g.N - n0 < BN ? (int)(g.N - n0) : BN;
+  const int64_t steps = (g.K + BK - 1) / BK;
+  const int64_t per = (steps + g.splits - 1) / g.splits;
+  const int64_t s0 = blockIdx.y * per;
+  int64_t s1 = s0 + per < steps ? s0 + per : steps;
+  const int64_t a_step = (LA == 0 ? BK : BK * g.lda) * 2;
+  const int64_t b_step = (LB == 0 ? BK : BK * g.ldb) * 2;
+  const char* a = (const char*)g.a + (LA == 0 ? m0 * g.lda : m0) * 2;
+  const char* b = (const char*)g.b + (LB == 0 ? n0 * g.ldb : n0) * 2;
+
+  f32x4 acc[FM][FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int64_t m = row0 + i * 16;
-      if (m >= g.M) continue;
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const uint32_t base_a = TA::base(wm * 128, lane);
+  const uint32_t base_b = TB::base(wn * 128, lane) + TA::kBytes;
+
+  const int tail = (int)(g.K % BK);
+  if (s0 < s1 && s1 == steps && tail) {  // the part of a step, before the others
+    s1 -= 1;
+    u32x4 v[TA::kPerWave];
+    TA::fetch(a + s1 * a_step, g.lda, have_m, tail, wave, lane, v);
+    TA::put(lds, wave, lane, v);
+    TB::fetch(b + s1 * b_step, g.ldb, have_n, tail, wave, lane, v);
+    TB::put(lds + TA::kBytes, wave, lane, v);
+    __syncthreads();
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const int64_t c = col0 + j * 16;
-        const int n = g.N - c < 4 ? (int)(g.N - c) : 4;
-        float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        store_pack<kFP32, 4>(out + m * g.N + c, pack<kFP32, 4>(v), n);
+        const F fb = TB::template frag<F>(lds, base_b, kk, j);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+          acc[i][j] = Mfma<DT>::run(fb, TA::template frag<F>(lds, base_a, kk, i), acc[i][j]);
       }
-    }
-    return;
+    __syncthreads();
   }
-  const float limit = save_limit(DT);
+  const int n = (int)(s1 - s0);
+  if (n > 0) {
+    a += s0 * a_step;
+    b += s0 * b_step;
+    uint32_t oa[TA::kPerWave], ob[TB::kPerWave];
+    TA::offsets(g.lda, have_m, wave, lane, oa);
+    TB::offsets(g.ldb, have_n, wave, lane, ob);
+    // eighth i of a step's loads
+    auto issue = [&](int i, uint32_t at) {
+      load_to_lds(a, oa[i], at + (wave * 8 + i) * 1024);
+      load_to_lds(b, ob[i], at + TA::kBytes + (wave * 8 + i) * 1024);
+    };
+    static_assert(TA::kPerWave == 8 && TB::kPerWave == 8, "eight loads of each operand");
+    F a0[FM], b0[FN], a1[FM], b1[FN];
+    // Products of the half in (fa, fb); meanwhile the half kk of stage
+    // `from` to (na, nb) and the loads of a step to LDS at `to`.
+    auto half = [&](F (&fa)[FM], F (&fb)[FN], F (&na)[FM], F (&nb)[FN], auto loads, int kk,
+                    const lds_char* from, uint32_t to) {
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t m = row0 + i * 16;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int64_t c = col0 + j * 16;
-      const int n = g.N - c < 4 ? (int)(g.N - c) : 4;
-      float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      add_bias4(g, c, n, v);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[i][j][q] = v[q];
-    }
-    if constexpr (FN % 2 == 0) {
-      if (g.codes) {
-#pragma unroll
-        for (int j = 0; j < FN; j += 2) {
-          // 32 columns: two tiles of the four lanes with this row
-          float amax = 0.0f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (col0 + (j + h) * 16 + q < g.N)
-                amax = __builtin_fmaxf(amax, save_mag(acc[i][j + h][q], limit));
-          amax = __builtin_fmaxf(amax, __shfl_xor(amax, 16));
-          amax = __builtin_fmaxf(amax, __shfl_xor(amax, 32));
-          const int s = save_scale(amax);
-          const float down = scale_down(s);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int64_t c = col0 + (j + h) * 16;
-            const int n = g.N - c < 4 ? (int)(g.N - c) : 4;
-            Codes<4> q;
-            q.w[0] = encode4(save_scaled(acc[i][j + h][0], limit, down),
-                             save_scaled(acc[i][j + h][1], limit, down),
-                             save_scaled(acc[i][j + h][2], limit, down),
-                             save_scaled(acc[i][j + h][3], limit, down));
-            if (m < g.M && n > 0) store_codes<4>(g.codes + m * g.N + c, q, n);
-          }
-          const int64_t c = col0 + j * 16;
-          if (m < g.M && c < g.N && (lane >> 4) == 0)
-            g.scales[m * ((g.N + kBlock - 1) / kBlock) + c / kBlock] = (uint8_t)s;
+      for (int i = 0; i < FM; ++i) {
+        if (i < 4) {
+          nb[2 * i] = TB::template frag<F>(from, base_b, kk, 2 * i);
+          nb[2 * i + 1] = TB::template frag<F>(from, base_b, kk, 2 * i + 1);
+        } else {
+          na[2 * i - 8] = TA::template frag<F>(from, base_a, kk, 2 * i - 8);
+          na[2 * i - 7] = TA::template frag<F>(from, base_a, kk, 2 * i - 7);
         }
-      }
-    }
-    if (m >= g.M) continue;
+        if constexpr (decltype(loads)::value) issue(i, to);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int64_t c = col0 + j * 16;
-      const int n = g.N - c < 4 ? (int)(g.N - c) : 4;
-      float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      if (n > 0) finish4<DT>(g, m, c, n, v);
+        for (int j = 0; j < FN; ++j) acc[i][j] = Mfma<DT>::run(fb[j], fa[i], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    auto meet = [&] {
+      wait_loads<0>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+    // one step further; past the last one the same again (loaded, not used)
+    int left = n;
+    auto next = [&] {
+      const bool more = --left > 0;
+      a += more ? a_step : 0;
+      b += more ? b_step : 0;
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) issue(i, lds0);
+    next();
+    meet();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) issue(i, lds0 + kStage);
+    next();
+#pragma unroll
+    for (int j = 0; j < FN; ++j) b0[j] = TB::template frag<F>(lds, base_b, 0, j);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) a0[i] = TA::template frag<F>(lds, base_a, 0, i);
+    uint32_t at = 0;  // of this step's stage
+    for (int t = 0; t < n; ++t) {
+      half(a0, b0, a1, b1, std::false_type{}, 1, lds + at, 0);
+      meet();  // step t + 1 has landed, stage `at` is read out
+      half(a1, b1, a0, b0, std::true_type{}, 0, lds + (at ^ kStage), lds0 + at);
+      next();
+      at ^= kStage;
     }
+    wait_loads<0>();
   }
+  __syncthreads();
+  store_tile<DT, FM, FN>(g, acc, lds + wave * kStoreBytes<FM, FN>, m0 + wm * 128, n0 + wn * 128,
+                         lane);
 }
 
 // The runs' sums added in run order, then the epilogue: four columns a
@@ -473,7 +608,10 @@ __global__ __launch_bounds__(256) void linear_finish_kernel(LinearArgs g) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] += u[i];
       }
-      add_bias4(g, c, n, v);
+      float bias[4];
+      load_bias<4>(g, c, n, bias);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += bias[i];
     }
     if (g.codes) {  // the eight lanes of a block are in the loop together
       Codes<4> q;
@@ -481,7 +619,7 @@ __global__ __launch_bounds__(256) void linear_finish_kernel(LinearArgs g) {
       if (n > 0) store_codes<4>(g.codes + m * g.N + c, q, n);
       if (c % kBlock == 0) g.scales[m * (quads / 8) + c / kBlock] = (uint8_t)s;
     }
-    if (n > 0) finish4<DT>(g, m, c, n, v);
+    if (n > 0) finish<DT, 4>(g, m, c, n, v);
   }
 }
 
@@ -493,7 +631,7 @@ struct TileShape {
   bool pairs;  // a wave holds whole checkpoint blocks
 };
 constexpr TileShape kTileShape[kTiles] = {
-    {256, 256, 64, 8, true}, {128, 128, 64, 4, true}, {64, 64, 64, 4, true}, {16, 64, 128, 4, false}};
+    {256, 256, 64, 4, true}, {128, 128, 64, 4, true}, {64, 64, 64, 4, true}, {16, 64, 128, 4, false}};
 
 template <int DT, int LA, int LB>
 hipError_t linear_launch_tile(int tile, bool direct, const LinearArgs& g, hipStream_t s) {
@@ -501,7 +639,7 @@ hipError_t linear_launch_tile(int tile, bool direct, const LinearArgs& g, hipStr
   if (direct) {
     switch (tile) {
       case kTileBig:
-        linear_kernel<DT, 256, 256, 64, 2, 4, LA, LB, 2, true, 2><<<grid, 512, 0, s>>>(g);
+        linear_wide_kernel<DT, LA, LB><<<grid, 256, 0, s>>>(g);
         break;
       case kTileMid:
         linear_kernel<DT, 128, 128, 64, 2, 2, LA, LB, 2, true, 2><<<grid, 256, 0, s>>>(g);

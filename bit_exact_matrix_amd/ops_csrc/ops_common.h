@@ -139,6 +139,30 @@ __device__ __forceinline__ float act_apply(float z, int act) {
   }
 }
 
+// the same for V values, one branch for all of them
+template <int V>
+__device__ __forceinline__ void act_apply_all(float (&v)[V], int act) {
+  switch (act) {
+    case kActRelu:
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = act_apply(v[i], kActRelu);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = act_apply(v[i], kActGelu);
+      break;
+    case kActGeluTanh:
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = act_apply(v[i], kActGeluTanh);
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = act_apply(v[i], kActSilu);
+      break;
+    default: break;
+  }
+}
+
 // d act / d z
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
