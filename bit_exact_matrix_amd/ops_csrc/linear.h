@@ -15,8 +15,8 @@
 // transposing LDS read, so that no operand is ever rearranged in memory.
 //
 // LDS banks.  A layout-0 tile row is BK elements; 16-byte chunk c of row r
-// is kept at chunk c ^ (r & 7), so that the 16 rows of a fragment read
-// spread over the banks.  A layout-1 tile row is one k with R columns;
+// is kept at chunk c ^ (r & 7) (c ^ (r >> 1 & 3) in a row of 4 chunks), so
+// that the rows of a fragment read spread over the banks.  A layout-1 tile row is one k with R columns;
 // 32-byte slot s of row k is kept at s ^ g(k), with g taking 8 values over
 // the 8 rows that half a wave reads at once.  The permutation is applied
 // to the global address of each lane, as the LDS side of a direct load is
@@ -85,6 +85,15 @@ __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint
       : "memory", "m0");
 }
 
+// A wave-uniform address, in scalar registers whatever the compiler keeps
+// it in.
+__device__ __forceinline__ const char* uniform(const char* p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (const char*)((uint64_t)hi << 32 | lo);
+}
+
 template <int N>
 __device__ __forceinline__ void wait_loads() {  // all but the last N, and all LDS reads
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
@@ -100,7 +109,7 @@ struct Tile {
   static constexpr int kRow = LAYOUT == 0 ? BK / 8 : R / 8;  // chunks of a tile row
 
   static __device__ __forceinline__ int swap_of(int r) {
-    if constexpr (LAYOUT == 0) return r & (kRow < 8 ? kRow - 1 : 7);
+    if constexpr (LAYOUT == 0) return kRow == 4 ? (r >> 1) & 3 : r & 7;
     constexpr int slots = R / 16;
     return ((r & 3) | ((r >> 3) & 1) << 2) & (slots < 8 ? slots - 1 : 7);
   }
@@ -134,7 +143,7 @@ struct Tile {
                                               uint32_t lds, int wave) {
 #pragma unroll
     for (int i = 0; i < kPerWave; ++i)
-      load_to_lds(base, off[i], lds + (wave * kPerWave + i) * 1024);
+      load_to_lds(uniform(base), off[i], lds + (wave * kPerWave + i) * 1024);
   }
 
   // The same through registers, for any alignment and for a tile with only
@@ -187,7 +196,7 @@ struct Tile {
   template <typename F>
   static __device__ __forceinline__ F frag(const lds_char* tile, uint32_t base, int kk, int i) {
     if constexpr (LAYOUT == 0) {
-      // kk > 1 (BK > 64): chunk bits above the three that are swapped
+      // kk & 1 is a chunk bit that the swap reaches, kk >> 1 one above
       return *(const __attribute__((address_space(3))) F*)(tile + (base ^ ((kk & 1) * 64)) +
                                                            (kk >> 1) * 128 + i * 16 * BK * 2);
     } else {
@@ -207,31 +216,42 @@ struct Tile {
 };
 
 // ------------------------------------------------------------ epilogue
-// Bias, pre-activation, activation, residual and store of V columns of one
-// row; n of them are there.
+// V columns of a row of the residual, as they are in memory.
+template <int DT, int V>
+struct Residual {
+  Pack<DT, V> own;
+  Pack<kFP32, V> wide;
+
+  __device__ __forceinline__ void load(const LinearArgs& g, int64_t m, int64_t c, int n) {
+    if (!g.residual) return;
+    if (g.out_dt == kFP32)
+      wide = load_pack<kFP32, V>((const float*)g.residual + m * g.ldr + c, n);
+    else
+      own = load_pack<DT, V>((const elem_t<DT>*)g.residual + m * g.ldr + c, n);
+  }
+};
+
+// Pre-activation, activation, residual and store of V columns of one row;
+// n of them are there.
 template <int DT, int V>
 __device__ __forceinline__ void finish(const LinearArgs& g, int64_t m, int64_t c, int n,
-                                       float (&v)[V]) {
+                                       float (&v)[V], const Residual<DT, V>& res) {
   using E = elem_t<DT>;
   if (g.z) store_pack<DT, V>((E*)g.z + m * g.ldz + c, pack<DT, V>(v), n);
   act_apply_all(v, g.act);
-  if (g.out_dt == kFP32) {
-    if (g.residual) {
-      float r[V];
-      unpack(load_pack<kFP32, V>((const float*)g.residual + m * g.ldr + c, n), r);
+  if (g.residual) {
+    float r[V];
+    if (g.out_dt == kFP32)
+      unpack(res.wide, r);
+    else
+      unpack(res.own, r);
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] += r[i];
-    }
-    store_pack<kFP32, V>((float*)g.y + m * g.ldy + c, pack<kFP32, V>(v), n);
-  } else {
-    if (g.residual) {
-      float r[V];
-      unpack(load_pack<DT, V>((const E*)g.residual + m * g.ldr + c, n), r);
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] += r[i];
-    }
-    store_pack<DT, V>((E*)g.y + m * g.ldy + c, pack<DT, V>(v), n);
+    for (int i = 0; i < V; ++i) v[i] += r[i];
   }
+  if (g.out_dt == kFP32)
+    store_pack<kFP32, V>((float*)g.y + m * g.ldy + c, pack<kFP32, V>(v), n);
+  else
+    store_pack<DT, V>((E*)g.y + m * g.ldy + c, pack<DT, V>(v), n);
 }
 
 template <int V>
@@ -261,6 +281,19 @@ __device__ __forceinline__ void store_tile(const LinearArgs& g, const f32x4 (&ac
   const float limit = save_limit(DT);
   float bias[8];
   if (!g.partial) load_bias<8>(g, c, n, bias);
+  // The residual of the next kAhead rows of the lane is under way: a load
+  // takes longer than a row's arithmetic, and with one wave a SIMD nothing
+  // else hides it.
+  constexpr int kAhead = 4;
+  const int64_t m1 = m0 + FM * 16 < g.M ? m0 + FM * 16 : g.M;
+  int64_t mr = m0 + lane / kLanes;  // the row whose residual is loaded next
+  Residual<DT, 8> ahead[kAhead];
+  auto fetch = [&](Residual<DT, 8>& r) {
+    r.load(g, mr < m1 ? mr : 0, c, mr < m1 && !g.partial ? n : 0);
+    mr += kRows;
+  };
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q) fetch(ahead[q]);
 #pragma unroll
   for (int i = 0; i < FM; i += kPass) {
 #pragma unroll
@@ -295,7 +328,11 @@ __device__ __forceinline__ void store_tile(const LinearArgs& g, const f32x4 (&ac
           }
         }
       }
-      if (m < g.M && n > 0) finish<DT, 8>(g, m, c, n, v);
+      const Residual<DT, 8> res = ahead[0];
+#pragma unroll
+      for (int q = 0; q + 1 < kAhead; ++q) ahead[q] = ahead[q + 1];
+      fetch(ahead[kAhead - 1]);
+      if (m < g.M && n > 0) finish<DT, 8>(g, m, c, n, v, res);
     }
   }
 }
@@ -454,11 +491,19 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
 // instructions, where 128 x 64 reads 1.5 KiB: with eight waves LDS reads
 // and the tile's arrival would take as many cycles as the products.  With
 // one wave a SIMD nothing else hides a wait, so the loop is laid out by
-// hand.  A step of BK = 64 has two halves of K; while one half's products
-// run, the fragments of the next half are read, two for every eight
-// products, and the loads of the step after next are issued.  One wait and
-// one barrier a step, half a step after the loads it waits for were needed
-// at the earliest and a step after they were issued.
+// hand: each LDS read and each load sits alone behind a matrix instruction,
+// as a lone wave issues one instruction every 4 cycles and a product takes
+// 16.  A step of BK = 64 runs in two halves of 64 products from registers:
+//   first half    the fragments of this step's second half are read; when
+//                 they are there (slot 40) a barrier frees the stage, and
+//                 the loads of the step after next begin to fill it
+//   (barrier: the next step has landed)
+//   second half   the fragments of the next step's first half are read, and
+//                 the loads go on
+// so a load has 1,400 to 2,400 cycles to land.  A row of 64 elements is a
+// whole 128-byte line; steps of 32 with a ring of four stages kept the
+// vector memory pipe busier than the products (8192^3, both operands with K
+// fastest: 922 us against 856).
 template <int DT, int LA, int LB>
 __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
   constexpr int BM = 256, BN = 256, BK = 64, NW = 4, FM = 8, FN = 8;
@@ -466,6 +511,8 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
   using TB = Tile<BN, BK, LB, NW>;
   using F = typename Mfma<DT>::frag;
   constexpr int kStage = TA::kBytes + TB::kBytes;
+  constexpr int kLoads = TA::kPerWave + TB::kPerWave;  // of a wave and step
+  static_assert(kLoads == 16 && TA::kPerWave == 8, "the slots below");
   __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
   lds_char* const lds = (lds_char*)smem;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
@@ -522,36 +569,12 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
     uint32_t oa[TA::kPerWave], ob[TB::kPerWave];
     TA::offsets(g.lda, have_m, wave, lane, oa);
     TB::offsets(g.ldb, have_n, wave, lane, ob);
-    // eighth i of a step's loads
-    auto issue = [&](int i, uint32_t at) {
-      load_to_lds(a, oa[i], at + (wave * 8 + i) * 1024);
-      load_to_lds(b, ob[i], at + TA::kBytes + (wave * 8 + i) * 1024);
-    };
-    static_assert(TA::kPerWave == 8 && TB::kPerWave == 8, "eight loads of each operand");
-    F a0[FM], b0[FN], a1[FM], b1[FN];
-    // Products of the half in (fa, fb); meanwhile the half kk of stage
-    // `from` to (na, nb) and the loads of a step to LDS at `to`.
-    auto half = [&](F (&fa)[FM], F (&fb)[FN], F (&na)[FM], F (&nb)[FN], auto loads, int kk,
-                    const lds_char* from, uint32_t to) {
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        if (i < 4) {
-          nb[2 * i] = TB::template frag<F>(from, base_b, kk, 2 * i);
-          nb[2 * i + 1] = TB::template frag<F>(from, base_b, kk, 2 * i + 1);
-        } else {
-          na[2 * i - 8] = TA::template frag<F>(from, base_a, kk, 2 * i - 8);
-          na[2 * i - 7] = TA::template frag<F>(from, base_a, kk, 2 * i - 7);
-        }
-        if constexpr (decltype(loads)::value) issue(i, to);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = Mfma<DT>::run(fb[j], fa[i], acc[i][j]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
-    auto meet = [&] {
-      wait_loads<0>();
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
+    // load i of a step, into the stage at `to`
+    auto issue = [&](int i, uint32_t to) {
+      if (i & 1)
+        load_to_lds(uniform(b), ob[i >> 1], to + TA::kBytes + (wave * 8 + (i >> 1)) * 1024);
+      else
+        load_to_lds(uniform(a), oa[i >> 1], to + (wave * 8 + (i >> 1)) * 1024);
     };
     // one step further; past the last one the same again (loaded, not used)
     int left = n;
@@ -560,22 +583,56 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
       a += more ? a_step : 0;
       b += more ? b_step : 0;
     };
+    auto read = [&](F (&fa)[FM], F (&fb)[FN], int q, int kk, const lds_char* from) {
+      if (q < FN)
+        fb[q] = TB::template frag<F>(from, base_b, kk, q);
+      else
+        fa[q - FN] = TA::template frag<F>(from, base_a, kk, q - FN);
+    };
+    auto barrier = [] {
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+    constexpr int kFree = 40, kFirst = 6;  // slot of the first barrier, loads before the second
+    F a0[FM], b0[FN], a1[FM], b1[FN];
+    uint32_t at = 0;  // this step's stage
+    auto first_half = [&] {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) issue(i, lds0);
-    next();
-    meet();
+      for (int s = 0; s < 64; ++s) {
+        acc[s / 8][s % 8] = Mfma<DT>::run(b0[s % 8], a0[s / 8], acc[s / 8][s % 8]);
+        if (s % 2 == 0 && s < 32) read(a1, b1, s / 2, 1, lds + at);
+        if (s == kFree) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          barrier();
+        }
+        if (s > kFree && s % 4 == 2) issue((s - kFree - 2) / 4, lds0 + at);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    auto second_half = [&] {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) issue(i, lds0 + kStage);
-    next();
+      for (int s = 0; s < 64; ++s) {
+        acc[s / 8][s % 8] = Mfma<DT>::run(b1[s % 8], a1[s / 8], acc[s / 8][s % 8]);
+        if (s % 2 == 0 && s < 32) read(a0, b0, s / 2, 0, lds + (at ^ kStage));
+        if (s % 4 == 1 && s / 4 < kLoads - kFirst) issue(kFirst + s / 4, lds0 + at);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
 #pragma unroll
-    for (int j = 0; j < FN; ++j) b0[j] = TB::template frag<F>(lds, base_b, 0, j);
+    for (int s = 0; s < 2; ++s) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) a0[i] = TA::template frag<F>(lds, base_a, 0, i);
-    uint32_t at = 0;  // of this step's stage
+      for (int i = 0; i < kLoads; ++i) issue(i, lds0 + s * kStage);
+      next();
+    }
+    wait_loads<kLoads>();
+    barrier();
+#pragma unroll
+    for (int q = 0; q < FM + FN; ++q) read(a0, b0, q, 0, lds);
     for (int t = 0; t < n; ++t) {
-      half(a0, b0, a1, b1, std::false_type{}, 1, lds + at, 0);
-      meet();  // step t + 1 has landed, stage `at` is read out
-      half(a1, b1, a0, b0, std::true_type{}, 0, lds + (at ^ kStage), lds0 + at);
+      first_half();
+      wait_loads<kFirst>();
+      barrier();
+      second_half();
       next();
       at ^= kStage;
     }
@@ -619,7 +676,11 @@ __global__ __launch_bounds__(256) void linear_finish_kernel(LinearArgs g) {
       if (n > 0) store_codes<4>(g.codes + m * g.N + c, q, n);
       if (c % kBlock == 0) g.scales[m * (quads / 8) + c / kBlock] = (uint8_t)s;
     }
-    if (n > 0) finish<DT, 4>(g, m, c, n, v);
+    if (n > 0) {
+      Residual<DT, 4> res;
+      res.load(g, m, c, n);
+      finish<DT, 4>(g, m, c, n, v, res);
+    }
   }
 }
 

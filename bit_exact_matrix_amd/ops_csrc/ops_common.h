@@ -119,21 +119,49 @@ __device__ __forceinline__ float wave_sum(float v) {
 // ---------------------------------------------------------- activations
 enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 
-constexpr float kSqrtHalf = 0.70710678118654752f;
+// An epilogue of 256 x 256 outputs on one CU takes 0.43 us for every VALU
+// instruction an element, so the functions are written for few of them:
+// hardware exp2 and reciprocal (1 ulp each) and no branches.
+constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kSqrt2OverPi = 0.79788456080286536f;
 
-__device__ __forceinline__ float logistic(float z) { return 1.0f / (1.0f + expf(-z)); }
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+
+__device__ __forceinline__ float logistic(float z) {
+  return fast_rcp(1.0f + fast_exp2(-kLog2e * z));
+}
+
+// The normal distribution's upper tail, 1 - Phi(a) for a >= 0, and exp(-a^2
+// / 2): erfc by the rational approximation 7.1.26 of Abramowitz and Stegun,
+// Handbook of Mathematical Functions (absolute error 1.5e-7), with x = a /
+// sqrt(2) and the factor 1/2 taken into the constants.
+__device__ __forceinline__ float normal_tail(float a, float& density) {
+  const float t = fast_rcp(__builtin_fmaf(0.3275911f * 0.70710678118654752f, a, 1.0f));
+  float p = __builtin_fmaf(0.5f * 1.061405429f, t, -0.5f * 1.453152027f);
+  p = __builtin_fmaf(p, t, 0.5f * 1.421413741f);
+  p = __builtin_fmaf(p, t, -0.5f * 0.284496736f);
+  p = __builtin_fmaf(p, t, 0.5f * 0.254829592f);
+  density = fast_exp2(a * a * (-0.5f * kLog2e));
+  return p * t * density;
+}
 
 __device__ __forceinline__ float act_apply(float z, int act) {
   switch (act) {
     case kActRelu: return z < 0.0f ? 0.0f : z;  // keeps NaN
-    case kActGelu: return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
-    case kActGeluTanh: {
-      // 0.5 (1 + tanh(u)) = logistic(2u)
-      const float u = kSqrt2OverPi * (z + 0.044715f * z * z * z);
-      return z * logistic(2.0f * u);
+    case kActGelu: {
+      // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|)): no cancellation in the
+      // lower tail.  The bound keeps an infinity from meeting the zero it
+      // makes (30 (1 - Phi(30)) is 0 in FP32); NaN comes through the tail.
+      float e;
+      const float a = __builtin_fabsf(z);
+      return __builtin_fmaf(-__builtin_fminf(a, 30.0f), normal_tail(a, e),
+                            __builtin_fmaxf(z, 0.0f));
     }
+    case kActGeluTanh:
+      // (1 + tanh(u)) / 2 = logistic(2u)
+      return z * logistic(2.0f * kSqrt2OverPi * z * __builtin_fmaf(0.044715f * z, z, 1.0f));
     case kActSilu: return z * logistic(z);
     default: return z;
   }
@@ -167,14 +195,17 @@ __device__ __forceinline__ void act_apply_all(float (&v)[V], int act) {
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
     case kActRelu: return z > 0.0f ? 1.0f : 0.0f;
-    case kActGelu:
-      return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
+    case kActGelu: {
+      float e;
+      const float q = normal_tail(__builtin_fabsf(z), e);
+      return __builtin_fmaf(z * e, kInvSqrt2Pi, z > 0.0f ? 1.0f - q : q);
+    }
     case kActGeluTanh: {
       // 0 or 1 beyond 12, where the product of a zero and a large power
       // of z must not become NaN
       z = z > 12.0f ? 12.0f : z < -12.0f ? -12.0f : z;
       const float z2 = z * z;
-      const float s = logistic(2.0f * kSqrt2OverPi * (z + 0.044715f * z2 * z));
+      const float s = logistic(2.0f * kSqrt2OverPi * z * __builtin_fmaf(0.044715f, z2, 1.0f));
       return s + z * s * (1.0f - s) * 2.0f * kSqrt2OverPi * (1.0f + 3.0f * 0.044715f * z2);
     }
     case kActSilu: {
