@@ -216,42 +216,56 @@ struct Tile {
 };
 
 // ------------------------------------------------------------ epilogue
-// V columns of a row of the residual, as they are in memory.
-template <int DT, int V>
-struct Residual {
-  Pack<DT, V> own;
-  Pack<kFP32, V> wide;
-
-  __device__ __forceinline__ void load(const LinearArgs& g, int64_t m, int64_t c, int n) {
-    if (!g.residual) return;
-    if (g.out_dt == kFP32)
-      wide = load_pack<kFP32, V>((const float*)g.residual + m * g.ldr + c, n);
-    else
-      own = load_pack<DT, V>((const elem_t<DT>*)g.residual + m * g.ldr + c, n);
-  }
-};
-
-// Pre-activation, activation, residual and store of V columns of one row;
-// n of them are there.
-template <int DT, int V>
-__device__ __forceinline__ void finish(const LinearArgs& g, int64_t m, int64_t c, int n,
-                                       float (&v)[V], const Residual<DT, V>& res) {
+// Pre-activation, activation, residual and store of V columns (n of them
+// there, V where FULL) of U rows m, m + step, ..; `res` has the residual's
+// elements where it is of the operands' type.
+template <int DT, int V, int U, bool FULL>
+__device__ __forceinline__ void finish(const LinearArgs& g, int64_t m, int step, int64_t c, int n,
+                                       float (&v)[U * V], const Pack<DT, V> (&res)[U]) {
   using E = elem_t<DT>;
-  if (g.z) store_pack<DT, V>((E*)g.z + m * g.ldz + c, pack<DT, V>(v), n);
-  act_apply_all(v, g.act);
-  if (g.residual) {
-    float r[V];
-    if (g.out_dt == kFP32)
-      unpack(res.wide, r);
-    else
-      unpack(res.own, r);
+  auto row = [&](int u, float (&o)[V]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] += r[i];
+    for (int i = 0; i < V; ++i) o[i] = v[u * V + i];
+  };
+  auto there = [&](int u) { return FULL || (m + u * step < g.M && n > 0); };
+  const int k = FULL ? V : n;
+  if (g.z) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float o[V];
+      row(u, o);
+      if (there(u))
+        store_pack<DT, V>((E*)g.z + (m + u * step) * g.ldz + c, pack<DT, V>(o), k);
+    }
   }
-  if (g.out_dt == kFP32)
-    store_pack<kFP32, V>((float*)g.y + m * g.ldy + c, pack<kFP32, V>(v), n);
-  else
-    store_pack<DT, V>((E*)g.y + m * g.ldy + c, pack<DT, V>(v), n);
+  act_apply_all(v, g.act);
+  if (g.out_dt != kFP32) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float o[V], r[V];
+      row(u, o);
+      if (g.residual) {
+        unpack(res[u], r);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] += r[i];
+      }
+      if (there(u))
+        store_pack<DT, V>((E*)g.y + (m + u * step) * g.ldy + c, pack<DT, V>(o), k);
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!there(u)) continue;
+      float o[V], r[V];
+      row(u, o);
+      if (g.residual) {
+        unpack(load_pack<kFP32, V>((const float*)g.residual + (m + u * step) * g.ldr + c, k), r);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] += r[i];
+      }
+      store_pack<kFP32, V>((float*)g.y + (m + u * step) * g.ldy + c, pack<kFP32, V>(o), k);
+    }
+  }
 }
 
 template <int V>
@@ -263,76 +277,114 @@ __device__ __forceinline__ void load_bias(const LinearArgs& g, int64_t c, int n,
 
 // A wave's FM x FN fragments of sums, whose first element is C's (m0, n0),
 // to their place: the partial sums of a split product, or the output.  They
-// go through LDS (the wave's own part of it, no barrier), 32 rows at a
-// time, so that a lane then has 8 neighbouring columns and neighbouring
-// lanes a row: whole 16-byte stores, and 4 lanes for a checkpoint block.
-// A row's 16 bytes of padding spread the 16 rows of a fragment over the
-// banks.
-template <int FM, int FN>
-constexpr int kStoreBytes = (FM > 1 ? 32 : 16) * (FN * 64 + 16);
+// go through LDS (the wave's own part of it, no barrier), PASS fragment
+// rows at a time, so that a lane then has 8 neighbouring columns and
+// neighbouring lanes a row: whole 16-byte stores, and 4 lanes for a
+// checkpoint block.  A row's 16 bytes of padding spread the 16 rows of a
+// fragment over the banks.  A lane takes four rows at once, so that their
+// LDS reads and functions overlap, and has the next four rows' residual on
+// its way meanwhile: with one wave a SIMD nothing else hides these.
+template <int FN, int PASS>
+constexpr int kStoreBytes = PASS * 16 * (FN * 64 + 16);
 
-template <int DT, int FM, int FN>
+template <int DT, int FM, int FN, int PASS>
 __device__ __forceinline__ void store_tile(const LinearArgs& g, const f32x4 (&acc)[FM][FN],
                                            lds_char* mem, int64_t m0, int64_t n0, int lane) {
-  constexpr int kRow = FN * 64 + 16, kPass = FM > 1 ? 2 : 1;
+  using E = elem_t<DT>;
+  using lds_f4 = __attribute__((address_space(3))) f32x4;
+  constexpr int kRow = FN * 64 + 16;
   constexpr int kLanes = FN * 2, kRows = 64 / kLanes;  // lanes a row, rows at once
+  constexpr int kPassRows = PASS * 16;
+  constexpr int kTurns = (kPassRows + kRows - 1) / kRows;
+  constexpr int U = kTurns < 4 ? kTurns : 4;
   const int64_t c = n0 + (lane % kLanes) * 8;
   const int n = g.N - c < 8 ? (int)(g.N - c) : 8;
-  const float limit = save_limit(DT);
-  float bias[8];
-  if (!g.partial) load_bias<8>(g, c, n, bias);
-  // The residual of the next kAhead rows of the lane is under way: a load
-  // takes longer than a row's arithmetic, and with one wave a SIMD nothing
-  // else hides it.
-  constexpr int kAhead = 4;
-  const int64_t m1 = m0 + FM * 16 < g.M ? m0 + FM * 16 : g.M;
-  int64_t mr = m0 + lane / kLanes;  // the row whose residual is loaded next
-  Residual<DT, 8> ahead[kAhead];
-  auto fetch = [&](Residual<DT, 8>& r) {
-    r.load(g, mr < m1 ? mr : 0, c, mr < m1 && !g.partial ? n : 0);
-    mr += kRows;
-  };
+  const bool full = m0 + FM * 16 <= g.M && n0 + FN * 16 <= g.N;
+  auto put = [&](int i) {
 #pragma unroll
-  for (int q = 0; q < kAhead; ++q) fetch(ahead[q]);
-#pragma unroll
-  for (int i = 0; i < FM; i += kPass) {
-#pragma unroll
-    for (int h = 0; h < kPass; ++h)
+    for (int h = 0; h < PASS; ++h)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
-        *(__attribute__((address_space(3))) f32x4*)(mem + (h * 16 + (lane & 15)) * kRow + j * 64 +
-                                                    (lane >> 4) * 16) = acc[i + h][j];
-#pragma unroll 1
-    for (int r = lane / kLanes; r < kPass * 16; r += kRows) {
-      const int64_t m = m0 + i * 16 + r;
-      const __attribute__((address_space(3))) f32x4* const p =
-          (const __attribute__((address_space(3))) f32x4*)(mem + r * kRow + (lane % kLanes) * 32);
-      const f32x4 lo = p[0], hi = p[1];
-      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      if (g.partial) {
-        if (m < g.M && n > 0)
-          store_pack<kFP32, 8>(g.partial + ((int64_t)blockIdx.y * g.M + m) * g.N + c,
-                               pack<kFP32, 8>(v), n);
-        continue;
-      }
+        *(lds_f4*)(mem + (h * 16 + (lane & 15)) * kRow + j * 64 + (lane >> 4) * 16) =
+            acc[i + h][j];
+  };
+  auto get = [&](int r, float* v) {
+    const lds_f4* const p = (const lds_f4*)(mem + r * kRow + (lane % kLanes) * 32);
+    const f32x4 lo = p[0], hi = p[1];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] += bias[q];
+    for (int q = 0; q < 4; ++q) {
+      v[q] = lo[q];
+      v[4 + q] = hi[q];
+    }
+  };
+  if (g.partial) {
+    float* const out = g.partial + (int64_t)blockIdx.y * g.M * g.N + c;
+#pragma unroll
+    for (int i = 0; i < FM; i += PASS) {
+      put(i);
+#pragma unroll 2
+      for (int r = lane / kLanes; r < kPassRows; r += kRows) {
+        const int64_t m = m0 + i * 16 + r;
+        float v[8];
+        get(r, v);
+        if (m < g.M && n > 0) store_pack<kFP32, 8>(out + m * g.N, pack<kFP32, 8>(v), n);
+      }
+    }
+    return;
+  }
+  const float limit = save_limit(DT);
+  float bias[8];
+  load_bias<8>(g, c, n, bias);
+  const bool fetches = g.residual && g.out_dt != kFP32;
+  int64_t mr = m0 + lane / kLanes;  // the row whose residual is loaded next
+  const int64_t m1 = m0 + FM * 16 < g.M ? m0 + FM * 16 : g.M;
+  Pack<DT, 8> ahead[U];
+  auto fetch = [&] {
+    if (!fetches) return;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (mr < m1) ahead[u] = load_pack<DT, 8>((const E*)g.residual + mr * g.ldr + c, n);
+      mr += kRows;
+    }
+  };
+  fetch();
+#pragma unroll
+  for (int i = 0; i < FM; i += PASS) {
+    put(i);
+#pragma unroll 1
+    for (int r = lane / kLanes; r < kPassRows; r += U * kRows) {
+      const int64_t m = m0 + i * 16 + r;
+      float v[U * 8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) get(r + u * kRows, v + u * 8);
+      Pack<DT, 8> res[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) res[u] = ahead[u];
+      fetch();
+#pragma unroll
+      for (int q = 0; q < U * 8; ++q) v[q] += bias[q % 8];
       if constexpr (FN % 2 == 0) {
         if (g.codes) {  // a row's lanes are here together
-          Codes<8> q;
-          const int s = encode<8>(v, n, limit, q);
-          if (m < g.M && n > 0) {
-            store_codes<8>(g.codes + m * g.N + c, q, n);
-            if (c % kBlock == 0)
-              g.scales[m * ((g.N + kBlock - 1) / kBlock) + c / kBlock] = (uint8_t)s;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int64_t mu = m + u * kRows;
+            float o[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = v[u * 8 + q];
+            Codes<8> q;
+            const int s = encode<8>(o, n, limit, q);
+            if (mu < g.M && n > 0) {
+              store_codes<8>(g.codes + mu * g.N + c, q, n);
+              if (c % kBlock == 0)
+                g.scales[mu * ((g.N + kBlock - 1) / kBlock) + c / kBlock] = (uint8_t)s;
+            }
           }
         }
       }
-      const Residual<DT, 8> res = ahead[0];
-#pragma unroll
-      for (int q = 0; q + 1 < kAhead; ++q) ahead[q] = ahead[q + 1];
-      fetch(ahead[kAhead - 1]);
-      if (m < g.M && n > 0) finish<DT, 8>(g, m, c, n, v, res);
+      if (full)
+        finish<DT, 8, U, true>(g, m, kRows, c, 8, v, res);
+      else
+        finish<DT, 8, U, false>(g, m, kRows, c, n, v, res);
     }
   }
 }
@@ -480,10 +532,11 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
     }
   }
 
-  static_assert(NW * kStoreBytes<FM, FN> <= STAGES * kStage, "the epilogue's LDS");
+  constexpr int kPass = FM > 1 ? 2 : 1;
+  static_assert(NW * kStoreBytes<FN, kPass> <= STAGES * kStage, "the epilogue's LDS");
   __syncthreads();
-  store_tile<DT, FM, FN>(g, acc, lds + wave * kStoreBytes<FM, FN>, m0 + wm * (BM / WM),
-                         n0 + wn * (BN / WN), lane);
+  store_tile<DT, FM, FN, kPass>(g, acc, lds + wave * kStoreBytes<FN, kPass>, m0 + wm * (BM / WM),
+                                n0 + wn * (BN / WN), lane);
 }
 
 // The largest tile, 256 x 256: four waves, one for each SIMD, with 128 x
@@ -495,12 +548,13 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
 // as a lone wave issues one instruction every 4 cycles and a product takes
 // 16.  A step of BK = 64 runs in two halves of 64 products from registers:
 //   first half    the fragments of this step's second half are read; when
-//                 they are there (slot 40) a barrier frees the stage, and
+//                 they are there (slot 34) a barrier frees the stage, and
 //                 the loads of the step after next begin to fill it
 //   (barrier: the next step has landed)
 //   second half   the fragments of the next step's first half are read, and
 //                 the loads go on
-// so a load has 1,400 to 2,400 cycles to land.  A row of 64 elements is a
+// so a load has 1,200 to 2,400 cycles to land.  Loads every 4 slots or fewer
+// wait for the vector memory pipe (8192^3: every 2, 844 us, 4, 792, 5, 782).  A row of 64 elements is a
 // whole 128-byte line; steps of 32 with a ring of four stages kept the
 // vector memory pipe busier than the products (8192^3, both operands with K
 // fastest: 922 us against 856).
@@ -513,7 +567,8 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
   constexpr int kStage = TA::kBytes + TB::kBytes;
   constexpr int kLoads = TA::kPerWave + TB::kPerWave;  // of a wave and step
   static_assert(kLoads == 16 && TA::kPerWave == 8, "the slots below");
-  __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
+  constexpr int kBytes = 2 * kStage > NW * kStoreBytes<FN, 4> ? 2 * kStage : NW * kStoreBytes<FN, 4>;
+  __shared__ __attribute__((aligned(1024))) char smem[kBytes];
   lds_char* const lds = (lds_char*)smem;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
@@ -593,7 +648,8 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     };
-    constexpr int kFree = 40, kFirst = 6;  // slot of the first barrier, loads before the second
+    // slot of the first barrier, slots between loads, loads before the second
+    constexpr int kFree = 34, kEvery = 5, kFirst = (63 - kFree - 2) / kEvery + 1;
     F a0[FM], b0[FN], a1[FM], b1[FN];
     uint32_t at = 0;  // this step's stage
     auto first_half = [&] {
@@ -605,7 +661,8 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
           barrier();
         }
-        if (s > kFree && s % 4 == 2) issue((s - kFree - 2) / 4, lds0 + at);
+        if (s >= kFree + 2 && (s - kFree - 2) % kEvery == 0)
+          issue((s - kFree - 2) / kEvery, lds0 + at);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -614,7 +671,8 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
       for (int s = 0; s < 64; ++s) {
         acc[s / 8][s % 8] = Mfma<DT>::run(b1[s % 8], a1[s / 8], acc[s / 8][s % 8]);
         if (s % 2 == 0 && s < 32) read(a0, b0, s / 2, 0, lds + (at ^ kStage));
-        if (s % 4 == 1 && s / 4 < kLoads - kFirst) issue(kFirst + s / 4, lds0 + at);
+        if (s % kEvery == 1 && s / kEvery < kLoads - kFirst)
+          issue(kFirst + s / kEvery, lds0 + at);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -639,8 +697,8 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
     wait_loads<0>();
   }
   __syncthreads();
-  store_tile<DT, FM, FN>(g, acc, lds + wave * kStoreBytes<FM, FN>, m0 + wm * 128, n0 + wn * 128,
-                         lane);
+  store_tile<DT, FM, FN, 4>(g, acc, lds + wave * kStoreBytes<FN, 4>, m0 + wm * 128,
+                            n0 + wn * 128, lane);
 }
 
 // The runs' sums added in run order, then the epilogue: four columns a
@@ -676,11 +734,10 @@ __global__ __launch_bounds__(256) void linear_finish_kernel(LinearArgs g) {
       if (n > 0) store_codes<4>(g.codes + m * g.N + c, q, n);
       if (c % kBlock == 0) g.scales[m * (quads / 8) + c / kBlock] = (uint8_t)s;
     }
-    if (n > 0) {
-      Residual<DT, 4> res;
-      res.load(g, m, c, n);
-      finish<DT, 4>(g, m, c, n, v, res);
-    }
+    Pack<DT, 4> res[1];
+    if (n > 0 && g.residual && g.out_dt != kFP32)
+      res[0] = load_pack<DT, 4>((const elem_t<DT>*)g.residual + m * g.ldr + c, n);
+    finish<DT, 4, 1, false>(g, m, 0, c, n, v, res);
   }
 }
 
