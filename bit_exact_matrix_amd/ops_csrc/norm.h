@@ -10,10 +10,11 @@
 //
 // What bounds both is memory: each element is read once and written once,
 // and a row stays in registers between its sums and its output.  A row is
-// held by GT lanes, NV vectors of 16 bytes each; a workgroup of GT * G
-// lanes works on G rows at a time and walks the matrix, so weight and bias
-// are loaded once and the weight gradient's sums stay in registers until
-// the workgroup's last row.  Each workgroup then writes one row of partial
+// held by GT lanes, NV vectors of 16 bytes each (one, as long as 1024 lanes
+// are enough: two cost the backward pass its registers, 134 us against 46
+// at 8192 x 4096 bf16); a workgroup of GT * G lanes works on G rows at a
+// time and walks the matrix, so weight and bias are loaded once and the
+// weight gradient's sums stay in registers until the workgroup's last row.  Each workgroup then writes one row of partial
 // sums, and a second kernel adds those in workgroup order: the result does
 // not depend on which workgroup ran first.
 #ifndef MMAOPS_NORM_H
@@ -106,19 +107,31 @@ __global__ __launch_bounds__(GT* G) void norm_kernel(NormArgs a) {
   load_param<PDT, V, NV, GT>(a.bias, lane, a.cols, 0.0f, b);
   const float n_f = (float)a.cols;
   const float limit = save_limit(DT);
-  for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < a.rows; r0 += (int64_t)gridDim.x * G) {
+  const int64_t step = (int64_t)gridDim.x * G;
+  // the next rows' loads are in flight while this row's sums meet
+  Pack<DT, V> raw[NV];
+  auto fetch = [&](int64_t row) {
+    const E* const x = (const E*)a.x + (row < a.rows ? row : 0) * a.ldx;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * GT + lane) * V;
+      raw[j] = load_pack<DT, V>(x + c, row < a.rows ? a.cols - c : 0);
+    }
+  };
+  int64_t r0 = (int64_t)blockIdx.x * G;
+  fetch(r0 + g);
+  for (; r0 < a.rows; r0 += step) {
     const int64_t row = r0 + g;
     const bool live = row < a.rows;
-    const E* const x = (const E*)a.x + (live ? row : 0) * a.ldx;
     float v[NV][V];
     float s[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * GT + lane) * V;
-      unpack(load_pack<DT, V>(x + c, live ? a.cols - c : 0), v[j]);
+      unpack(raw[j], v[j]);
 #pragma unroll
       for (int i = 0; i < V; ++i) s[0] += v[j][i];
     }
+    if (r0 + step < a.rows) fetch(row + step);
     if constexpr (SAVE) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {

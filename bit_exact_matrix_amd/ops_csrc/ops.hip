@@ -95,28 +95,21 @@ struct NormPlan {
   int gt, nv;  // gt = 0: the row is too long for registers
 };
 
-// Forward.  A row takes one wave while it fits 2 vectors a lane, then as
-// many waves as that needs; with few rows (a decoding step) one vector a
-// lane and more waves, as latency counts then.
-NormPlan norm_plan(int64_t rows, int64_t cols, int V) {
+// One vector a lane and as many waves as the row needs, up to 1024 lanes;
+// then two.
+NormPlan norm_plan(int64_t cols, int V) {
   const int64_t vecs = (cols + V - 1) / V;
-  if (vecs <= 64) return {64, 1};
-  if (rows <= kCUs) {
-    if (vecs <= 256) return {256, 1};
-    if (vecs <= 512) return {512, 1};
-    if (vecs <= 1024) return {1024, 1};
-  }
-  if (vecs <= 128) return {64, 2};
-  if (vecs <= 256) return {256, 1};
-  if (vecs <= 512) return {256, 2};
-  if (vecs <= 1024) return {512, 2};
+  int gt = 64;
+  while (gt < 1024 && gt < vecs) gt *= 2;
+  if (vecs <= gt) return {gt, 1};
   if (vecs <= 2048) return {1024, 2};
-  if (vecs <= 4096) return {1024, 4};
   return {0, 0};
 }
 
-template <int DT, int PDT, int GT, int NV, int G>
+// Workgroups of 256 lanes or a row's, as many as the CUs hold at once.
+template <int DT, int PDT, int GT, int NV>
 void norm_run(const NormArgs& a, hipStream_t s) {
+  constexpr int G = GT < 256 ? 256 / GT : 1;
   const int64_t groups = (a.rows + G - 1) / G;
   constexpr int kPerCU = 2048 / (GT * G);
   const uint32_t grid = (uint32_t)(groups < kCUs * kPerCU ? groups : kCUs * kPerCU);
@@ -128,17 +121,14 @@ void norm_run(const NormArgs& a, hipStream_t s) {
 
 template <int DT, int PDT>
 hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
-  const NormPlan p = norm_plan(a.rows, a.cols, kVec<DT>);
-  switch (p.gt * 8 + p.nv) {
-    case 64 * 8 + 1: norm_run<DT, PDT, 64, 1, 4>(a, s); break;
-    case 64 * 8 + 2: norm_run<DT, PDT, 64, 2, 4>(a, s); break;
-    case 256 * 8 + 1: norm_run<DT, PDT, 256, 1, 1>(a, s); break;
-    case 256 * 8 + 2: norm_run<DT, PDT, 256, 2, 1>(a, s); break;
-    case 512 * 8 + 1: norm_run<DT, PDT, 512, 1, 1>(a, s); break;
-    case 512 * 8 + 2: norm_run<DT, PDT, 512, 2, 1>(a, s); break;
-    case 1024 * 8 + 1: norm_run<DT, PDT, 1024, 1, 1>(a, s); break;
-    case 1024 * 8 + 2: norm_run<DT, PDT, 1024, 2, 1>(a, s); break;
-    case 1024 * 8 + 4: norm_run<DT, PDT, 1024, 4, 1>(a, s); break;
+  const NormPlan p = norm_plan(a.cols, kVec<DT>);
+  switch (p.gt * p.nv) {
+    case 64: norm_run<DT, PDT, 64, 1>(a, s); break;
+    case 128: norm_run<DT, PDT, 128, 1>(a, s); break;
+    case 256: norm_run<DT, PDT, 256, 1>(a, s); break;
+    case 512: norm_run<DT, PDT, 512, 1>(a, s); break;
+    case 1024: norm_run<DT, PDT, 1024, 1>(a, s); break;
+    case 2048: norm_run<DT, PDT, 1024, 2>(a, s); break;
     default: {
       const uint32_t grid = (uint32_t)(a.rows < 2 * kCUs ? a.rows : 2 * kCUs);
       if (a.codes_out)
@@ -151,21 +141,11 @@ hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
 }
 
 // Backward: workgroups of 1024 lanes, one for each CU at most, so that the
-// partial sums stay at one row for each CU.
-NormPlan norm_backward_plan(int64_t cols, int V) {
-  const int64_t vecs = (cols + V - 1) / V;
-  if (vecs <= 64) return {64, 1};
-  if (vecs <= 128) return {64, 2};
-  if (vecs <= 256) return {256, 1};
-  if (vecs <= 512) return {256, 2};
-  if (vecs <= 1024) return {512, 2};
-  if (vecs <= 2048) return {1024, 2};
-  return {0, 0};
-}
-
+// partial sums stay at one row for each CU; rows of more than 1024 vectors
+// go to the kernels that read them in several passes.
 int norm_backward_groups(int64_t rows, int64_t cols, int V) {
-  const NormPlan p = norm_backward_plan(cols, V);
-  if (!p.gt) {  // runs of rows of the column pass
+  const NormPlan p = norm_plan(cols, V);
+  if (p.gt * p.nv == 0 || p.nv > 1) {  // runs of rows of the column pass
     const int64_t runs = (rows + 31) / 32;
     return (int)(runs < kCUs ? runs : kCUs);
   }
@@ -173,12 +153,12 @@ int norm_backward_groups(int64_t rows, int64_t cols, int V) {
   return (int)(groups < kCUs ? groups : kCUs);
 }
 
-template <int DT, int PDT, int GT, int NV>
+template <int DT, int PDT, int GT>
 void norm_backward_run(const NormArgs& a, int grid, hipStream_t s) {
   if (a.codes)
-    norm_backward_kernel<DT, PDT, GT, NV, 1024 / GT, true><<<grid, 1024, 0, s>>>(a);
+    norm_backward_kernel<DT, PDT, GT, 1, 1024 / GT, true><<<grid, 1024, 0, s>>>(a);
   else
-    norm_backward_kernel<DT, PDT, GT, NV, 1024 / GT, false><<<grid, 1024, 0, s>>>(a);
+    norm_backward_kernel<DT, PDT, GT, 1, 1024 / GT, false><<<grid, 1024, 0, s>>>(a);
 }
 
 template <int DT, bool SAVED>
@@ -197,14 +177,13 @@ hipError_t norm_backward_long(const NormArgs& a, int pdt, int groups, hipStream_
 
 template <int DT, int PDT>
 hipError_t norm_backward_launch(const NormArgs& a, int groups, hipStream_t s) {
-  const NormPlan p = norm_backward_plan(a.cols, kVec<DT>);
-  switch (p.gt * 8 + p.nv) {
-    case 64 * 8 + 1: norm_backward_run<DT, PDT, 64, 1>(a, groups, s); break;
-    case 64 * 8 + 2: norm_backward_run<DT, PDT, 64, 2>(a, groups, s); break;
-    case 256 * 8 + 1: norm_backward_run<DT, PDT, 256, 1>(a, groups, s); break;
-    case 256 * 8 + 2: norm_backward_run<DT, PDT, 256, 2>(a, groups, s); break;
-    case 512 * 8 + 2: norm_backward_run<DT, PDT, 512, 2>(a, groups, s); break;
-    case 1024 * 8 + 2: norm_backward_run<DT, PDT, 1024, 2>(a, groups, s); break;
+  const NormPlan p = norm_plan(a.cols, kVec<DT>);
+  switch (p.gt * p.nv) {
+    case 64: norm_backward_run<DT, PDT, 64>(a, groups, s); break;
+    case 128: norm_backward_run<DT, PDT, 128>(a, groups, s); break;
+    case 256: norm_backward_run<DT, PDT, 256>(a, groups, s); break;
+    case 512: norm_backward_run<DT, PDT, 512>(a, groups, s); break;
+    case 1024: norm_backward_run<DT, PDT, 1024>(a, groups, s); break;
     default:
       return a.codes ? norm_backward_long<DT, true>(a, PDT, groups, s)
                      : norm_backward_long<DT, false>(a, PDT, groups, s);

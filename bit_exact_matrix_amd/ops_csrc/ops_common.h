@@ -107,12 +107,36 @@ __device__ __forceinline__ Pack<DT, V> pack(const float (&v)[V]) {
 }
 
 // ---------------------------------------------------------- reductions
-// Sum over the 64 lanes of a wave, the same in every lane.  The pairs are
-// the same in every lane (each step adds two values that both lanes hold),
-// so the result does not depend on the lane.
+// Lane exchanges without LDS: the value of another lane of the 16-lane row
+// (CTRL: quad_perm, row_ror or row_half_mirror).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kRor4 = 0x124, kRor8 = 0x128;
+
+// Sum over the 64 lanes of a wave, the same bits in every lane: each step
+// adds two values that both lanes of a pair hold.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  v += dpp<kXor1>(v);
+  v += dpp<kXor2>(v);
+  v += dpp<kRor8>(v);  // a quad's lanes are equal: quads k and k + 2, then all
+  v += dpp<kRor4>(v);
+  // rows 0 and 1, 2 and 3; then the halves
+  auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+// Maximum over 4 or 8 neighbouring lanes.
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+  static_assert(LANES == 4 || LANES == 8, "");
+  v = __builtin_fmaxf(v, dpp<kXor1>(v));
+  v = __builtin_fmaxf(v, dpp<kXor2>(v));
+  if constexpr (LANES == 8) v = __builtin_fmaxf(v, dpp<kHalfMirror>(v));
   return v;
 }
 
@@ -329,8 +353,7 @@ __device__ __forceinline__ int encode(const float (&v)[V], int n, float limit, C
 #pragma unroll
   for (int i = 0; i < V; ++i)
     if (i < n) amax = __builtin_fmaxf(amax, save_mag(v[i], limit));
-#pragma unroll
-  for (int m = 1; m < kBlock / V; m <<= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, m));
+  amax = lanes_max<kBlock / V>(amax);
   const int s = save_scale(amax);
   const float down = scale_down(s);
 #pragma unroll
