@@ -199,6 +199,17 @@ struct Raw<DT, true, V> {
   __device__ __forceinline__ void values(float (&v)[V]) const { decode<V>(q, s, v); }
 };
 
+// What the compiler knows of a value's registers ends here.
+template <typename T>
+__device__ __forceinline__ void hide(T& v) {
+  static_assert(sizeof(T) % 4 == 0, "whole registers");
+  uint32_t u[sizeof(T) / 4];
+  __builtin_memcpy(u, &v, sizeof(T));
+#pragma unroll
+  for (uint32_t& x : u) asm volatile("" : "+v"(x));
+  __builtin_memcpy(&v, u, sizeof(T));
+}
+
 // dx of every row, and the workgroup's partial sums of dw and db.
 template <int DT, int PDT, int GT, int NV, int G, bool SAVED>
 __global__ __launch_bounds__(GT* G) void norm_backward_kernel(NormArgs a) {
@@ -216,48 +227,54 @@ __global__ __launch_bounds__(GT* G) void norm_backward_kernel(NormArgs a) {
   const float n_f = (float)a.cols;
   const int64_t step = (int64_t)gridDim.x * G;
 
-  // the next rows' loads are in flight while this row's sums meet
-  Raw<DT, SAVED, V> xr[NV];
-  Pack<DT, V> dr[NV];
-  float mu = 0.0f, r = 0.0f;
-  auto fetch = [&](int64_t row) {
+  // Three rows' loads: the one that is worked on and two on their way (a CU
+  // needs some 30 KB under way to draw its share of memory's rate; a
+  // workgroup of 1024 lanes has 32 bytes of each lane's row).  To leave
+  // registers for them, xh and h are made again from the loaded row after
+  // its sums have met, not kept.
+  constexpr int kAhead = 2;
+  Raw<DT, SAVED, V> xr[kAhead][NV];
+  Pack<DT, V> dr[kAhead][NV];
+  float mu[kAhead], rs[kAhead];
+  auto fetch = [&](int q, int64_t row) {
     const bool live = row < a.rows;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * GT + lane) * V;
       const int n = live ? a.cols - c : 0;
-      xr[j].load(a, live ? row : 0, c, n);
-      dr[j] = load_pack<DT, V>((const E*)a.dy + (live ? row : 0) * a.lddy + c, n);
+      xr[q][j].load(a, live ? row : 0, c, n);
+      dr[q][j] = load_pack<DT, V>((const E*)a.dy + (live ? row : 0) * a.lddy + c, n);
     }
-    mu = live ? a.mean[row] : 0.0f;
-    r = live ? a.rstd[row] : 0.0f;
+    mu[q] = live ? a.mean[row] : 0.0f;
+    rs[q] = live ? a.rstd[row] : 0.0f;
   };
-  int64_t r0 = (int64_t)blockIdx.x * G;
-  fetch(r0 + g);
-  for (; r0 < a.rows; r0 += step) {
-    const int64_t row = r0 + g;
-    float xh[NV][V], h[NV][V];
+  auto work = [&](int q, int64_t row) {
     float s[2] = {0.0f, 0.0f};
-    const float rr = r, m = mu;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
+    const float r = rs[q], m = mu[q];
+    // xh, dy and h of vector j; a lane past the row's end has dy = 0, which
+    // the sums take as it is, and xh must be 0, not -mu r (maybe NaN)
+    auto values = [&](int j, float (&xh)[V], float (&d)[V], float (&h)[V]) {
       const int n = a.cols - (j * GT + lane) * V;
-      float x[V], d[V];
-      xr[j].values(x);
-      unpack(dr[j], d);
+      xr[q][j].values(xh);
+      unpack(dr[q][j], d);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        // a lane past the row's end holds dy = 0, which its sums take as
-        // it is; its xh must be 0, not -mu r (which may be NaN)
-        xh[j][i] = i < n ? (x[i] - m) * rr : 0.0f;
-        h[j][i] = d[i] * w[j][i];
-        s[0] += h[j][i];
-        s[1] += h[j][i] * xh[j][i];
-        dw[j][i] += d[i] * xh[j][i];
+        xh[i] = i < n ? (xh[i] - m) * r : 0.0f;
+        h[i] = d[i] * w[j][i];
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float xh[V], d[V], h[V];
+      values(j, xh, d, h);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        s[0] += h[i];
+        s[1] += h[i] * xh[i];
+        dw[j][i] += d[i] * xh[i];
         db[j][i] += d[i];
       }
     }
-    if (r0 + step < a.rows) fetch(row + step);
     row_sum<GT, 2>(s, lds, turn);
     if (row < a.rows && a.y) {
       const float m0 = s[0] / n_f, m1 = s[1] / n_f;
@@ -265,11 +282,27 @@ __global__ __launch_bounds__(GT* G) void norm_backward_kernel(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (j * GT + lane) * V;
-        float o[V];
+        float xh[V], d[V], h[V], o[V];
+        hide(xr[q][j]);
+        hide(dr[q][j]);
+        values(j, xh, d, h);
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = rr * (h[j][i] - m0 - xh[j][i] * m1);
+        for (int i = 0; i < V; ++i) o[i] = r * (h[i] - m0 - xh[i] * m1);
         store_pack<DT, V>(dx + c, pack<DT, V>(o), a.cols - c);
       }
+    }
+    fetch(q, row + kAhead * step);
+  };
+  int64_t row = (int64_t)blockIdx.x * G + g;
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q) fetch(q, row + q * step);
+  // every group of the workgroup takes as many turns (rows past the end
+  // are empty), for the barriers
+  for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < a.rows; r0 += kAhead * step) {
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      work(q, row);
+      row += step;
     }
   }
   if (!a.partial) return;

@@ -56,18 +56,21 @@ __device__ __forceinline__ void store_any(void* p, int64_t i, float v, int dt) {
     ((__bf16*)p)[i] = (__bf16)v;
 }
 
-// V consecutive elements, in registers as they are in memory.  Global loads
-// and stores of 16 bytes need no more than the element's alignment on
-// gfx950, so rows of odd lengths and strides take the same wide accesses.
+// V consecutive elements, in registers as they are in memory, word by word
+// (element by element the compiler would give each 16-bit one a register).
+// Global loads and stores of 16 bytes need no more than the element's
+// alignment on gfx950, so rows of odd lengths and strides take the same
+// wide accesses.
 template <int DT, int V>
 struct Pack {
-  elem_t<DT> e[V];
+  static constexpr int kWords = V * elem_bytes(DT) / 4;
+  uint32_t w[kWords];
 };
 
 template <int DT, int V>
 __device__ __forceinline__ Pack<DT, V> load_pack(const elem_t<DT>* p) {
   Pack<DT, V> q;
-  __builtin_memcpy(&q, p, sizeof q);
+  __builtin_memcpy(q.w, p, sizeof q.w);
   return q;
 }
 
@@ -77,32 +80,71 @@ __device__ __forceinline__ Pack<DT, V> load_pack(const elem_t<DT>* p, int n) {
   if (n >= V) return load_pack<DT, V>(p);
   Pack<DT, V> q;
 #pragma unroll
-  for (int i = 0; i < V; ++i) q.e[i] = i < n ? p[i] : (elem_t<DT>)0.0f;
+  for (int i = 0; i < Pack<DT, V>::kWords; ++i) q.w[i] = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (i >= n) continue;
+    if constexpr (DT == kFP32)
+      q.w[i] = ((const uint32_t*)p)[i];
+    else
+      q.w[i / 2] |= (uint32_t)((const uint16_t*)p)[i] << (16 * (i & 1));
+  }
   return q;
 }
 
 template <int DT, int V>
 __device__ __forceinline__ void store_pack(elem_t<DT>* p, const Pack<DT, V>& q, int n) {
   if (n >= V) {
-    __builtin_memcpy(p, &q, sizeof q);
+    __builtin_memcpy(p, q.w, sizeof q.w);
     return;
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (i < n) p[i] = q.e[i];
+  for (int i = 0; i < V; ++i) {
+    if (i >= n) continue;
+    if constexpr (DT == kFP32)
+      ((uint32_t*)p)[i] = q.w[i];
+    else
+      ((uint16_t*)p)[i] = (uint16_t)(q.w[i / 2] >> (16 * (i & 1)));
+  }
 }
 
 template <int DT, int V>
 __device__ __forceinline__ void unpack(const Pack<DT, V>& q, float (&v)[V]) {
+  if constexpr (DT == kFP32) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = (float)q.e[i];
+    for (int i = 0; i < V; ++i) v[i] = __uint_as_float(q.w[i]);
+  } else if constexpr (DT == kBF16) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      v[i] = __uint_as_float(q.w[i / 2] << 16);
+      v[i + 1] = __uint_as_float(q.w[i / 2] & 0xFFFF0000u);
+    }
+  } else {
+    using h2 = __attribute__((ext_vector_type(2))) _Float16;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const h2 h = __builtin_bit_cast(h2, q.w[i / 2]);
+      v[i] = (float)h[0];
+      v[i + 1] = (float)h[1];
+    }
+  }
 }
 
 template <int DT, int V>
 __device__ __forceinline__ Pack<DT, V> pack(const float (&v)[V]) {
   Pack<DT, V> q;
+  if constexpr (DT == kFP32) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) q.e[i] = (elem_t<DT>)v[i];
+    for (int i = 0; i < V; ++i) q.w[i] = __float_as_uint(v[i]);
+  } else {
+    using f2 = __attribute__((ext_vector_type(2))) float;
+    using e2 = __attribute__((ext_vector_type(2))) elem_t<DT>;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const e2 h = __builtin_convertvector((f2){v[i], v[i + 1]}, e2);
+      q.w[i / 2] = __builtin_bit_cast(uint32_t, h);
+    }
+  }
   return q;
 }
 
