@@ -42,6 +42,9 @@ struct LinearArgs {
   // partial[split][M][N] and linear_finish_kernel does the rest
   int splits;
   int tiles_m, tiles_n;
+  // the last whole step goes through registers too: its last row's last
+  // chunk would pass the end of an operand
+  int guard;
   float* partial;
   // epilogue
   const void* bias;
@@ -124,8 +127,8 @@ struct Tile {
   }
 
   // byte offsets of the lane's chunks from the tile's first element; rows
-  // past the matrix (`have` rows are there) repeat the last one: what they
-  // give is never stored
+  // past the matrix (`have` rows are there) repeat the last one, and a
+  // chunk may pass the row's end: what they give is never stored
   static __device__ __forceinline__ void offsets(int64_t ld, int have, int wave, int lane,
                                                  uint32_t (&off)[kPerWave]) {
 #pragma unroll
@@ -135,7 +138,7 @@ struct Tile {
       if constexpr (LAYOUT == 0)
         row = row < have ? row : have - 1;
       else
-        chunk = chunk * 8 < have ? chunk : have / 8 - 1;
+        chunk = chunk * 8 < have ? chunk : (have - 1) / 8;
       off[i] = (uint32_t)(row * ld * 2) + chunk * 16;
     }
   }
@@ -332,7 +335,6 @@ __device__ __forceinline__ void store_tile(const LinearArgs& g, const f32x4 (&ac
     }
     return;
   }
-  const float limit = save_limit(DT);
   float bias[8];
   load_bias<8>(g, c, n, bias);
   const bool fetches = g.residual && g.out_dt != kFP32;
@@ -372,7 +374,7 @@ __device__ __forceinline__ void store_tile(const LinearArgs& g, const f32x4 (&ac
 #pragma unroll
             for (int q = 0; q < 8; ++q) o[q] = v[u * 8 + q];
             Codes<8> q;
-            const int s = encode<8>(o, n, limit, q);
+            const int s = encode<DT, 8>(o, n, q);
             if (mu < g.M && n > 0) {
               store_codes<8>(g.codes + mu * g.N + c, q, n);
               if (c % kBlock == 0)
@@ -461,7 +463,7 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
     }
   };
 
-  const int tail = (int)(g.K % BK);
+  const int tail = g.K % BK ? (int)(g.K % BK) : g.guard ? BK : 0;
   if (s0 < s1) {
     u32x4 va[TA::kPerWave], vb[TB::kPerWave];
     if (s1 == steps && tail) {  // the part of a step, before the others
@@ -597,7 +599,7 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
   const uint32_t base_a = TA::base(wm * 128, lane);
   const uint32_t base_b = TB::base(wn * 128, lane) + TA::kBytes;
 
-  const int tail = (int)(g.K % BK);
+  const int tail = g.K % BK ? (int)(g.K % BK) : g.guard ? BK : 0;
   if (s0 < s1 && s1 == steps && tail) {  // the part of a step, before the others
     s1 -= 1;
     u32x4 v[TA::kPerWave];
@@ -707,7 +709,6 @@ template <int DT>
 __global__ __launch_bounds__(256) void linear_finish_kernel(LinearArgs g) {
   const int64_t quads = (g.N + kBlock - 1) / kBlock * (kBlock / 4);  // of a row
   const int64_t total = quads * g.M;
-  const float limit = save_limit(DT);
   for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total;
        t += (int64_t)gridDim.x * 256) {
     const int64_t m = t / quads, c = (t - m * quads) * 4;
@@ -730,7 +731,8 @@ __global__ __launch_bounds__(256) void linear_finish_kernel(LinearArgs g) {
     }
     if (g.codes) {  // the eight lanes of a block are in the loop together
       Codes<4> q;
-      const int s = encode<4>(v, n, limit, q);
+      float o[4] = {v[0], v[1], v[2], v[3]};
+      const int s = encode<DT, 4>(o, n, q);
       if (n > 0) store_codes<4>(g.codes + m * g.N + c, q, n);
       if (c % kBlock == 0) g.scales[m * (quads / 8) + c / kBlock] = (uint8_t)s;
     }
@@ -754,31 +756,21 @@ constexpr TileShape kTileShape[kTiles] = {
 template <int DT, int LA, int LB>
 hipError_t linear_launch_tile(int tile, bool direct, const LinearArgs& g, hipStream_t s) {
   const dim3 grid((uint32_t)(g.tiles_m * g.tiles_n), (uint32_t)g.splits);
-  if (direct) {
-    switch (tile) {
-      case kTileBig:
-        linear_wide_kernel<DT, LA, LB><<<grid, 256, 0, s>>>(g);
-        break;
-      case kTileMid:
-        linear_kernel<DT, 128, 128, 64, 2, 2, LA, LB, 2, true, 2><<<grid, 256, 0, s>>>(g);
-        break;
-      case kTileSmall:
-        linear_kernel<DT, 64, 64, 64, 2, 2, LA, LB, 3, true, 2><<<grid, 256, 0, s>>>(g);
-        break;
-      default:
+  switch (tile) {
+    case kTileBig:
+      linear_wide_kernel<DT, LA, LB><<<grid, 256, 0, s>>>(g);
+      break;
+    case kTileMid:
+      linear_kernel<DT, 128, 128, 64, 2, 2, LA, LB, 2, true, 2><<<grid, 256, 0, s>>>(g);
+      break;
+    case kTileSmall:
+      linear_kernel<DT, 64, 64, 64, 2, 2, LA, LB, 3, true, 2><<<grid, 256, 0, s>>>(g);
+      break;
+    default:
+      if (direct)
         linear_kernel<DT, 16, 64, 128, 1, 4, LA, LB, 3, true, 2><<<grid, 256, 0, s>>>(g);
-    }
-  } else {
-    switch (tile) {
-      case kTileMid:
-        linear_kernel<DT, 128, 128, 64, 2, 2, LA, LB, 2, false, 2><<<grid, 256, 0, s>>>(g);
-        break;
-      case kTileSmall:
-        linear_kernel<DT, 64, 64, 64, 2, 2, LA, LB, 2, false, 2><<<grid, 256, 0, s>>>(g);
-        break;
-      default:
+      else
         linear_kernel<DT, 16, 64, 128, 1, 4, LA, LB, 2, false, 2><<<grid, 256, 0, s>>>(g);
-    }
   }
   return hipGetLastError();
 }

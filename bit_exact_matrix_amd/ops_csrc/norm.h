@@ -106,7 +106,6 @@ __global__ __launch_bounds__(GT* G) void norm_kernel(NormArgs a) {
   load_param<PDT, V, NV, GT>(a.weight, lane, a.cols, 1.0f, w);
   load_param<PDT, V, NV, GT>(a.bias, lane, a.cols, 0.0f, b);
   const float n_f = (float)a.cols;
-  const float limit = save_limit(DT);
   const int64_t step = (int64_t)gridDim.x * G;
   // the next rows' loads are in flight while this row's sums meet
   Pack<DT, V> raw[NV];
@@ -131,14 +130,13 @@ __global__ __launch_bounds__(GT* G) void norm_kernel(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < V; ++i) s[0] += v[j][i];
     }
-    if (r0 + step < a.rows) fetch(row + step);
     if constexpr (SAVE) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (j * GT + lane) * V;
         const int n = live ? a.cols - c : 0;
         Codes<V> q;
-        const int sc = encode<V>(v[j], n, limit, q);
+        const int sc = encode<DT, V>(raw[j], q);
         if (n > 0) {
           store_codes<V>(a.codes_out + row * a.cols + c, q, n);
           if (c % kBlock == 0)
@@ -146,6 +144,7 @@ __global__ __launch_bounds__(GT* G) void norm_kernel(NormArgs a) {
         }
       }
     }
+    if (r0 + step < a.rows) fetch(row + step);
     row_sum<GT, 1>(s, lds, turn);
     const float mu = s[0] / n_f;
     s[0] = 0.0f;
@@ -343,7 +342,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a, int pdt) {
   using E = elem_t<DT>;
   __shared__ float lds[2 * 16];
   int turn = 0;
-  const float n_f = (float)a.cols, limit = save_limit(DT);
+  const float n_f = (float)a.cols;
   // whole waves walk the row together, so that a block's lanes are all there
   const int end = (a.cols + 64 * V - 1) / (64 * V) * 64 * V;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -351,13 +350,14 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a, int pdt) {
     float s[1] = {0.0f};
     for (int c = threadIdx.x * V; c < end; c += GT * V) {
       const int n = a.cols - c;
+      const Pack<DT, V> raw = load_pack<DT, V>(x + c, n);
       float v[V];
-      unpack(load_pack<DT, V>(x + c, n), v);
+      unpack(raw, v);
 #pragma unroll
       for (int i = 0; i < V; ++i) s[0] += v[i];
       if constexpr (SAVE) {
         Codes<V> q;
-        const int sc = encode<V>(v, n, limit, q);
+        const int sc = encode<DT, V>(raw, q);
         if (n > 0) {
           store_codes<V>(a.codes_out + row * a.cols + c, q, n);
           if (c % kBlock == 0)
@@ -503,7 +503,7 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, 
   if (c < cols) {
     const float* p = partial + blockIdx.y * cols + c;
     const int64_t stride = (int64_t)gridDim.y * cols;
-#pragma unroll 4
+#pragma unroll 16
     for (int q = p0; q < p1; ++q) s += p[q * stride];
   }
   meet[wave][lane] = s;

@@ -256,9 +256,13 @@ struct Product {
   int64_t lda, ldb;
 };
 
+// direct: direct loads from both operands.  What they cannot be loaded from
+// directly is copied to aligned rows first (copy_a, copy_b), except for the
+// tile of few rows, where that would read the weight twice: there the
+// tile goes through registers.
 struct Plan {
   int tile, splits;
-  bool direct, partial;
+  bool direct, partial, copy_a, copy_b, guard;
 };
 
 // MMAOPS_LINEAR_TILE (0 to 3) and MMAOPS_LINEAR_SPLITS: diagnostic
@@ -274,24 +278,26 @@ int env_int(const char* name, int lo, int hi) {
 
 Plan linear_plan(const Product& p, bool saves) {
   Plan q;
-  // direct loads take 16-byte pieces: rows that start on 16 bytes, and for
-  // layout 1 a row length of whole pieces; 32-bit offsets within a tile
-  auto fits = [](const void* a, int64_t ld, int layout, int64_t len) {
-    return aligned(a, 16) && ld % 8 == 0 && ld <= (int64_t(1) << 22) &&
-           (layout == 0 || len % 8 == 0);
+  // direct loads take 16-byte pieces: rows that start on 16 bytes, and
+  // 32-bit offsets within a tile
+  auto fits = [](const void* a, int64_t ld) {
+    return aligned(a, 16) && ld % 8 == 0 && ld <= (int64_t(1) << 22);
   };
-  q.direct = fits(p.a, p.lda, p.la, p.M) && fits(p.b, p.ldb, p.lb, p.N);
+  const bool fa = fits(p.a, p.lda), fb = fits(p.b, p.ldb);
   auto tiles = [&](int t) {
     const TileShape& s = kTileShape[t];
     return ((p.M + s.bm - 1) / s.bm) * ((p.N + s.bn - 1) / s.bn);
   };
-  q.tile = p.M <= 32                              ? kTileFew
-           : q.direct && tiles(kTileBig) >= 192   ? kTileBig
-           : tiles(kTileMid) >= 128               ? kTileMid
-                                                  : kTileSmall;
+  q.tile = p.M <= 32                   ? kTileFew
+           : tiles(kTileBig) >= 192    ? kTileBig
+           : tiles(kTileMid) >= 128    ? kTileMid
+                                       : kTileSmall;
   const int env_tile = env_int("MMAOPS_LINEAR_TILE", 0, kTiles - 1);
   if (env_tile >= 0) q.tile = env_tile;
-  if (!q.direct && q.tile == kTileBig) q.tile = kTileMid;
+  q.copy_a = q.tile != kTileFew && !fa;
+  q.copy_b = q.tile != kTileFew && !fb;
+  q.direct = q.tile != kTileFew || (fa && fb);
+  q.guard = q.direct && ((p.la == 1 && p.M % 8) || (p.lb == 1 && p.N % 8));
   const TileShape& s = kTileShape[q.tile];
   const int64_t steps = (p.K + s.bk - 1) / s.bk, t = tiles(q.tile), n = t < 1 ? 1 : t;
   int64_t want = q.tile == kTileFew ? 512 : 256;
@@ -304,8 +310,34 @@ Plan linear_plan(const Product& p, bool saves) {
   return q;
 }
 
+// Rows and row length of an operand as it is stored.
+struct Stored {
+  int64_t rows, cols, ld;  // ld: of its aligned copy
+};
+Stored stored(int layout, int64_t len, int64_t K) {
+  const int64_t rows = layout == 0 ? len : K, cols = layout == 0 ? K : len;
+  return {rows, cols, (cols + 7) / 8 * 8};
+}
+
+// What a product takes of the workspace: the partial sums, then the copies.
 int64_t partial_bytes(const Product& p, const Plan& q) {
   return q.partial ? up256(p.M * p.N * q.splits * 4) : 0;
+}
+int64_t copy_bytes(bool copy, const Stored& t) { return copy ? up256(t.rows * t.ld * 2) : 0; }
+int64_t product_bytes(const Product& p, const Plan& q) {
+  return partial_bytes(p, q) + copy_bytes(q.copy_a, stored(p.la, p.M, p.K)) +
+         copy_bytes(q.copy_b, stored(p.lb, p.N, p.K));
+}
+
+// x (16-bit elements) to rows of t.ld elements at y
+hipError_t align_rows(const void* x, int64_t ldx, void* y, const Stored& t, hipStream_t s) {
+  if (t.rows == 0 || t.cols == 0) return hipSuccess;
+  int shift;
+  dim3 grid;
+  row_grid<kBF16>(t.rows, t.cols, &shift, &grid);
+  align_kernel<<<grid, 256, 0, s>>>((const uint16_t*)x, ldx, (uint16_t*)y, t.ld, t.rows, t.cols,
+                                    shift);
+  return hipGetLastError();
 }
 
 hipError_t linear_run(int dt, const Product& p, const Plan& q, LinearArgs g, void* ws,
@@ -315,10 +347,27 @@ hipError_t linear_run(int dt, const Product& p, const Plan& q, LinearArgs g, voi
   g.b = p.b;
   g.lda = p.lda;
   g.ldb = p.ldb;
+  char* at = (char*)ws + partial_bytes(p, q);
+  if (q.copy_a) {
+    const Stored t = stored(p.la, p.M, p.K);
+    const hipError_t e = align_rows(p.a, p.lda, at, t, s);
+    if (e != hipSuccess) return e;
+    g.a = at;
+    g.lda = t.ld;
+    at += copy_bytes(true, t);
+  }
+  if (q.copy_b) {
+    const Stored t = stored(p.lb, p.N, p.K);
+    const hipError_t e = align_rows(p.b, p.ldb, at, t, s);
+    if (e != hipSuccess) return e;
+    g.b = at;
+    g.ldb = t.ld;
+  }
   g.M = p.M;
   g.N = p.N;
   g.K = p.K;
   g.splits = q.splits;
+  g.guard = q.guard;
   g.tiles_m = (int)((p.M + t.bm - 1) / t.bm);
   g.tiles_n = (int)((p.N + t.bn - 1) / t.bn);
   g.partial = q.partial ? (float*)ws : nullptr;
@@ -342,7 +391,7 @@ Product forward_product(const mma_linear_args& r) {
 int64_t linear_need(const mma_linear_args& r) {
   if (r.M == 0 || r.N == 0) return 0;
   const Product p = forward_product(r);
-  return partial_bytes(p, linear_plan(p, r.codes != nullptr));
+  return product_bytes(p, linear_plan(p, r.codes != nullptr));
 }
 
 int check_linear(const mma_linear_args& r, int64_t ws_bytes, const void* ws, bool sizes_only) {
@@ -408,7 +457,7 @@ BackwardPlan backward_plan(const mma_linear_backward_args& r, void* ws) {
   }
   if (r.dbias) {
     const int64_t cols = (r.N + 511) / 512;
-    int64_t runs = (4 * kCUs + cols - 1) / cols;
+    int64_t runs = (8 * kCUs + cols - 1) / cols;
     if (runs > (r.M + 15) / 16) runs = (r.M + 15) / 16;
     b.db_run = (r.M + runs - 1) / runs;
     b.db_runs = (int)((r.M + b.db_run - 1) / b.db_run);
@@ -424,13 +473,13 @@ BackwardPlan backward_plan(const mma_linear_backward_args& r, void* ws) {
   if (r.dX) {
     b.dx = Product{r.M, r.K, r.N, 0, r.w_transposed ? 1 : 0, dz, r.W, lddz, r.ldw};
     b.pdx = linear_plan(b.dx, false);
-    part = partial_bytes(b.dx, b.pdx);
+    part = product_bytes(b.dx, b.pdx);
   }
   if (r.dW) {
     b.dw = r.w_transposed ? Product{r.N, r.K, r.M, 1, 1, dz, x, lddz, ldx}
                           : Product{r.K, r.N, r.M, 1, 1, x, dz, ldx, lddz};
     b.pdw = linear_plan(b.dw, false);
-    const int64_t w = partial_bytes(b.dw, b.pdw);
+    const int64_t w = product_bytes(b.dw, b.pdw);
     part = part > w ? part : w;
   }
   b.bytes = at + part;

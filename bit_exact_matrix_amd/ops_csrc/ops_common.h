@@ -174,11 +174,12 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // Maximum over 4 or 8 neighbouring lanes.
 template <int LANES>
-__device__ __forceinline__ float lanes_max(float v) {
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   static_assert(LANES == 4 || LANES == 8, "");
-  v = __builtin_fmaxf(v, dpp<kXor1>(v));
-  v = __builtin_fmaxf(v, dpp<kXor2>(v));
-  if constexpr (LANES == 8) v = __builtin_fmaxf(v, dpp<kHalfMirror>(v));
+  auto with = [&](uint32_t u) { v = u > v ? u : v; };
+  with(__float_as_uint(dpp<kXor1>(__uint_as_float(v))));
+  with(__float_as_uint(dpp<kXor2>(__uint_as_float(v))));
+  if constexpr (LANES == 8) with(__float_as_uint(dpp<kHalfMirror>(__uint_as_float(v))));
   return v;
 }
 
@@ -293,14 +294,8 @@ constexpr int kBlock = 32;
 // The largest magnitude that a checkpoint keeps, so that a code never
 // restores to an infinity of the element type: 1.875 times its largest
 // power of two (61440 for FP16).
-__device__ __forceinline__ float save_limit(int dt) {
-  return dt == kFP16 ? 61440.0f : __uint_as_float(0x7F700000u);
-}
-
-// |x| as it enters a block's maximum: 0 for NaN and infinities.
-__device__ __forceinline__ float save_mag(float x, float limit) {
-  const float m = __builtin_fabsf(x);
-  return m < __builtin_inff() ? __builtin_fminf(m, limit) : 0.0f;
+__device__ __forceinline__ constexpr uint32_t save_limit(int dt) {  // FP32 bits
+  return dt == kFP16 ? 0x47700000u : 0x7F700000u;
 }
 
 // The scale's exponent + 127 from the block's largest magnitude: the
@@ -308,8 +303,8 @@ __device__ __forceinline__ float save_mag(float x, float limit) {
 // the pattern carries into the exponent exactly when the fraction is above
 // .75.  e is at least -117, where 448 * 2^e still covers every smaller
 // block and 2^-9 * 2^e, the smallest value, is a normal BF16 number.
-__device__ __forceinline__ int save_scale(float amax) {
-  const int e = (int)((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 127 - 8;
+__device__ __forceinline__ int save_scale(uint32_t amax) {  // FP32 bits
+  const int e = (int)((amax + 0x1FFFFFu) >> 23) - 127 - 8;
   return (e < -117 ? -117 : e) + 127;
 }
 
@@ -317,15 +312,6 @@ __device__ __forceinline__ int save_scale(float amax) {
 __device__ __forceinline__ float scale_up(int s) { return __uint_as_float((uint32_t)s << 23); }
 __device__ __forceinline__ float scale_down(int s) {
   return __uint_as_float((uint32_t)(254 - s) << 23);
-}
-
-// x as it is handed to the E4M3 conversion: its limited magnitude times
-// 2^-e, or NaN where x is not finite (E4M3 has no infinity, and an
-// overflow must not come back as a number).
-__device__ __forceinline__ float save_scaled(float x, float limit, float down) {
-  const float m = __builtin_fabsf(x);
-  const float v = __builtin_copysignf(__builtin_fminf(m, limit) * down, x);
-  return m < __builtin_inff() ? v : __builtin_nanf("");
 }
 
 // Four E4M3 codes of four scaled values (|v| <= 448 or NaN).
@@ -387,23 +373,71 @@ __device__ __forceinline__ void decode(const Codes<V>& c, int scale, float (&v)[
 }
 
 // The codes of V consecutive elements held by each lane, where 32 / V
-// neighbouring lanes hold a block; elements past n do not count.  Returns
-// the block's scale, the same in its lanes.
-template <int V>
-__device__ __forceinline__ int encode(const float (&v)[V], int n, float limit, Codes<V>& c) {
-  float amax = 0.0f;
+// neighbouring lanes hold a block, from the lane's largest magnitude pattern
+// (FP32 bits of |v|).  Returns the block's scale, the same in its lanes.
+template <int DT, int V>
+__device__ __forceinline__ int encode_with(float (&v)[V], uint32_t mag, Codes<V>& c) {
+  constexpr uint32_t limit = save_limit(DT);
+  mag = lanes_max<kBlock / V>(mag);
+  if (mag > limit) {
+    // past the limit, infinities and NaN (a pattern above all others):
+    // numbers go to the limit, what is not finite to NaN (E4M3 has no
+    // infinity, and an overflow must not come back as a number) and out
+    // of the maximum
+    mag = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (i < n) amax = __builtin_fmaxf(amax, save_mag(v[i], limit));
-  amax = lanes_max<kBlock / V>(amax);
-  const int s = save_scale(amax);
+    for (int i = 0; i < V; ++i) {
+      const uint32_t u = __float_as_uint(v[i]), m = u & 0x7FFFFFFFu;
+      const uint32_t t = m < 0x7F800000u ? (m < limit ? m : limit) : 0u;
+      mag = t > mag ? t : mag;
+      v[i] = __uint_as_float(m < 0x7F800000u ? (u & 0x80000000u) | t : 0x7FC00000u);
+    }
+    mag = lanes_max<kBlock / V>(mag);
+  }
+  const int s = save_scale(mag);
   const float down = scale_down(s);
 #pragma unroll
   for (int j = 0; j < V / 4; ++j)
-    c.w[j] = encode4(save_scaled(v[4 * j], limit, down), save_scaled(v[4 * j + 1], limit, down),
-                     save_scaled(v[4 * j + 2], limit, down),
-                     save_scaled(v[4 * j + 3], limit, down));
+    c.w[j] = encode4(v[4 * j] * down, v[4 * j + 1] * down, v[4 * j + 2] * down,
+                     v[4 * j + 3] * down);
   return s;
+}
+
+// of FP32 values, saved as the element type DT; those past n do not count
+template <int DT, int V>
+__device__ __forceinline__ int encode(float (&v)[V], int n, Codes<V>& c) {
+  uint32_t mag = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t m = i < n ? __float_as_uint(v[i]) & 0x7FFFFFFFu : 0u;
+    mag = m > mag ? m : mag;
+  }
+  return encode_with<DT, V>(v, mag, c);
+}
+
+// of elements as they are in memory (0 where there are none)
+template <int DT, int V>
+__device__ __forceinline__ int encode(const Pack<DT, V>& q, Codes<V>& c) {
+  uint32_t mag = 0;
+  if constexpr (DT == kFP32) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint32_t m = q.w[i] & 0x7FFFFFFFu;
+      mag = m > mag ? m : mag;
+    }
+  } else {  // two patterns a word
+    using u2 = __attribute__((ext_vector_type(2))) uint16_t;
+    u2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u2, q.w[i] & 0x7FFF7FFFu));
+    const uint16_t top = m[0] > m[1] ? m[0] : m[1];
+    mag = DT == kBF16 ? (uint32_t)top << 16
+                      : __float_as_uint((float)__builtin_bit_cast(_Float16, top));
+  }
+  float v[V];
+  unpack(q, v);
+  return encode_with<DT, V>(v, mag, c);
 }
 
 }  // namespace mmaops

@@ -22,15 +22,13 @@ __global__ __launch_bounds__(256) void save_kernel(const void* x, int64_t ldx, u
   const int lane = threadIdx.x & ((1 << shift) - 1), g = threadIdx.x >> shift;
   const int64_t step = (int64_t)gridDim.x * (256 >> shift);
   const int64_t nb = (cols + kBlock - 1) / kBlock, end = nb * kBlock;
-  const float limit = save_limit(DT);
   const int64_t c0 = ((int64_t)blockIdx.y << shift) * V, cstep = ((int64_t)gridDim.y << shift) * V;
   for (int64_t row = (int64_t)blockIdx.x * (256 >> shift) + g; row < rows; row += step)
     for (int64_t c = c0 + lane * V; c < end; c += cstep) {
       const int n = cols - c < V ? (int)(cols - c) : V;
-      float v[V];
-      unpack(load_pack<DT, V>((const elem_t<DT>*)x + row * ldx + c, n), v);
       Codes<V> q;
-      const int s = encode<V>(v, n, limit, q);
+      const int s =
+          encode<DT, V>(load_pack<DT, V>((const elem_t<DT>*)x + row * ldx + c, n), q);
       if (n > 0) store_codes<V>(codes + row * cols + c, q, n);
       if (c % kBlock == 0) scales[row * nb + c / kBlock] = (uint8_t)s;
     }
@@ -52,6 +50,23 @@ __global__ __launch_bounds__(256) void restore_kernel(const uint8_t* codes,
       float v[V];
       decode<V>(load_codes<V>(codes + row * cols + c, n), scales[row * nb + c / kBlock], v);
       store_pack<DT, V>((elem_t<DT>*)y + row * ldy + c, pack<DT, V>(v), n);
+    }
+}
+
+// A matrix of 16-bit elements copied to rows of ldy elements that start on
+// 16 bytes, for the direct loads of a product.
+__global__ __launch_bounds__(256) void align_kernel(const uint16_t* x, int64_t ldx, uint16_t* y,
+                                                    int64_t ldy, int64_t rows, int64_t cols,
+                                                    int shift) {
+  constexpr int V = 8;
+  const int lane = threadIdx.x & ((1 << shift) - 1), g = threadIdx.x >> shift;
+  const int64_t step = (int64_t)gridDim.x * (256 >> shift);
+  const int64_t c0 = ((int64_t)blockIdx.y << shift) * V, cstep = ((int64_t)gridDim.y << shift) * V;
+  for (int64_t row = (int64_t)blockIdx.x * (256 >> shift) + g; row < rows; row += step)
+    for (int64_t c = c0 + lane * V; c < cols; c += cstep) {
+      const int n = cols - c < V ? (int)(cols - c) : V;
+      store_pack<kBF16, V>((__bf16*)(y + row * ldy + c),
+                           load_pack<kBF16, V>((const __bf16*)(x + row * ldx + c), n), V);
     }
 }
 
@@ -87,7 +102,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) db[i] = 0.0f;
   if (n > 0) {
-#pragma unroll 2
+#pragma unroll 4
     for (int64_t row = r0 + wave; row < r1; row += 4) {
       float d[V], z[V];
       unpack(load_pack<DT, V>((const E*)a.dy + row * a.lddy + c, n), d);
