@@ -135,7 +135,18 @@ def _types():
     return torch, {torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32}
 
 
-_torch = _dt = None
+_torch = _dt = _raw_stream = None
+
+
+def _start():
+    """torch and what is taken from it, on the first call."""
+    global _torch, _dt, _raw_stream
+    torch, types = _types()
+    # the handle of a device's current stream: torch's own short way to it,
+    # where this torch has it (making a Stream object takes 2.7 us)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _torch, _dt = torch, types
 
 
 def _matrix(t, what, dtype=None, shape=None, dev=None):
@@ -204,16 +215,15 @@ class _Call:
     __slots__ = ("dev", "raw", "_guards")
 
     def __init__(self, t, what, stream):
-        global _torch, _dt
         if _torch is None:
-            _torch, _dt = _types()
+            _start()
         if not isinstance(t, _torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{what} must be a device tensor")
         self.dev = t.device
         self._guards = None
         cuda = _torch.cuda
         if stream is None and cuda.current_device() == self.dev.index:
-            self.raw = cuda.current_stream().cuda_stream
+            self.raw = _raw_stream(self.dev.index)
             return
         if stream is not None and stream.device != self.dev:
             raise ValueError(f"the stream is on {stream.device}, the operands on {self.dev}")

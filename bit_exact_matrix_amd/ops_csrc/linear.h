@@ -97,6 +97,15 @@ __device__ __forceinline__ const char* uniform(const char* p) {
   return (const char*)((uint64_t)hi << 32 | lo);
 }
 
+// fn(integral_constant 0), .. fn(integral_constant N - 1)
+template <int N, typename FN>
+__device__ __forceinline__ void static_for(FN fn) {
+  if constexpr (N > 0) {
+    static_for<N - 1>(fn);
+    fn(std::integral_constant<int, N - 1>{});
+  }
+}
+
 template <int N>
 __device__ __forceinline__ void wait_loads() {  // all but the last N, and all LDS reads
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
@@ -241,7 +250,7 @@ __device__ __forceinline__ void finish(const LinearArgs& g, int64_t m, int step,
         store_pack<DT, V>((E*)g.z + (m + u * step) * g.ldz + c, pack<DT, V>(o), k);
     }
   }
-  act_apply_all(v, g.act);
+  act_all(v, g.act, act_apply);
   if (g.out_dt != kFP32) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -703,6 +712,116 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
                             n0 + wn * 128, lane);
 }
 
+// Up to 16 rows (a decoding step): what bounds it is reading the weight
+// once, from as many CUs and with as much under way as there can be.  A
+// workgroup takes BN = 16 columns (32 where z is saved, as a checkpoint
+// block is) and all of K, shared out over its eight waves.  A wave issues
+// the loads of its whole part of the weight at once, up to 16 KB, to LDS of
+// its own (no barrier); its part of X goes to registers.  The waves' sums
+// meet once, in wave order.  1 x 4096 x 4096 bf16, time on the GPU: W stored
+// N x K 8.6 us (3.9 TB/s), K x N 13.2 us, where a row of the tile is only 32
+// bytes (32 columns 13.6, 64 columns 14.9: fewer workgroups); K split over
+// workgroups and joined by a second kernel takes 8.7 + 3.8 us and a second
+// launch.
+template <int DT, int LB, int BN>
+__global__ __launch_bounds__(512, 2) void linear_rows_kernel(LinearArgs g) {
+  constexpr int BK = 64, NW = 8, FN = BN / 16, kSteps = 8 / FN;  // steps at once
+  using TB = Tile<BN, BK, LB, 1>;
+  using F = typename Mfma<DT>::frag;
+  using lds_f4 = __attribute__((address_space(3))) f32x4;
+  constexpr int kPer = TB::kPerWave;
+  __shared__ __attribute__((aligned(1024))) char smem[NW * kSteps * TB::kBytes];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  lds_char* const lds = (lds_char*)smem + wave * kSteps * TB::kBytes;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+  int tm, tn;
+  tile_of(1, (int)gridDim.x, tm, tn);
+  const int64_t n0 = (int64_t)tn * BN;
+  const int have_n = g.N - n0 < BN ? (int)(g.N - n0) : BN;
+  const int64_t steps = g.K / BK, s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
+  const int64_t b_step = (LB == 0 ? BK : BK * g.ldb) * 2;
+  const char* b = (const char*)g.b + (LB == 0 ? n0 * g.ldb : n0) * 2 + s0 * b_step;
+  // rows past M repeat the last one: what they give is not stored
+  const int64_t row = (lane & 15) < g.M ? (lane & 15) : g.M - 1;
+  const char* x = (const char*)g.a + (row * g.lda + s0 * BK + (lane >> 4) * 8) * 2;
+  uint32_t ob[kPer];
+  TB::offsets(g.ldb, have_n, 0, lane, ob);
+  const uint32_t base_b = TB::base(0, lane);
+  f32x4 acc[FN];
+#pragma unroll
+  for (int j = 0; j < FN; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t s = s0; s < s1; s += kSteps) {
+    const int n = s1 - s < kSteps ? (int)(s1 - s) : kSteps;
+    F fx[kSteps][2];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // LDS is read out
+#pragma unroll
+    for (int t = 0; t < kSteps; ++t) {
+      if (t >= n) continue;
+      __builtin_memcpy(&fx[t][0], x + t * BK * 2, 16);
+      __builtin_memcpy(&fx[t][1], x + t * BK * 2 + 64, 16);
+    }
+#pragma unroll
+    for (int t = 0; t < kSteps; ++t) {
+      if (t >= n) continue;
+      TB::load(b, ob, lds0 + t * TB::kBytes, 0);
+      b += b_step;
+    }
+    x += kSteps * BK * 2;
+    static_for<kSteps>([&](auto step) {
+      constexpr int t = decltype(step)::value;
+      if (t >= n) return;
+      if (n == kSteps)
+        wait_loads<(kSteps - 1 - t) * kPer>();
+      else
+        wait_loads<0>();
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[j] = Mfma<DT>::run(
+              TB::template frag<F>(lds + t * TB::kBytes, base_b, kk, j), fx[t][kk], acc[j]);
+    });
+  }
+  // [wave][row][column] sums
+  constexpr int kMeet = 16 * BN * 4;
+  lds_char* const meet = (lds_char*)smem;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+    *(lds_f4*)(meet + wave * kMeet + (lane & 15) * BN * 4 + j * 64 + (lane >> 4) * 16) = acc[j];
+  __syncthreads();
+  if (threadIdx.x >= 4 * BN) return;
+  const int64_t m = threadIdx.x / (BN / 4), c = n0 + threadIdx.x % (BN / 4) * 4;
+  const int have = g.N - c < 4 ? (int)(g.N - c) : 4;
+  float v[4], bias[4];
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const f32x4 u = *(const lds_f4*)(meet + w * kMeet + threadIdx.x * 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = w ? v[i] + u[i] : u[i];
+  }
+  load_bias<4>(g, c, have, bias);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] += bias[i];
+  if constexpr (BN == 32) {
+    if (g.codes) {
+      Codes<4> q;
+      float o[4] = {v[0], v[1], v[2], v[3]};
+      const int s = encode<DT, 4>(o, have, q);
+      if (m < g.M && have > 0) {
+        store_codes<4>(g.codes + m * g.N + c, q, have);
+        if (c % kBlock == 0)
+          g.scales[m * ((g.N + kBlock - 1) / kBlock) + c / kBlock] = (uint8_t)s;
+      }
+    }
+  }
+  Pack<DT, 4> res[1] = {};
+  if (m < g.M && have > 0 && g.residual && g.out_dt != kFP32)
+    res[0] = load_pack<DT, 4>((const elem_t<DT>*)g.residual + m * g.ldr + c, have);
+  finish<DT, 4, 1, false>(g, m, 0, c, have, v, res);
+}
+
 // The runs' sums added in run order, then the epilogue: four columns a
 // lane, eight neighbouring lanes for a checkpoint block.
 template <int DT>
@@ -745,13 +864,14 @@ __global__ __launch_bounds__(256) void linear_finish_kernel(LinearArgs g) {
 
 // ------------------------------------------------------------ variants
 // Tile sizes, workgroup shapes and how they are picked: linear_plan.
-enum { kTileBig = 0, kTileMid = 1, kTileSmall = 2, kTileFew = 3, kTiles = 4 };
+enum { kTileBig = 0, kTileMid = 1, kTileSmall = 2, kTileFew = 3, kTileRows = 4, kTiles = 5 };
 struct TileShape {
   int bm, bn, bk, waves;
   bool pairs;  // a wave holds whole checkpoint blocks
 };
 constexpr TileShape kTileShape[kTiles] = {
-    {256, 256, 64, 4, true}, {128, 128, 64, 4, true}, {64, 64, 64, 4, true}, {16, 64, 128, 4, false}};
+    {256, 256, 64, 4, true}, {128, 128, 64, 4, true}, {64, 64, 64, 4, true}, {16, 64, 128, 4, false},
+    {16, 16, 64, 8, true}};
 
 template <int DT, int LA, int LB>
 hipError_t linear_launch_tile(int tile, bool direct, const LinearArgs& g, hipStream_t s) {
@@ -765,6 +885,14 @@ hipError_t linear_launch_tile(int tile, bool direct, const LinearArgs& g, hipStr
       break;
     case kTileSmall:
       linear_kernel<DT, 64, 64, 64, 2, 2, LA, LB, 3, true, 2><<<grid, 256, 0, s>>>(g);
+      break;
+    case kTileRows:
+      if constexpr (LA == 0) {
+        if (g.codes)
+          linear_rows_kernel<DT, LB, 32><<<dim3((uint32_t)((g.N + 31) / 32)), 512, 0, s>>>(g);
+        else
+          linear_rows_kernel<DT, LB, 16><<<grid, 512, 0, s>>>(g);
+      }
       break;
     default:
       if (direct)

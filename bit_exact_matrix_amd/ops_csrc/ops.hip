@@ -265,7 +265,7 @@ struct Plan {
   bool direct, partial, copy_a, copy_b, guard;
 };
 
-// MMAOPS_LINEAR_TILE (0 to 3) and MMAOPS_LINEAR_SPLITS: diagnostic
+// MMAOPS_LINEAR_TILE (0 to 4) and MMAOPS_LINEAR_SPLITS: diagnostic
 // overrides of the choice below, read on every call, so that each variant
 // can be tested on any shape.
 int env_int(const char* name, int lo, int hi) {
@@ -292,11 +292,16 @@ Plan linear_plan(const Product& p, bool saves) {
            : tiles(kTileBig) >= 192    ? kTileBig
            : tiles(kTileMid) >= 128    ? kTileMid
                                        : kTileSmall;
+  // all of K in one workgroup: while K is short enough, whole steps, from
+  // direct loads that need no guard
+  const bool rows_fit = p.M <= 16 && p.la == 0 && fa && fb && p.K > 0 && p.K % 64 == 0 &&
+                        (p.lb == 0 || p.N % 8 == 0);
+  if (rows_fit && p.K <= 8192 && p.N <= 16384) q.tile = kTileRows;
   const int env_tile = env_int("MMAOPS_LINEAR_TILE", 0, kTiles - 1);
-  if (env_tile >= 0) q.tile = env_tile;
-  q.copy_a = q.tile != kTileFew && !fa;
-  q.copy_b = q.tile != kTileFew && !fb;
-  q.direct = q.tile != kTileFew || (fa && fb);
+  if (env_tile >= 0) q.tile = env_tile != kTileRows || rows_fit ? env_tile : kTileFew;
+  q.copy_a = q.tile < kTileFew && !fa;
+  q.copy_b = q.tile < kTileFew && !fb;
+  q.direct = q.tile < kTileFew || (fa && fb);
   q.guard = q.direct && ((p.la == 1 && p.M % 8) || (p.lb == 1 && p.N % 8));
   const TileShape& s = kTileShape[q.tile];
   const int64_t steps = (p.K + s.bk - 1) / s.bk, t = tiles(q.tile), n = t < 1 ? 1 : t;
@@ -305,6 +310,7 @@ Plan linear_plan(const Product& p, bool saves) {
   if (splits > steps / 4) splits = steps / 4;
   const int env_splits = env_int("MMAOPS_LINEAR_SPLITS", 1, 4096);
   if (env_splits >= 0) splits = env_splits < steps ? env_splits : steps;
+  if (q.tile == kTileRows) splits = 1;
   q.splits = splits < 1 ? 1 : (int)splits;
   q.partial = q.splits > 1 || (saves && !s.pairs);
   return q;

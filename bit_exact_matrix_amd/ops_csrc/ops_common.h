@@ -234,30 +234,6 @@ __device__ __forceinline__ float act_apply(float z, int act) {
   }
 }
 
-// the same for V values, one branch for all of them
-template <int V>
-__device__ __forceinline__ void act_apply_all(float (&v)[V], int act) {
-  switch (act) {
-    case kActRelu:
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = act_apply(v[i], kActRelu);
-      break;
-    case kActGelu:
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = act_apply(v[i], kActGelu);
-      break;
-    case kActGeluTanh:
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = act_apply(v[i], kActGeluTanh);
-      break;
-    case kActSilu:
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = act_apply(v[i], kActSilu);
-      break;
-    default: break;
-  }
-}
-
 // d act / d z
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
@@ -280,6 +256,32 @@ __device__ __forceinline__ float act_slope(float z, int act) {
       return s * (1.0f + z * (1.0f - s));
     }
     default: return 1.0f;
+  }
+}
+
+// FN of V values, one branch for all of them
+template <int V, typename FN>
+__device__ __forceinline__ void act_all(float (&v)[V], int act, FN fn) {
+  switch (act) {
+    case kActRelu:
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = fn(v[i], kActRelu);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = fn(v[i], kActGelu);
+      break;
+    case kActGeluTanh:
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = fn(v[i], kActGeluTanh);
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = fn(v[i], kActSilu);
+      break;
+    default:
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = fn(v[i], kActNone);
   }
 }
 

@@ -102,22 +102,46 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) db[i] = 0.0f;
   if (n > 0) {
-#pragma unroll 4
-    for (int64_t row = r0 + wave; row < r1; row += 4) {
-      float d[V], z[V];
-      unpack(load_pack<DT, V>((const E*)a.dy + row * a.lddy + c, n), d);
-      if (a.act != kActNone) {
-        if (a.codes)
-          decode<V>(load_codes<V>(a.codes + row * a.N + c, n), a.scales[row * nb + c / kBlock],
-                    z);
-        else
-          unpack(load_pack<DT, V>((const E*)a.z + row * a.ldz + c, n), z);
+    // kRows rows of the wave at once, so that their loads are all on their
+    // way before the first is used
+    constexpr int kRows = 2;
+    for (int64_t row = r0 + wave; row < r1; row += 4 * kRows) {
+      Pack<DT, V> dy[kRows], z[kRows];
+      Codes<V> q[kRows];
+      int sc[kRows];
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] *= act_slope(z[i], a.act);
+      for (int u = 0; u < kRows; ++u) {
+        const int64_t m = row + 4 * u;
+        const int k = m < r1 ? n : 0;
+        dy[u] = load_pack<DT, V>((const E*)a.dy + m * a.lddy + c, k);
+        if (a.act == kActNone) continue;
+        if (a.codes) {
+          q[u] = load_codes<V>(a.codes + m * a.N + c, k);
+          sc[u] = k ? a.scales[m * nb + c / kBlock] : 0;
+        } else {
+          z[u] = load_pack<DT, V>((const E*)a.z + m * a.ldz + c, k);
+        }
       }
-      if (a.dz) store_pack<DT, V>((E*)a.dz + row * a.lddz + c, pack<DT, V>(d), n);
 #pragma unroll
-      for (int i = 0; i < V; ++i) db[i] += d[i];
+      for (int u = 0; u < kRows; ++u) {
+        const int64_t m = row + 4 * u;
+        float d[V];
+        unpack(dy[u], d);
+        if (a.act != kActNone) {
+          float t[V];
+          if (a.codes)
+            decode<V>(q[u], sc[u], t);
+          else
+            unpack(z[u], t);
+          act_all(t, a.act, act_slope);
+#pragma unroll
+          for (int i = 0; i < V; ++i) d[i] *= t[i];
+        }
+        if (m >= r1) continue;
+        if (a.dz) store_pack<DT, V>((E*)a.dz + m * a.lddz + c, pack<DT, V>(d), n);
+#pragma unroll
+        for (int i = 0; i < V; ++i) db[i] += d[i];
+      }
     }
   }
   if (!a.partial) return;
