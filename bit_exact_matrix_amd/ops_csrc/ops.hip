@@ -276,6 +276,33 @@ int env_int(const char* name, int lo, int hi) {
   return end && *end == '\0' && x >= lo && x <= hi ? (int)x : -1;
 }
 
+// An estimate of a product's time on one MI355X, in us: `n` workgroups of a
+// tile, each `steps` long.  Fitted to times on the GPU from 33 x 4096 x 4096
+// to 2048 x 4096 x 4096, 64 x 1024 x 1024 to 8192 x 256 x 1024 and 256 x
+// 256 x 65536 (bf16, X W).  What the tiles take there, each side measured:
+//   512 x 4096 x 4096    small 31  mid 42  big 77
+//   1024 x 4096 x 4096   small 57  mid 46  big 79
+//   2048 x 4096 x 4096   small 106 mid 71  big 86
+//   4096 x 4096 x 4096             mid 132 big 102
+//   64 x 1024 x 1024     few 6.4  small 8.5  mid 14
+//   512 x 512 x 8192     small 36, its inner size split in four 19
+double tile_time(int tile, int64_t n, int64_t steps) {
+  const int64_t full = (n + kCUs - 1) / kCUs;  // workgroups of the fullest CU
+  const double even = (double)n / kCUs;
+  switch (tile) {
+    case kTileBig: return 8.0 + steps * 1.45 * full;
+    case kTileMid: return 4.6 + steps * (full / 2 * 1.03 + full % 2 * 0.62);
+    case kTileSmall: return 4.6 + steps * (even > 1.3 ? even * 0.2 : 0.26);
+    default: return 4.5 + steps * (even > 1.25 ? even * 0.24 : 0.3);
+  }
+}
+
+// the second kernel of a split product: its launch, and the partial sums
+// written and read
+double join_time(int64_t M, int64_t N, int64_t splits) {
+  return 4.5 + (double)M * N * splits * 8 / 5e6;
+}
+
 Plan linear_plan(const Product& p, bool saves) {
   Plan q;
   // direct loads take 16-byte pieces: rows that start on 16 bytes, and
@@ -288,31 +315,43 @@ Plan linear_plan(const Product& p, bool saves) {
     const TileShape& s = kTileShape[t];
     return ((p.M + s.bm - 1) / s.bm) * ((p.N + s.bn - 1) / s.bn);
   };
-  q.tile = p.M <= 32                   ? kTileFew
-           : tiles(kTileBig) >= 192    ? kTileBig
-           : tiles(kTileMid) >= 128    ? kTileMid
-                                       : kTileSmall;
   // all of K in one workgroup: while K is short enough, whole steps, from
   // direct loads that need no guard
   const bool rows_fit = p.M <= 16 && p.la == 0 && fa && fb && p.K > 0 && p.K % 64 == 0 &&
                         (p.lb == 0 || p.N % 8 == 0);
-  if (rows_fit && p.K <= 8192 && p.N <= 16384) q.tile = kTileRows;
   const int env_tile = env_int("MMAOPS_LINEAR_TILE", 0, kTiles - 1);
-  if (env_tile >= 0) q.tile = env_tile != kTileRows || rows_fit ? env_tile : kTileFew;
+  const int env_splits = env_int("MMAOPS_LINEAR_SPLITS", 1, 4096);
+  q.tile = kTileFew;
+  q.splits = 1;
+  if (env_tile == kTileRows ? rows_fit
+                            : env_tile < 0 && rows_fit && p.K <= 8192 && p.N <= 16384) {
+    q.tile = kTileRows;
+  } else {
+    double best = 1e300;
+    for (int t = 0; t <= kTileFew; ++t) {
+      if (env_tile >= 0 ? t != (env_tile < kTileFew ? env_tile : kTileFew)
+                        : t == kTileFew ? p.M > 128 : p.M <= 16)
+        continue;
+      const int64_t steps = (p.K + kTileShape[t].bk - 1) / kTileShape[t].bk, n = tiles(t);
+      for (int s = 1; s <= 32; s += s < 4 ? 1 : s / 2) {
+        const int k = env_splits >= 0 ? (int)(env_splits < steps ? env_splits : steps) : s;
+        if (env_splits < 0 && s > 1 && steps / s < 4) break;
+        const double time = tile_time(t, n * s, (steps + s - 1) / s) +
+                            (s > 1 ? join_time(p.M, p.N, s) : 0.0);
+        if (time < best) {
+          best = time;
+          q.tile = t;
+          q.splits = k < 1 ? 1 : k;
+        }
+        if (env_splits >= 0) break;
+      }
+    }
+  }
   q.copy_a = q.tile < kTileFew && !fa;
   q.copy_b = q.tile < kTileFew && !fb;
   q.direct = q.tile < kTileFew || (fa && fb);
   q.guard = q.direct && ((p.la == 1 && p.M % 8) || (p.lb == 1 && p.N % 8));
-  const TileShape& s = kTileShape[q.tile];
-  const int64_t steps = (p.K + s.bk - 1) / s.bk, t = tiles(q.tile), n = t < 1 ? 1 : t;
-  int64_t want = q.tile == kTileFew ? 512 : 256;
-  int64_t splits = n >= want ? 1 : want / n;
-  if (splits > steps / 4) splits = steps / 4;
-  const int env_splits = env_int("MMAOPS_LINEAR_SPLITS", 1, 4096);
-  if (env_splits >= 0) splits = env_splits < steps ? env_splits : steps;
-  if (q.tile == kTileRows) splits = 1;
-  q.splits = splits < 1 ? 1 : (int)splits;
-  q.partial = q.splits > 1 || (saves && !s.pairs);
+  q.partial = q.splits > 1 || (saves && !kTileShape[q.tile].pairs);
   return q;
 }
 
@@ -464,7 +503,7 @@ BackwardPlan backward_plan(const mma_linear_backward_args& r, void* ws) {
   if (r.dbias) {
     const int64_t cols = (r.N + 511) / 512;
     int64_t runs = (8 * kCUs + cols - 1) / cols;
-    if (runs > (r.M + 15) / 16) runs = (r.M + 15) / 16;
+    if (runs > (r.M + 7) / 8) runs = (r.M + 7) / 8;
     b.db_run = (r.M + runs - 1) / runs;
     b.db_runs = (int)((r.M + b.db_run - 1) / b.db_run);
     b.db_at = at;
@@ -593,7 +632,7 @@ hipError_t backward_run(const mma_linear_backward_args& r, void* ws, hipStream_t
     int64_t runs = b.db_runs;
     d.run = b.db_run;
     if (!r.dbias) {
-      runs = (r.M + 15) / 16 < 4096 ? (r.M + 15) / 16 : 4096;
+      runs = (r.M + 7) / 8 < 4096 ? (r.M + 7) / 8 : 4096;
       d.run = (r.M + runs - 1) / runs;
     }
     e = r.dtype == kFP16 ? dz_launch<kFP16>(d, runs, s) : dz_launch<kBF16>(d, runs, s);

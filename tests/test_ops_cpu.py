@@ -123,7 +123,7 @@ def test_linear_argument_errors(change, code):
 
 
 def test_linear_workspace_is_asked_for_and_checked():
-    few = dict(M=4, N=4096, K=4096, ldx=4096, ldw=4096, ldy=4096, ldr=4096, ldz=4096)
+    few = dict(M=4, N=4096, K=16384, ldx=16384, ldw=4096, ldy=4096, ldr=4096, ldz=4096)
     v = dict(LINEAR_OK, **few)
     need = ops.mma_linear_workspace(struct.pack("6i3q13Q", *(v[k] for k in LINEAR)))
     assert need > 0 and need % 256 == 0
@@ -137,7 +137,7 @@ def test_columns_of_one_buffer_do_not_overlap():
     """Y and the residual side by side in rows of 192 elements pass the
     alias check (this one stops at the missing workspace of a call that
     needs one, before any launch); one column more on either side does not."""
-    few = dict(M=4, N=4096, K=4096, ldx=4096, ldw=4096, ldz=4096, ldy=8192, ldr=8192)
+    few = dict(M=4, N=4096, K=16384, ldx=16384, ldw=4096, ldz=4096, ldy=8192, ldr=8192)
     v = dict(few, Y=Y, residual=Y + 4096 * 2)
     need = ops.mma_linear_workspace(struct.pack(
         "6i3q13Q", *(dict(LINEAR_OK, **v)[k] for k in LINEAR)))
