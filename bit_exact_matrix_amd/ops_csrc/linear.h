@@ -550,12 +550,12 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
                                 n0 + wn * (BN / WN), lane);
 }
 
-// The largest tile, 256 x 256: four waves, one for each SIMD, with 128 x
-// 128 each. A wave of that size reads 1 KiB of LDS for 16 matrix
-// instructions, where 128 x 64 reads 1.5 KiB: with eight waves LDS reads
-// and the tile's arrival would take as many cycles as the products.  With
-// one wave a SIMD nothing else hides a wait, so the loop is laid out by
-// hand: each LDS read and each load sits alone behind a matrix instruction,
+// The large tiles: four waves, one for each SIMD, with a quarter of the tile
+// each.  A wave of 128 x 128 (256 x 256 tile) reads 1 KiB of LDS for 16
+// matrix instructions, where 128 x 64 reads 1.5 KiB: with eight waves LDS
+// reads and the tile's arrival would take as many cycles as the products.
+// With one wave a SIMD nothing else hides a wait, so the loop is laid out
+// by hand (times below: 256 x 256, two stages): each LDS read and each load sits alone behind a matrix instruction,
 // as a lone wave issues one instruction every 4 cycles and a product takes
 // 16.  A step of BK = 64 runs in two halves of 64 products from registers:
 //   first half    the fragments of this step's second half are read; when
@@ -569,16 +569,18 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
 // whole 128-byte line; steps of 32 with a ring of four stages kept the
 // vector memory pipe busier than the products (8192^3, both operands with K
 // fastest: 922 us against 856).
-template <int DT, int LA, int LB>
+template <int DT, int LA, int LB, int BM, int BN, int STAGES>
 __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
-  constexpr int BM = 256, BN = 256, BK = 64, NW = 4, FM = 8, FN = 8;
+  constexpr int BK = 64, NW = 4, FM = BM / 32, FN = BN / 32;
   using TA = Tile<BM, BK, LA, NW>;
   using TB = Tile<BN, BK, LB, NW>;
   using F = typename Mfma<DT>::frag;
   constexpr int kStage = TA::kBytes + TB::kBytes;
   constexpr int kLoads = TA::kPerWave + TB::kPerWave;  // of a wave and step
-  static_assert(kLoads == 16 && TA::kPerWave == 8, "the slots below");
-  constexpr int kBytes = 2 * kStage > NW * kStoreBytes<FN, 4> ? 2 * kStage : NW * kStoreBytes<FN, 4>;
+  constexpr int kPass = FM < 8 ? 2 : 4;  // of the epilogue
+  constexpr int kBytes = STAGES * kStage > NW * kStoreBytes<FN, kPass>
+                             ? STAGES * kStage
+                             : NW * kStoreBytes<FN, kPass>;
   __shared__ __attribute__((aligned(1024))) char smem[kBytes];
   lds_char* const lds = (lds_char*)smem;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
@@ -605,17 +607,17 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const uint32_t base_a = TA::base(wm * 128, lane);
-  const uint32_t base_b = TB::base(wn * 128, lane) + TA::kBytes;
+  const uint32_t base_a = TA::base(wm * (BM / 2), lane);
+  const uint32_t base_b = TB::base(wn * (BN / 2), lane) + TA::kBytes;
 
   const int tail = g.K % BK ? (int)(g.K % BK) : g.guard ? BK : 0;
   if (s0 < s1 && s1 == steps && tail) {  // the part of a step, before the others
     s1 -= 1;
-    u32x4 v[TA::kPerWave];
-    TA::fetch(a + s1 * a_step, g.lda, have_m, tail, wave, lane, v);
-    TA::put(lds, wave, lane, v);
-    TB::fetch(b + s1 * b_step, g.ldb, have_n, tail, wave, lane, v);
-    TB::put(lds + TA::kBytes, wave, lane, v);
+    u32x4 va[TA::kPerWave], vb[TB::kPerWave];
+    TA::fetch(a + s1 * a_step, g.lda, have_m, tail, wave, lane, va);
+    TA::put(lds, wave, lane, va);
+    TB::fetch(b + s1 * b_step, g.ldb, have_n, tail, wave, lane, vb);
+    TB::put(lds + TA::kBytes, wave, lane, vb);
     __syncthreads();
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk)
@@ -637,10 +639,11 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
     TB::offsets(g.ldb, have_n, wave, lane, ob);
     // load i of a step, into the stage at `to`
     auto issue = [&](int i, uint32_t to) {
-      if (i & 1)
-        load_to_lds(uniform(b), ob[i >> 1], to + TA::kBytes + (wave * 8 + (i >> 1)) * 1024);
+      if (i < TB::kPerWave)
+        load_to_lds(uniform(b), ob[i], to + TA::kBytes + (wave * TB::kPerWave + i) * 1024);
       else
-        load_to_lds(uniform(a), oa[i >> 1], to + (wave * 8 + (i >> 1)) * 1024);
+        load_to_lds(uniform(a), oa[i - TB::kPerWave],
+                    to + (wave * TA::kPerWave + i - TB::kPerWave) * 1024);
     };
     // one step further; past the last one the same again (loaded, not used)
     int left = n;
@@ -659,15 +662,22 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     };
-    // slot of the first barrier, slots between loads, loads before the second
-    constexpr int kFree = 34, kEvery = 5, kFirst = (63 - kFree - 2) / kEvery + 1;
+    // Products of a half, slots between reads and between loads, the slot
+    // of the first barrier, and the loads before the second.
+    constexpr int S = FM * FN, kRead = S >= 64 ? 2 : 1, kEvery = S >= 64 ? 5 : 2;
+    constexpr int kFree = S >= 64 ? 34 : S >= 32 ? 20 : 12;
+    constexpr int kFirst = (S - 1 - kFree - 2) / kEvery + 1;
+    static_assert((FM + FN) * kRead <= kFree && (kLoads - kFirst) * kEvery < S, "slots");
     F a0[FM], b0[FN], a1[FM], b1[FN];
     uint32_t at = 0;  // this step's stage
+    auto after = [](uint32_t stage) {
+      return stage + kStage == STAGES * kStage ? 0u : stage + kStage;
+    };
     auto first_half = [&] {
 #pragma unroll
-      for (int s = 0; s < 64; ++s) {
-        acc[s / 8][s % 8] = Mfma<DT>::run(b0[s % 8], a0[s / 8], acc[s / 8][s % 8]);
-        if (s % 2 == 0 && s < 32) read(a1, b1, s / 2, 1, lds + at);
+      for (int s = 0; s < S; ++s) {
+        acc[s / FN][s % FN] = Mfma<DT>::run(b0[s % FN], a0[s / FN], acc[s / FN][s % FN]);
+        if (s % kRead == 0 && s / kRead < FM + FN) read(a1, b1, s / kRead, 1, lds + at);
         if (s == kFree) {
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
           barrier();
@@ -678,38 +688,39 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
       }
     };
     auto second_half = [&] {
+      const lds_char* const from = lds + after(at);
 #pragma unroll
-      for (int s = 0; s < 64; ++s) {
-        acc[s / 8][s % 8] = Mfma<DT>::run(b1[s % 8], a1[s / 8], acc[s / 8][s % 8]);
-        if (s % 2 == 0 && s < 32) read(a0, b0, s / 2, 0, lds + (at ^ kStage));
+      for (int s = 0; s < S; ++s) {
+        acc[s / FN][s % FN] = Mfma<DT>::run(b1[s % FN], a1[s / FN], acc[s / FN][s % FN]);
+        if (s % kRead == 0 && s / kRead < FM + FN) read(a0, b0, s / kRead, 0, from);
         if (s % kEvery == 1 && s / kEvery < kLoads - kFirst)
           issue(kFirst + s / kEvery, lds0 + at);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) issue(i, lds0 + s * kStage);
       next();
     }
-    wait_loads<kLoads>();
+    wait_loads<(STAGES - 1) * kLoads>();
     barrier();
 #pragma unroll
     for (int q = 0; q < FM + FN; ++q) read(a0, b0, q, 0, lds);
     for (int t = 0; t < n; ++t) {
       first_half();
-      wait_loads<kFirst>();
+      wait_loads<(STAGES - 2) * kLoads + kFirst>();
       barrier();
       second_half();
       next();
-      at ^= kStage;
+      at = after(at);
     }
     wait_loads<0>();
   }
   __syncthreads();
-  store_tile<DT, FM, FN, 4>(g, acc, lds + wave * kStoreBytes<FN, 4>, m0 + wm * 128,
-                            n0 + wn * 128, lane);
+  store_tile<DT, FM, FN, kPass>(g, acc, lds + wave * kStoreBytes<FN, kPass>,
+                                m0 + wm * (BM / 2), n0 + wn * (BN / 2), lane);
 }
 
 // Up to 16 rows (a decoding step): what bounds it is reading the weight
@@ -878,10 +889,17 @@ hipError_t linear_launch_tile(int tile, bool direct, const LinearArgs& g, hipStr
   const dim3 grid((uint32_t)(g.tiles_m * g.tiles_n), (uint32_t)g.splits);
   switch (tile) {
     case kTileBig:
-      linear_wide_kernel<DT, LA, LB><<<grid, 256, 0, s>>>(g);
+      linear_wide_kernel<DT, LA, LB, 256, 256, 2><<<grid, 256, 0, s>>>(g);
       break;
     case kTileMid:
-      linear_kernel<DT, 128, 128, 64, 2, 2, LA, LB, 2, true, 2><<<grid, 256, 0, s>>>(g);
+      // One workgroup a CU: three stages, for the loads have only 32 products
+      // a step to land behind.  More: two stages, so that two workgroups
+      // share a CU and hide each other's waits (bf16, K = 4096: 256 tiles
+      // 34.6 us with three, 43 with two; 512 tiles 64 and 59).
+      if ((int64_t)grid.x * grid.y <= 256)
+        linear_wide_kernel<DT, LA, LB, 128, 128, 3><<<grid, 256, 0, s>>>(g);
+      else
+        linear_wide_kernel<DT, LA, LB, 128, 128, 2><<<grid, 256, 0, s>>>(g);
       break;
     case kTileSmall:
       linear_kernel<DT, 64, 64, 64, 2, 2, LA, LB, 3, true, 2><<<grid, 256, 0, s>>>(g);

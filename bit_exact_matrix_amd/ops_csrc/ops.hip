@@ -280,18 +280,18 @@ int env_int(const char* name, int lo, int hi) {
 // tile, each `steps` long.  Fitted to times on the GPU from 33 x 4096 x 4096
 // to 2048 x 4096 x 4096, 64 x 1024 x 1024 to 8192 x 256 x 1024 and 256 x
 // 256 x 65536 (bf16, X W).  What the tiles take there, each side measured:
-//   512 x 4096 x 4096    small 31  mid 42  big 77
-//   1024 x 4096 x 4096   small 57  mid 46  big 79
-//   2048 x 4096 x 4096   small 106 mid 71  big 86
-//   4096 x 4096 x 4096             mid 132 big 102
-//   64 x 1024 x 1024     few 6.4  small 8.5  mid 14
+//   512 x 4096 x 4096    small 31  mid 33  big 77
+//   1024 x 4096 x 4096   small 57  mid 35  big 79
+//   2048 x 4096 x 4096   small 106 mid 59  big 86
+//   4096 x 4096 x 1024             mid 38  big 36
+//   64 x 1024 x 1024     few 6.4   small 8.5
 //   512 x 512 x 8192     small 36, its inner size split in four 19
 double tile_time(int tile, int64_t n, int64_t steps) {
   const int64_t full = (n + kCUs - 1) / kCUs;  // workgroups of the fullest CU
   const double even = (double)n / kCUs;
   switch (tile) {
     case kTileBig: return 8.0 + steps * 1.45 * full;
-    case kTileMid: return 4.6 + steps * (full / 2 * 1.03 + full % 2 * 0.62);
+    case kTileMid: return 4.6 + steps * (full / 2 * 0.86 + full % 2 * 0.47);
     case kTileSmall: return 4.6 + steps * (even > 1.3 ? even * 0.2 : 0.26);
     default: return 4.5 + steps * (even > 1.25 ? even * 0.24 : 0.3);
   }
@@ -315,8 +315,11 @@ Plan linear_plan(const Product& p, bool saves) {
     const TileShape& s = kTileShape[t];
     return ((p.M + s.bm - 1) / s.bm) * ((p.N + s.bn - 1) / s.bn);
   };
-  // all of K in one workgroup: while K is short enough, whole steps, from
-  // direct loads that need no guard
+  // all of K in one workgroup: whole steps, from direct loads that need no
+  // guard, one workgroup for each CU at most, while K is short enough (bf16,
+  // weights from memory, rows against few: 1 x 4096 x 4096 W stored N x K
+  // 10.5 us and 12.4, K x N 18.9 and 14.0; 1 x 4096 x 1024 4.9 and 5.8, 5.8
+  // and 6.2; 1 x 8192 x 4096 19.8 and 18.2; 16 x 512 x 8192 13.1 and 9.7)
   const bool rows_fit = p.M <= 16 && p.la == 0 && fa && fb && p.K > 0 && p.K % 64 == 0 &&
                         (p.lb == 0 || p.N % 8 == 0);
   const int env_tile = env_int("MMAOPS_LINEAR_TILE", 0, kTiles - 1);
@@ -324,7 +327,8 @@ Plan linear_plan(const Product& p, bool saves) {
   q.tile = kTileFew;
   q.splits = 1;
   if (env_tile == kTileRows ? rows_fit
-                            : env_tile < 0 && rows_fit && p.K <= 8192 && p.N <= 16384) {
+                            : env_tile < 0 && rows_fit && p.N <= 16 * kCUs &&
+                                  p.K <= (p.lb == 0 ? 4096 : 1024)) {
     q.tile = kTileRows;
   } else {
     double best = 1e300;
