@@ -287,7 +287,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, checkpoint=False, stream=Non
         raise TypeError("weight and bias must be of one type")
     pt = wt if wt is not None else bt if bt is not None else _dt[dt]
     with call:
-        y = call.empty((rows, cols), dt)
+        y = _torch.empty_like(x)  # rows of cols elements, whatever x's stride
         mean, rstd = call.empty((rows,), _torch.float32), call.empty((rows,), _torch.float32)
         ck = call.checkpoint((rows, cols), dt) if checkpoint else None
         rc = _load()["mma_layer_norm"](

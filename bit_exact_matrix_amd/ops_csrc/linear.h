@@ -836,23 +836,32 @@ __global__ __launch_bounds__(512, 2) void linear_rows_kernel(LinearArgs g) {
 // The runs' sums added in run order, then the epilogue: four columns a
 // lane, eight neighbouring lanes for a checkpoint block.
 template <int DT>
-__global__ __launch_bounds__(256) void linear_finish_kernel(LinearArgs g) {
+__global__ __launch_bounds__(64) void linear_finish_kernel(LinearArgs g) {
   const int64_t quads = (g.N + kBlock - 1) / kBlock * (kBlock / 4);  // of a row
   const int64_t total = quads * g.M;
-  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total;
-       t += (int64_t)gridDim.x * 256) {
+  for (int64_t t = (int64_t)blockIdx.x * 64 + threadIdx.x; t < total;
+       t += (int64_t)gridDim.x * 64) {
     const int64_t m = t / quads, c = (t - m * quads) * 4;
     const int n = g.N - c < 4 ? (int)(g.N - c) : 4;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (n > 0) {
+      // eight runs' sums on their way at once
       const float* p = g.partial + m * g.N + c;
-      unpack(load_pack<kFP32, 4>(p, n), v);
-#pragma unroll 4
-      for (int s = 1; s < g.splits; ++s) {
-        float u[4];
-        unpack(load_pack<kFP32, 4>(p + s * g.M * g.N, n), u);
+      const int64_t run = g.M * g.N;
+      for (int s0 = 0; s0 < g.splits; s0 += 8) {
+        Pack<kFP32, 4> u[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += u[i];
+        for (int s = 0; s < 8; ++s)
+          u[s] = load_pack<kFP32, 4>(p + (s0 + s) * run, s0 + s < g.splits ? n : 0);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          float w[4];
+          unpack(u[s], w);
+          if (s0 + s < g.splits) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = s0 + s ? v[i] + w[i] : w[i];
+          }
+        }
       }
       float bias[4];
       load_bias<4>(g, c, n, bias);
@@ -934,8 +943,8 @@ hipError_t linear_launch(int tile, bool direct, int la, int lb, const LinearArgs
     e = linear_launch_tile<DT, 1, 1>(tile, direct, g, s);
   if (e != hipSuccess || !g.partial) return e;
   const int64_t lanes = (g.N + kBlock - 1) / kBlock * (kBlock / 4) * g.M;
-  const int64_t blocks = (lanes + 255) / 256;
-  linear_finish_kernel<DT><<<(uint32_t)(blocks < 65536 ? blocks : 65536), 256, 0, s>>>(g);
+  const int64_t blocks = (lanes + 63) / 64;  // small ones: few outputs on many CUs
+  linear_finish_kernel<DT><<<(uint32_t)(blocks < 65536 ? blocks : 65536), 64, 0, s>>>(g);
   return hipGetLastError();
 }
 

@@ -293,7 +293,7 @@ double tile_time(int tile, int64_t n, int64_t steps) {
     case kTileBig: return 8.0 + steps * 1.45 * full;
     case kTileMid: return 4.6 + steps * (full / 2 * 0.86 + full % 2 * 0.47);
     case kTileSmall: return 4.6 + steps * (even > 1.3 ? even * 0.2 : 0.26);
-    default: return 4.5 + steps * (even > 1.25 ? even * 0.24 : 0.3);
+    default: return 4.5 + steps * (full > 1 ? full * 0.24 : 0.3);
   }
 }
 
@@ -354,7 +354,8 @@ Plan linear_plan(const Product& p, bool saves) {
   q.copy_a = q.tile < kTileFew && !fa;
   q.copy_b = q.tile < kTileFew && !fb;
   q.direct = q.tile < kTileFew || (fa && fb);
-  q.guard = q.direct && ((p.la == 1 && p.M % 8) || (p.lb == 1 && p.N % 8));
+  q.guard = q.direct && ((p.la == 1 && p.M % 8 && !q.copy_a) ||
+                         (p.lb == 1 && p.N % 8 && !q.copy_b));
   q.partial = q.splits > 1 || (saves && !kTileShape[q.tile].pairs);
   return q;
 }
