@@ -12,13 +12,21 @@
 //   X^T dz  A = X^T layout 1, B = dz  layout 1
 // A tile goes to LDS as it is stored, by direct global->LDS loads of 16
 // bytes a lane; layout 1 is turned on the way to the registers by the
-// transposing LDS read, so that no operand is ever rearranged in memory.
+// transposing LDS read, so that no operand is rearranged in memory (only
+// one whose rows do not start on 16 bytes is copied to rows that do).
+//
+// Kernels.  linear_wide_kernel (256 x 256 and 128 x 128 tiles, a loop laid
+// out by hand) for most products; linear_kernel for small tiles of 64 x 64
+// and for few rows (16 x 64, also through registers where an operand allows
+// no direct load); linear_rows_kernel for up to 16 rows in one launch.
+// Where there are few tiles, K is split over workgroups and
+// linear_finish_kernel adds the runs in order.
 //
 // LDS banks.  A layout-0 tile row is BK elements; 16-byte chunk c of row r
-// is kept at chunk c ^ (r & 7) (c ^ (r >> 1 & 3) in a row of 4 chunks), so
-// that the rows of a fragment read spread over the banks.  A layout-1 tile row is one k with R columns;
-// 32-byte slot s of row k is kept at s ^ g(k), with g taking 8 values over
-// the 8 rows that half a wave reads at once.  The permutation is applied
+// is kept at chunk c ^ (r & 7), so that the rows of a fragment read spread
+// over the banks.  A layout-1 tile row is one k with R columns; 32-byte
+// slot s of row k is kept at s ^ g(k), with g taking 8 values over the 8
+// rows that half a wave reads at once.  (Measured: no bank conflicts.)  The permutation is applied
 // to the global address of each lane, as the LDS side of a direct load is
 // always lane after lane.
 //
@@ -121,7 +129,7 @@ struct Tile {
   static constexpr int kRow = LAYOUT == 0 ? BK / 8 : R / 8;  // chunks of a tile row
 
   static __device__ __forceinline__ int swap_of(int r) {
-    if constexpr (LAYOUT == 0) return kRow == 4 ? (r >> 1) & 3 : r & 7;
+    if constexpr (LAYOUT == 0) return r & 7;
     constexpr int slots = R / 16;
     return ((r & 3) | ((r >> 3) & 1) << 2) & (slots < 8 ? slots - 1 : 7);
   }
@@ -416,6 +424,9 @@ __device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int& tm, int& 
   tn = in / down;
 }
 
+// The small tiles, their loop left to the compiler: several workgroups on a
+// CU hide each other's waits.  A ring of STAGES steps, one barrier a step;
+// DIRECT: direct loads, else through registers.
 template <int DT, int BM, int BN, int BK, int WM, int WN, int LA, int LB, int STAGES,
           bool DIRECT, int WAVES_EU>
 __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArgs g) {
@@ -565,7 +576,10 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
 //   second half   the fragments of the next step's first half are read, and
 //                 the loads go on
 // so a load has 1,200 to 2,400 cycles to land.  Loads every 4 slots or fewer
-// wait for the vector memory pipe (8192^3: every 2, 844 us, 4, 792, 5, 782).  A row of 64 elements is a
+// wait for the vector memory pipe (8192^3: every 2, 844 us, 4, 792, 5, 782).
+// What is left: 8192^3 bf16 takes 776 us (X W), 758 (X W^T) and 796 (X^T
+// dY), 1.38 to 1.45 PFLOP/s, at 1.8 GHz under this load with the matrix
+// cores busy 72% of the cycles; a fifth of the rest is the epilogue.  A row of 64 elements is a
 // whole 128-byte line; steps of 32 with a ring of four stages kept the
 // vector memory pipe busier than the products (8192^3, both operands with K
 // fastest: 922 us against 856).

@@ -11,12 +11,17 @@
 // What bounds both is memory: each element is read once and written once,
 // and a row stays in registers between its sums and its output.  A row is
 // held by GT lanes, NV vectors of 16 bytes each (one, as long as 1024 lanes
-// are enough: two cost the backward pass its registers, 134 us against 46
+// are enough: two cost the backward pass its registers, 134 us against 55
 // at 8192 x 4096 bf16); a workgroup of GT * G lanes works on G rows at a
 // time and walks the matrix, so weight and bias are loaded once and the
-// weight gradient's sums stay in registers until the workgroup's last row.  Each workgroup then writes one row of partial
-// sums, and a second kernel adds those in workgroup order: the result does
-// not depend on which workgroup ran first.
+// weight gradient's sums stay in registers until the workgroup's last row.
+// Each workgroup then writes one row of partial sums, and a second kernel
+// adds those in workgroup order: the result does not depend on which
+// workgroup ran first.
+//
+// Measured, 8192 x 4096 bf16: forward 27 us (134 MB, 5.0 TB/s), with the
+// checkpoint 31 us (169 MB, 5.4 TB/s); backward 42 us (201 MB, 4.8 TB/s) and
+// 4.6 us for the partial sums.  A copy of 256 MiB reaches 5.4 TB/s.
 #ifndef MMAOPS_NORM_H
 #define MMAOPS_NORM_H
 
@@ -226,11 +231,11 @@ __global__ __launch_bounds__(GT* G) void norm_backward_kernel(NormArgs a) {
   const float n_f = (float)a.cols;
   const int64_t step = (int64_t)gridDim.x * G;
 
-  // Three rows' loads: the one that is worked on and two on their way (a CU
-  // needs some 30 KB under way to draw its share of memory's rate; a
-  // workgroup of 1024 lanes has 32 bytes of each lane's row).  To leave
-  // registers for them, xh and h are made again from the loaded row after
-  // its sums have met, not kept.
+  // Two rows' loads: the one that is worked on and the next (a CU needs some
+  // 30 KB under way to draw its share of memory's rate; a workgroup of 1024
+  // lanes has 32 bytes of each lane's row).  To leave registers for them,
+  // xh and h are made again from the loaded row after its sums have met,
+  // not kept (55 us kept, 42 made again; a third row spills).
   constexpr int kAhead = 2;
   Raw<DT, SAVED, V> xr[kAhead][NV];
   Pack<DT, V> dr[kAhead][NV];
