@@ -132,8 +132,7 @@ __global__ __launch_bounds__(GT* G) void norm_kernel(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       unpack(raw[j], v[j]);
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[0] += v[j][i];
+      s[0] += pair_sum(v[j]);
     }
     if constexpr (SAVE) {
 #pragma unroll
@@ -305,6 +304,7 @@ __global__ __launch_bounds__(GT* G) void norm_backward_kernel(NormArgs a) {
   for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < a.rows; r0 += kAhead * step) {
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) {
+      if (r0 + q * step >= a.rows) break;  // the whole workgroup
       work(q, row);
       row += step;
     }
@@ -358,8 +358,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a, int pdt) {
       const Pack<DT, V> raw = load_pack<DT, V>(x + c, n);
       float v[V];
       unpack(raw, v);
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[0] += v[i];
+      s[0] += pair_sum(v);
       if constexpr (SAVE) {
         Codes<V> q;
         const int sc = encode<DT, V>(raw, q);

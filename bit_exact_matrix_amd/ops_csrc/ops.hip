@@ -73,8 +73,9 @@ struct Views {
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 // rows x cols of elements with leading dimension ld: sizes that 64-bit byte
-// offsets and the kernels' 32-bit column counters hold
-constexpr int64_t kMaxCols = int64_t(1) << 30, kMaxRows = int64_t(1) << 40;
+// offsets, the kernels' 32-bit column counters and a grid of fewer than 2^32
+// lanes (16 for each column, of the column sums) hold
+constexpr int64_t kMaxCols = int64_t(1) << 27, kMaxRows = int64_t(1) << 40;
 
 bool shape_ok(int64_t rows, int64_t cols, int64_t ld) {
   if (rows < 0 || cols < 0 || rows > kMaxRows || cols > kMaxCols) return false;
@@ -337,6 +338,8 @@ Plan linear_plan(const Product& p, bool saves) {
                         : t == kTileFew ? p.M > 128 : p.M <= 16)
         continue;
       const int64_t steps = (p.K + kTileShape[t].bk - 1) / kTileShape[t].bk, n = tiles(t);
+      if (t != kTileBig && env_tile < 0 && n * kTileShape[t].waves * 64 > UINT32_MAX)
+        continue;  // more lanes than a grid has
       for (int s = 1; s <= 32; s += s < 4 ? 1 : s / 2) {
         const int k = env_splits >= 0 ? (int)(env_splits < steps ? env_splits : steps) : s;
         if (env_splits < 0 && s > 1 && steps / s < 4) break;
@@ -427,7 +430,7 @@ hipError_t linear_run(int dt, const Product& p, const Plan& q, LinearArgs g, voi
 
 // sizes whose products and tile counts the 64-bit and 31-bit counters hold
 bool product_shape_ok(int64_t M, int64_t N, int64_t K) {
-  constexpr int64_t kMax = int64_t(1) << 30;
+  constexpr int64_t kMax = kMaxCols;
   if (M < 0 || N < 0 || K < 0 || M > kMax || N > kMax || K > kMax) return false;
   return ((M + 15) / 16) * ((N + 15) / 16) <= INT32_MAX &&
          ((M + 15) / 16) * ((K + 15) / 16) <= INT32_MAX &&

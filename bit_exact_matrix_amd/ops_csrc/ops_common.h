@@ -209,6 +209,20 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
+// Sum of V values (a power of two) in pairs: a third of the roundings on
+// each value's way that a chain has.
+template <int V>
+__device__ __forceinline__ float pair_sum(const float (&v)[V]) {
+  float t[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) t[i] = v[i];
+#pragma unroll
+  for (int n = V / 2; n > 0; n /= 2)
+#pragma unroll
+    for (int i = 0; i < n; ++i) t[i] += t[i + n];
+  return t[0];
+}
+
 // Maximum over 4 or 8 neighbouring lanes.
 template <int LANES>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {

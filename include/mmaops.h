@@ -43,7 +43,8 @@
  *   the caller and aligned to its elements.  Matrices are row-major with a
  *   leading dimension in elements (ld >= the row length); sizes may be odd
  *   and zero (an empty output is a no-op; sums over no rows are +0; with
- *   K = 0 a product is 0).  cols of a layer norm is at least 1.  Outputs
+ *   K = 0 a product is 0).  cols of a layer norm is at least 1; row lengths
+ *   and the sizes of a product are at most 2^27.  Outputs
  *   may not overlap any input or each other, except dX over dY of a layer
  *   norm (exactly, with the same leading dimension).
  *   WORKSPACE.  The library allocates nothing here: a call that needs

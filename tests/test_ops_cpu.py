@@ -37,7 +37,7 @@ NORM = [1, 1, X, 64, W, B, Y, 64, R, S, C, P, 8, 64, 1e-5, None]
 @pytest.mark.parametrize("at,value,code", [
     (0, 2, DTYPE), (0, 7, DTYPE), (1, 0, DTYPE), (1, 2, DTYPE),
     (13, 0, SHAPE), (13, -1, SHAPE), (12, -1, SHAPE), (3, 63, SHAPE), (7, 63, SHAPE),
-    (13, 1 << 31, SHAPE), (12, 1 << 41, SHAPE),
+    (13, 1 << 31, SHAPE), (13, (1 << 27) + 1, SHAPE), (12, 1 << 41, SHAPE),
     (2, 0, NULL), (6, 0, NULL), (8, 0, NULL), (9, 0, NULL), (10, 0, NULL), (11, 0, NULL),
     (2, X + 1, ALIGN), (4, W + 1, ALIGN), (5, B + 1, ALIGN), (6, Y + 1, ALIGN), (8, R + 2, ALIGN),
     (6, X, ALIAS), (6, X + 64, ALIAS), (6, W, ALIAS), (10, Y + 5, ALIAS), (9, R + 4, ALIAS),
