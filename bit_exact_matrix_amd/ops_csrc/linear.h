@@ -167,8 +167,8 @@ struct Tile {
   }
 
   // The same through registers, for any alignment and for a tile with only
-  // `kn` of its BK (the rest 0): `have` rows, element by element where a
-  // chunk passes an edge.
+  // `kn` of its BK (the rest 0): `have` rows, in parts where a chunk passes
+  // an edge.
   static __device__ __forceinline__ void fetch(const char* tile, int64_t ld, int have, int kn,
                                                int wave, int lane, u32x4 (&v)[kPerWave]) {
 #pragma unroll
@@ -182,11 +182,10 @@ struct Tile {
         const int n = cols - chunk * 8;
         if (n >= 8) {
           __builtin_memcpy(&v[i], p, 16);
-        } else {
-          const uint16_t* e = (const uint16_t*)p;
-#pragma unroll
-          for (int j = 0; j < 7; ++j)
-            if (j < n) v[i][j >> 1] |= (uint32_t)e[j] << (16 * (j & 1));
+        } else if (n > 0) {
+          uint32_t w[4];
+          load_part<4, 2>(p, n * 2, w);
+          v[i] = u32x4{w[0], w[1], w[2], w[3]};
         }
       }
     }
@@ -566,9 +565,10 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
 // matrix instructions, where 128 x 64 reads 1.5 KiB: with eight waves LDS
 // reads and the tile's arrival would take as many cycles as the products.
 // With one wave a SIMD nothing else hides a wait, so the loop is laid out
-// by hand (times below: 256 x 256, two stages): each LDS read and each load sits alone behind a matrix instruction,
-// as a lone wave issues one instruction every 4 cycles and a product takes
-// 16.  A step of BK = 64 runs in two halves of 64 products from registers:
+// by hand (times below: 256 x 256, two stages): each LDS read and each load
+// sits alone behind a matrix instruction, as a lone wave issues one
+// instruction every 4 cycles and a product takes 16.  A step of BK = 64
+// runs in two halves of 64 products from registers:
 //   first half    the fragments of this step's second half are read; when
 //                 they are there (slot 34) a barrier frees the stage, and
 //                 the loads of the step after next begin to fill it
@@ -904,8 +904,8 @@ struct TileShape {
   bool pairs;  // a wave holds whole checkpoint blocks
 };
 constexpr TileShape kTileShape[kTiles] = {
-    {256, 256, 64, 4, true}, {128, 128, 64, 4, true}, {64, 64, 64, 4, true}, {16, 64, 128, 4, false},
-    {16, 16, 64, 8, true}};
+    {256, 256, 64, 4, true},  {128, 128, 64, 4, true}, {64, 64, 64, 4, true},
+    {16, 64, 128, 4, false}, {16, 16, 64, 8, true}};
 
 template <int DT, int LA, int LB>
 hipError_t linear_launch_tile(int tile, bool direct, const LinearArgs& g, hipStream_t s) {

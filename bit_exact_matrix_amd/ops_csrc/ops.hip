@@ -258,9 +258,8 @@ struct Product {
 };
 
 // direct: direct loads from both operands.  What they cannot be loaded from
-// directly is copied to aligned rows first (copy_a, copy_b), except for the
-// tile of few rows, where that would read the weight twice: there the
-// tile goes through registers.
+// directly is copied to aligned rows first (copy_a, copy_b); for few rows,
+// where that reads the weight twice, the tile may go through registers.
 struct Plan {
   int tile, splits;
   bool direct, partial, copy_a, copy_b, guard;
@@ -298,6 +297,17 @@ double tile_time(int tile, int64_t n, int64_t steps) {
   }
 }
 
+// The tile of few rows through registers: a step waits for its loads, until
+// several workgroups share a CU (6 x 2135 x 132, W stored N x K: 33 us in 17
+// steps; copied to aligned rows and loaded directly, 12).
+double few_through_registers_time(int64_t n, int64_t steps) {
+  const double even = (double)n / kCUs;
+  return 4.5 + steps * (even > 3.6 ? even * 0.5 : 1.8);
+}
+
+// an operand of `elements` copied to aligned rows: a launch, read and written
+double copy_time(int64_t elements) { return 3.0 + (double)elements * 4 / 5e6; }
+
 // the second kernel of a split product: its launch, and the partial sums
 // written and read
 double join_time(int64_t M, int64_t N, int64_t splits) {
@@ -327,36 +337,43 @@ Plan linear_plan(const Product& p, bool saves) {
   const int env_splits = env_int("MMAOPS_LINEAR_SPLITS", 1, 4096);
   q.tile = kTileFew;
   q.splits = 1;
+  q.direct = true;
   if (env_tile == kTileRows ? rows_fit
                             : env_tile < 0 && rows_fit && p.N <= 16 * kCUs &&
                                   p.K <= (p.lb == 0 ? 4096 : 1024)) {
     q.tile = kTileRows;
   } else {
     double best = 1e300;
-    for (int t = 0; t <= kTileFew; ++t) {
+    const double copies = (fa ? 0.0 : copy_time(p.M * p.K)) + (fb ? 0.0 : copy_time(p.N * p.K));
+    for (int v = 0; v <= kTileFew + 1; ++v) {  // the last: few rows through registers
+      const int t = v < kTileFew ? v : kTileFew;
+      const bool direct = v <= kTileFew;
       if (env_tile >= 0 ? t != (env_tile < kTileFew ? env_tile : kTileFew)
                         : t == kTileFew ? p.M > 128 : p.M <= 16)
         continue;
+      if (!direct && fa && fb) continue;
       const int64_t steps = (p.K + kTileShape[t].bk - 1) / kTileShape[t].bk, n = tiles(t);
       if (t != kTileBig && env_tile < 0 && n * kTileShape[t].waves * 64 > UINT32_MAX)
         continue;  // more lanes than a grid has
       for (int s = 1; s <= 32; s += s < 4 ? 1 : s / 2) {
         const int k = env_splits >= 0 ? (int)(env_splits < steps ? env_splits : steps) : s;
-        if (env_splits < 0 && s > 1 && steps / s < 4) break;
-        const double time = tile_time(t, n * s, (steps + s - 1) / s) +
+        if (env_splits < 0 && s > 1 && steps / s < (direct ? 4 : 1)) break;
+        const int64_t run = (steps + s - 1) / s;
+        const double time = (direct ? tile_time(t, n * s, run) + copies
+                                    : few_through_registers_time(n * s, run)) +
                             (s > 1 ? join_time(p.M, p.N, s) : 0.0);
         if (time < best) {
           best = time;
           q.tile = t;
+          q.direct = direct;
           q.splits = k < 1 ? 1 : k;
         }
         if (env_splits >= 0) break;
       }
     }
   }
-  q.copy_a = q.tile < kTileFew && !fa;
-  q.copy_b = q.tile < kTileFew && !fb;
-  q.direct = q.tile < kTileFew || (fa && fb);
+  q.copy_a = q.direct && !fa;
+  q.copy_b = q.direct && !fb;
   q.guard = q.direct && ((p.la == 1 && p.M % 8 && !q.copy_a) ||
                          (p.lb == 1 && p.N % 8 && !q.copy_b));
   q.partial = q.splits > 1 || (saves && !kTileShape[q.tile].pairs);
