@@ -308,7 +308,8 @@ constexpr int kStoreBytes = PASS * 16 * (FN * 64 + 16);
 
 template <int DT, int FM, int FN, int PASS>
 __device__ __forceinline__ void store_tile(const LinearArgs& g, const f32x4 (&acc)[FM][FN],
-                                           lds_char* mem, int64_t m0, int64_t n0, int lane) {
+                                           lds_char* mem, int64_t m0, int64_t n0, int lane,
+                                           int split) {
   using E = elem_t<DT>;
   using lds_f4 = __attribute__((address_space(3))) f32x4;
   constexpr int kRow = FN * 64 + 16;
@@ -337,7 +338,7 @@ __device__ __forceinline__ void store_tile(const LinearArgs& g, const f32x4 (&ac
     }
   };
   if (g.partial) {
-    float* const out = g.partial + (int64_t)blockIdx.y * g.M * g.N + c;
+    float* const out = g.partial + (int64_t)split * g.M * g.N + c;
 #pragma unroll
     for (int i = 0; i < FM; i += PASS) {
       put(i);
@@ -407,12 +408,12 @@ __device__ __forceinline__ void store_tile(const LinearArgs& g, const f32x4 (&ac
   }
 }
 
-// Which tile a workgroup takes.  Workgroups go to the 8 XCDs in turn, so
+// Which tile workgroup b takes.  Workgroups go to the 8 XCDs in turn, so
 // workgroup i of an XCD is i * 8 + xcd; each XCD gets a run of consecutive
 // tiles, and tiles run down 8 rows before the next column, so that what
 // its L2 holds of A and B is used by its neighbours.
-__device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int n = tiles_m * tiles_n, b = blockIdx.x;
+__device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int b, int& tm, int& tn) {
+  const int n = tiles_m * tiles_n;
   const int per = n / 8, rest = n % 8, xcd = b % 8;
   const int t = xcd * per + (xcd < rest ? xcd : rest) + b / 8;
   constexpr int kDown = 8;
@@ -423,19 +424,22 @@ __device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int& tm, int& 
   tn = in / down;
 }
 
+template <int BM, int BN, int BK, int STAGES>
+constexpr int kRingBytes = STAGES * (BM + BN) * BK * 2;
+
 // The small tiles, their loop left to the compiler: several workgroups on a
 // CU hide each other's waits.  A ring of STAGES steps, one barrier a step;
 // DIRECT: direct loads, else through registers.
 template <int DT, int BM, int BN, int BK, int WM, int WN, int LA, int LB, int STAGES,
-          bool DIRECT, int WAVES_EU>
-__global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArgs g) {
+          bool DIRECT>
+__device__ __forceinline__ void small_product(const LinearArgs& g, int block, int split,
+                                              char* smem) {
   constexpr int NW = WM * WN;
   using TA = Tile<BM, BK, LA, NW>;
   using TB = Tile<BN, BK, LB, NW>;
   using F = typename Mfma<DT>::frag;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
   constexpr int kStage = TA::kBytes + TB::kBytes;
-  __shared__ __attribute__((aligned(1024))) char smem[STAGES * kStage];
   lds_char* const lds = (lds_char*)smem;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
@@ -443,7 +447,7 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   int tm, tn;
-  tile_of(g.tiles_m, g.tiles_n, tm, tn);
+  tile_of(g.tiles_m, g.tiles_n, block, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int have_m = g.M - m0 < BM ? (int)(g.M - m0) : BM;
   const int have_n = g.N - n0 < BN ? (int)(g.N - n0) : BN;
@@ -451,7 +455,7 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
   // this split's steps of BK; the last of all may be a part of one
   const int64_t steps = (g.K + BK - 1) / BK;
   const int64_t per = (steps + g.splits - 1) / g.splits;
-  const int64_t s0 = blockIdx.y * per;
+  const int64_t s0 = split * per;
   int64_t s1 = s0 + per < steps ? s0 + per : steps;
   const int64_t a_step = (LA == 0 ? BK : BK * g.lda) * 2;
   const int64_t b_step = (LB == 0 ? BK : BK * g.ldb) * 2;
@@ -557,7 +561,56 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
   static_assert(NW * kStoreBytes<FN, kPass> <= STAGES * kStage, "the epilogue's LDS");
   __syncthreads();
   store_tile<DT, FM, FN, kPass>(g, acc, lds + wave * kStoreBytes<FN, kPass>, m0 + wm * (BM / WM),
-                                n0 + wn * (BN / WN), lane);
+                                n0 + wn * (BN / WN), lane, split);
+}
+
+template <int DT, int BM, int BN, int BK, int WM, int WN, int LA, int LB, int STAGES,
+          bool DIRECT, int WAVES_EU>
+__global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArgs g) {
+  __shared__ __attribute__((aligned(1024))) char smem[kRingBytes<BM, BN, BK, STAGES>];
+  small_product<DT, BM, BN, BK, WM, WN, LA, LB, STAGES, DIRECT>(g, blockIdx.x, blockIdx.y, smem);
+}
+
+// A small backward pass's second launch: the tiles of dz W^T (layouts 0, LB),
+// then those of X^T dz (1, 1), then the bias gradient's column sums, 64
+// columns a workgroup; all need only the first launch's dz and partial sums.
+// Launches bound such a pass, so three are one (fp16, gelu, the whole pass on
+// the GPU, apart and together: 299 x 260 x 640 21.5 us and 13.8, 512 x 512 x
+// 512 17.7 and 10.3, 1024 x 1024 x 1024 25.5 and 16.7).
+struct PairArgs {
+  LinearArgs dx, dw;
+  const float* partial;  // [count][cols]
+  void* dbias;           // NULL: none
+  int64_t cols;
+  int count, dbias_dt;
+};
+
+template <int DT, int LB>
+__global__ __launch_bounds__(256, 2) void linear_pair_kernel(PairArgs p) {
+  __shared__ __attribute__((aligned(1024))) char smem[kRingBytes<64, 64, 64, 3>];
+  const int n1 = p.dx.tiles_m * p.dx.tiles_n, n2 = p.dw.tiles_m * p.dw.tiles_n;
+  const int b = blockIdx.x;
+  if (b < n1) {
+    small_product<DT, 64, 64, 64, 2, 2, 0, LB, 3, true>(p.dx, b, 0, smem);
+  } else if (b < n1 + n2) {
+    small_product<DT, 64, 64, 64, 2, 2, 1, 1, 3, true>(p.dw, b - n1, 0, smem);
+  } else {
+    float(&meet)[4][64] = *(float(*)[4][64])smem;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = (int64_t)(b - n1 - n2) * 64 + lane;
+    const int run = (p.count + 3) / 4, q0 = wave * run;
+    const int q1 = q0 + run < p.count ? q0 + run : p.count;
+    float s = 0.0f;
+    if (c < p.cols) {
+#pragma unroll 16
+      for (int q = q0; q < q1; ++q) s += p.partial[q * p.cols + c];
+    }
+    meet[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < p.cols)
+      store_any(p.dbias, c, ((meet[0][lane] + meet[1][lane]) + meet[2][lane]) + meet[3][lane],
+                p.dbias_dt);
+  }
 }
 
 // The large tiles: four waves, one for each SIMD, with a quarter of the tile
@@ -579,7 +632,7 @@ __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArg
 // wait for the vector memory pipe (8192^3: every 2, 844 us, 4, 792, 5, 782).
 // What is left: 8192^3 bf16 takes 776 us (X W), 758 (X W^T) and 796 (X^T
 // dY), 1.38 to 1.45 PFLOP/s, at 1.8 GHz under this load with the matrix
-// cores busy 72% of the cycles; a fifth of the rest is the epilogue.  A row of 64 elements is a
+// cores busy 71% of the cycles; a fifth of the rest is the epilogue.  A row of 64 elements is a
 // whole 128-byte line; steps of 32 with a ring of four stages kept the
 // vector memory pipe busier than the products (8192^3, both operands with K
 // fastest: 922 us against 856).
@@ -603,7 +656,7 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   int tm, tn;
-  tile_of(g.tiles_m, g.tiles_n, tm, tn);
+  tile_of(g.tiles_m, g.tiles_n, blockIdx.x, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int have_m = g.M - m0 < BM ? (int)(g.M - m0) : BM;
   const int have_n = g.N - n0 < BN ? (int)(g.N - n0) : BN;
@@ -734,7 +787,7 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
   }
   __syncthreads();
   store_tile<DT, FM, FN, kPass>(g, acc, lds + wave * kStoreBytes<FN, kPass>,
-                                m0 + wm * (BM / 2), n0 + wn * (BN / 2), lane);
+                                m0 + wm * (BM / 2), n0 + wn * (BN / 2), lane, blockIdx.y);
 }
 
 // Up to 16 rows (a decoding step): what bounds it is reading the weight
@@ -761,7 +814,7 @@ __global__ __launch_bounds__(512, 2) void linear_rows_kernel(LinearArgs g) {
   lds_char* const lds = (lds_char*)smem + wave * kSteps * TB::kBytes;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
   int tm, tn;
-  tile_of(1, (int)gridDim.x, tm, tn);
+  tile_of(1, (int)gridDim.x, blockIdx.x, tm, tn);
   const int64_t n0 = (int64_t)tn * BN;
   const int have_n = g.N - n0 < BN ? (int)(g.N - n0) : BN;
   const int64_t steps = g.K / BK, s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
@@ -962,6 +1015,20 @@ hipError_t linear_launch(int tile, bool direct, int la, int lb, const LinearArgs
   return hipGetLastError();
 }
 
+template <int DT>
+hipError_t pair_launch(int lb, const PairArgs& p, hipStream_t s) {
+  const int64_t sums = p.dbias ? (p.cols + 63) / 64 : 0;
+  const uint32_t grid = (uint32_t)((int64_t)p.dx.tiles_m * p.dx.tiles_n +
+                                   (int64_t)p.dw.tiles_m * p.dw.tiles_n + sums);
+  if (lb)
+    linear_pair_kernel<DT, 1><<<grid, 256, 0, s>>>(p);
+  else
+    linear_pair_kernel<DT, 0><<<grid, 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t pair_launch_fp16(int lb, const PairArgs& p, hipStream_t s);
+hipError_t pair_launch_bf16(int lb, const PairArgs& p, hipStream_t s);
 hipError_t linear_launch_fp16(int tile, bool direct, int la, int lb, const LinearArgs& g,
                               hipStream_t s);
 hipError_t linear_launch_bf16(int tile, bool direct, int la, int lb, const LinearArgs& g,

@@ -410,8 +410,9 @@ hipError_t align_rows(const void* x, int64_t ldx, void* y, const Stored& t, hipS
   return hipGetLastError();
 }
 
-hipError_t linear_run(int dt, const Product& p, const Plan& q, LinearArgs g, void* ws,
-                      hipStream_t s) {
+// A product's arguments, with its operands copied where the plan says so.
+hipError_t linear_fill(const Product& p, const Plan& q, LinearArgs& g, void* ws,
+                       hipStream_t s) {
   const TileShape& t = kTileShape[q.tile];
   g.a = p.a;
   g.b = p.b;
@@ -441,6 +442,13 @@ hipError_t linear_run(int dt, const Product& p, const Plan& q, LinearArgs g, voi
   g.tiles_m = (int)((p.M + t.bm - 1) / t.bm);
   g.tiles_n = (int)((p.N + t.bn - 1) / t.bn);
   g.partial = q.partial ? (float*)ws : nullptr;
+  return hipSuccess;
+}
+
+hipError_t linear_run(int dt, const Product& p, const Plan& q, LinearArgs g, void* ws,
+                      hipStream_t s) {
+  const hipError_t e = linear_fill(p, q, g, ws, s);
+  if (e != hipSuccess) return e;
   return dt == kFP16 ? linear_launch_fp16(q.tile, q.direct, p.la, p.lb, g, s)
                      : linear_launch_bf16(q.tile, q.direct, p.la, p.lb, g, s);
 }
@@ -507,7 +515,8 @@ struct BackwardPlan {
   bool has_dz;      // dz is written (an activation, and a product to use it)
   int db_runs;      // rows of column sums, 0: no bias gradient
   int64_t db_run;   // rows of one of them
-  int64_t dz_at, x_at, db_at, part_at, bytes;
+  int64_t dz_at, x_at, db_at, part_at, part2_at, bytes;
+  bool pair;        // both products and the column sums in one launch
 };
 
 BackwardPlan backward_plan(const mma_linear_backward_args& r, void* ws) {
@@ -552,7 +561,13 @@ BackwardPlan backward_plan(const mma_linear_backward_args& r, void* ws) {
     const int64_t w = product_bytes(b.dw, b.pdw);
     part = part > w ? part : w;
   }
-  b.bytes = at + part;
+  // Both on small tiles, whole, and few enough that one grid holds them: one
+  // launch.  Their copies, if any, then stand in the workspace side by side.
+  auto tiles = [](const Product& p) { return ((p.M + 63) / 64) * ((p.N + 63) / 64); };
+  b.pair = r.dX && r.dW && r.K && b.pdx.tile == kTileSmall && b.pdw.tile == kTileSmall &&
+           !b.pdx.partial && !b.pdw.partial && tiles(b.dx) + tiles(b.dw) <= (1 << 20);
+  b.part2_at = b.pair ? at + product_bytes(b.dx, b.pdx) : at;
+  b.bytes = b.pair ? b.part2_at + product_bytes(b.dw, b.pdw) : at + part;
   return b;
 }
 
@@ -662,31 +677,44 @@ hipError_t backward_run(const mma_linear_backward_args& r, void* ws, hipStream_t
     }
     e = r.dtype == kFP16 ? dz_launch<kFP16>(d, runs, s) : dz_launch<kBF16>(d, runs, s);
     if (e != hipSuccess) return e;
-    if (r.dbias) {
+    if (r.dbias && !b.pair) {
       e = column_sums(d.partial, b.db_runs, r.N, r.dbias, nullptr, 0, r.bias_dtype, s);
       if (e != hipSuccess) return e;
     }
   }
-  LinearArgs g;
-  memset(&g, 0, sizeof g);
-  if (r.dX && r.K) {
-    g.y = r.dX;
-    g.ldy = r.lddx;
-    g.out_dt = r.dtype;
-    e = linear_run(r.dtype, b.dx, b.pdx, g, base + b.part_at, s);
+  if (r.dW && r.K && r.x_codes) {
+    e = restore_to(r.dtype, r.x_codes, r.x_scales, base + b.x_at, (r.K + 7) / 8 * 8, r.M, r.K, s);
     if (e != hipSuccess) return e;
   }
-  if (r.dW && r.K) {
-    if (r.x_codes) {
-      e = restore_to(r.dtype, r.x_codes, r.x_scales, base + b.x_at, (r.K + 7) / 8 * 8, r.M, r.K,
-                     s);
-      if (e != hipSuccess) return e;
-    }
-    g.y = r.dW;
-    g.ldy = r.lddw;
-    g.out_dt = r.dw_dtype;
-    e = linear_run(r.dtype, b.dw, b.pdw, g, base + b.part_at, s);
+  LinearArgs gx, gw;
+  memset(&gx, 0, sizeof gx);
+  memset(&gw, 0, sizeof gw);
+  gx.y = r.dX;
+  gx.ldy = r.lddx;
+  gx.out_dt = r.dtype;
+  gw.y = r.dW;
+  gw.ldy = r.lddw;
+  gw.out_dt = r.dw_dtype;
+  if (b.pair) {
+    PairArgs p;
+    memset(&p, 0, sizeof p);
+    e = linear_fill(b.dx, b.pdx, gx, base + b.part_at, s);
+    if (e == hipSuccess) e = linear_fill(b.dw, b.pdw, gw, base + b.part2_at, s);
+    if (e != hipSuccess) return e;
+    p.dx = gx;
+    p.dw = gw;
+    p.partial = (const float*)(base + b.db_at);
+    p.dbias = r.dbias;
+    p.cols = r.N;
+    p.count = b.db_runs;
+    p.dbias_dt = r.bias_dtype;
+    return r.dtype == kFP16 ? pair_launch_fp16(b.dx.lb, p, s) : pair_launch_bf16(b.dx.lb, p, s);
   }
+  if (r.dX && r.K) {
+    e = linear_run(r.dtype, b.dx, b.pdx, gx, base + b.part_at, s);
+    if (e != hipSuccess) return e;
+  }
+  if (r.dW && r.K) e = linear_run(r.dtype, b.dw, b.pdw, gw, base + b.part2_at, s);
   return e;
 }
 

@@ -140,6 +140,19 @@ def test_linear_backward_as_chosen(torch_dev, act):
                        "nk" if i % 2 else "kn", act, 0, i != 1, seed=i)
 
 
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+def test_backward_products_in_one_launch(torch_dev, monkeypatch, layout):
+    """Small tiles, whole: dX, dW and the bias sums share a launch, and the
+    products' bits are those of each asked for alone."""
+    torch, dev = torch_dev
+    monkeypatch.setenv("MMAOPS_LINEAR_TILE", TILES["small"])
+    monkeypatch.setenv("MMAOPS_LINEAR_SPLITS", "1")
+    for i, (m, n, k) in enumerate([(17, 24, 40), (299, 261, 643), (64, 640, 8), (1000, 65, 129)]):
+        for act in ("none", ACTS[1 + i]):
+            check_backward(torch, dev, m, n, k, torch.float16 if i % 2 else torch.bfloat16,
+                           layout, act, (0, 3)[i % 2], i == 3, wide=i == 0, seed=i)
+
+
 def test_gradient_against_differences(torch_dev):
     """<gradient, v> against central differences of the float64 formula of
     sum(c y): the difference is off by h^2/6 of a third derivative (below
