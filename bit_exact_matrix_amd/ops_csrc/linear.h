@@ -790,6 +790,44 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
                                 m0 + wm * (BM / 2), n0 + wn * (BN / 2), lane, blockIdx.y);
 }
 
+// The end of a product of up to ROWS rows: BN columns' [wave][row][column]
+// sums added in wave order, then the epilogue, four columns a lane.
+template <int DT, int ROWS, int BN, int NW>
+__device__ __forceinline__ void finish_rows(const LinearArgs& g, const lds_char* meet,
+                                            int64_t n0) {
+  using lds_f4 = __attribute__((address_space(3))) f32x4;
+  constexpr int kMeet = ROWS * BN * 4;
+  if (threadIdx.x >= ROWS * BN / 4) return;
+  const int64_t m = threadIdx.x / (BN / 4), c = n0 + threadIdx.x % (BN / 4) * 4;
+  const int have = g.N - c < 4 ? (int)(g.N - c) : 4;
+  float v[4], bias[4];
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const f32x4 u = *(const lds_f4*)(meet + w * kMeet + threadIdx.x * 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = w ? v[i] + u[i] : u[i];
+  }
+  load_bias<4>(g, c, have, bias);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] += bias[i];
+  if constexpr (BN >= 32) {
+    if (g.codes) {
+      Codes<4> q;
+      float o[4] = {v[0], v[1], v[2], v[3]};
+      const int s = encode<DT, 4>(o, have, q);
+      if (m < g.M && have > 0) {
+        store_codes<4>(g.codes + m * g.N + c, q, have);
+        if (c % kBlock == 0)
+          g.scales[m * ((g.N + kBlock - 1) / kBlock) + c / kBlock] = (uint8_t)s;
+      }
+    }
+  }
+  Pack<DT, 4> res[1] = {};
+  if (m < g.M && have > 0 && g.residual && g.out_dt != kFP32)
+    res[0] = load_pack<DT, 4>((const elem_t<DT>*)g.residual + m * g.ldr + c, have);
+  finish<DT, 4, 1, false>(g, m, 0, c, have, v, res);
+}
+
 // Up to 16 rows (a decoding step): what bounds it is reading the weight
 // once, from as many CUs and with as much under way as there can be.  A
 // workgroup takes BN = 16 columns (32 where z is saved, as a checkpoint
@@ -862,42 +900,94 @@ __global__ __launch_bounds__(512, 2) void linear_rows_kernel(LinearArgs g) {
     });
   }
   // [wave][row][column] sums
-  constexpr int kMeet = 16 * BN * 4;
   lds_char* const meet = (lds_char*)smem;
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < FN; ++j)
-    *(lds_f4*)(meet + wave * kMeet + (lane & 15) * BN * 4 + j * 64 + (lane >> 4) * 16) = acc[j];
+    *(lds_f4*)(meet + wave * (16 * BN * 4) + (lane & 15) * BN * 4 + j * 64 + (lane >> 4) * 16) =
+        acc[j];
   __syncthreads();
-  if (threadIdx.x >= 4 * BN) return;
-  const int64_t m = threadIdx.x / (BN / 4), c = n0 + threadIdx.x % (BN / 4) * 4;
-  const int have = g.N - c < 4 ? (int)(g.N - c) : 4;
-  float v[4], bias[4];
+  finish_rows<DT, 16, BN, NW>(g, meet, n0);
+}
+
+// One or two rows against a weight stored K x N whose rows direct loads
+// cannot take (odd lengths): in one launch, through registers.  A lane has 8
+// columns of 8 consecutive rows of the weight, all on their way at once (128
+// KB a workgroup), and its own sums of MR x 8 products.  The lanes' sums meet
+// by swaps, the waves' in LDS in wave order.  A row's piece of 32 bytes costs
+// a CU about 4 cycles and one of 128 bytes 5, so BN = 16 columns only while
+// that gives each CU one workgroup, then 32, then 64 (1 x 4097 x 4096: 18.9,
+// 15.2 and 23.2 us; 1 x 11009 x 4095: 39.9, 33.5 and 25.6).  One row, bf16,
+// beside the weight copied to aligned rows or the tile of few rows through
+// registers: N x K 1499 x 1023 8.7 us and 13.7, 2135 x 132 5.4 and 7.3, 4097
+// x 4096 15.2 and 21.6.  Aligned weights: 4096 x 4096 14.8 here, 13.0 with K
+// split over workgroups.  Four rows: more products and sums than registers,
+// 11.7 and 14.0, 22.0 and 25.2, but 42 and 32 at 11009 x 4095.
+template <int DT, int MR, int BN>
+__global__ __launch_bounds__(1024) void linear_vec_kernel(LinearArgs g) {
+  constexpr int NW = 16, kLanes = BN / 8, kAtOnce = NW * 64 / kLanes;  // runs of 8 rows
+  __shared__ __attribute__((aligned(16))) float smem[NW * MR * BN];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int tm, tn;
+  tile_of(1, (int)gridDim.x, blockIdx.x, tm, tn);
+  const int64_t n0 = (int64_t)tn * BN;
+  const int64_t c = n0 + (lane % kLanes) * 8;
+  const int n = g.N - c < 8 ? (int)(g.N - c) : 8;
+  const elem_t<DT>* const b = (const elem_t<DT>*)g.b + c;
+  const elem_t<DT>* const a = (const elem_t<DT>*)g.a;
+  float v[MR * 8];
 #pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    const f32x4 u = *(const lds_f4*)(meet + w * kMeet + threadIdx.x * 16);
+  for (int i = 0; i < MR * 8; ++i) v[i] = 0.0f;
+  for (int64_t k = (int64_t)(threadIdx.x / kLanes) * 8; k < g.K; k += kAtOnce * 8) {
+    const int have = g.K - k < 8 ? (int)(g.K - k) : 8;
+    Pack<DT, 8> w[8], x[MR];
+    if (n == 8 && have == 8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = w ? v[i] + u[i] : u[i];
-  }
-  load_bias<4>(g, c, have, bias);
+      for (int t = 0; t < 8; ++t) w[t] = load_pack<DT, 8>(b + (k + t) * g.ldb);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] += bias[i];
-  if constexpr (BN == 32) {
-    if (g.codes) {
-      Codes<4> q;
-      float o[4] = {v[0], v[1], v[2], v[3]};
-      const int s = encode<DT, 4>(o, have, q);
-      if (m < g.M && have > 0) {
-        store_codes<4>(g.codes + m * g.N + c, q, have);
-        if (c % kBlock == 0)
-          g.scales[m * ((g.N + kBlock - 1) / kBlock) + c / kBlock] = (uint8_t)s;
-      }
+      for (int m = 0; m < MR; ++m) x[m] = load_pack<DT, 8>(a + m * g.lda + k);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) w[t] = load_pack<DT, 8>(b + (k + t) * g.ldb, t < have ? n : 0);
+#pragma unroll
+      for (int m = 0; m < MR; ++m) x[m] = load_pack<DT, 8>(a + m * g.lda + k, have);
+    }
+    float xv[MR][8];
+#pragma unroll
+    for (int m = 0; m < MR; ++m) unpack(x[m], xv[m]);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      float wv[8];
+      unpack(w[t], wv);
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[m * 8 + i] = fmaf(wv[i], xv[m][t], v[m * 8 + i]);
     }
   }
-  Pack<DT, 4> res[1] = {};
-  if (m < g.M && have > 0 && g.residual && g.out_dt != kFP32)
-    res[0] = load_pack<DT, 4>((const elem_t<DT>*)g.residual + m * g.ldr + c, have);
-  finish<DT, 4, 1, false>(g, m, 0, c, have, v, res);
+  // over the wave's lanes of the same columns: the upper half keeps columns
+  // 4 to 7, odd rows of 16 lanes 2 and 3 (6 and 7), then rows turned
+#pragma unroll
+  for (int m = 0; m < MR; ++m) {
+    float h[4], q[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = swap_add32(v[m * 8 + i], v[m * 8 + 4 + i]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      q[i] = swap_add16(h[i], h[2 + i]);
+      if constexpr (kLanes <= 2) q[i] += dpp<kRor2>(q[i]);
+      if constexpr (kLanes <= 4) q[i] += dpp<kRor4>(q[i]);
+      q[i] += dpp<kRor8>(q[i]);
+    }
+    if ((lane & 15) < kLanes) {
+      float* const o = smem + (wave * MR + m) * BN + (lane & 15) * 8 + (lane >> 5) * 4 +
+                       (lane >> 4 & 1) * 2;
+      o[0] = q[0];
+      o[1] = q[1];
+    }
+  }
+  __syncthreads();
+  finish_rows<DT, MR, BN, NW>(g, (const lds_char*)smem, n0);
 }
 
 // The runs' sums added in run order, then the epilogue: four columns a
@@ -951,14 +1041,33 @@ __global__ __launch_bounds__(64) void linear_finish_kernel(LinearArgs g) {
 
 // ------------------------------------------------------------ variants
 // Tile sizes, workgroup shapes and how they are picked: linear_plan.
-enum { kTileBig = 0, kTileMid = 1, kTileSmall = 2, kTileFew = 3, kTileRows = 4, kTiles = 5 };
+enum {
+  kTileBig = 0,
+  kTileMid = 1,
+  kTileSmall = 2,
+  kTileFew = 3,
+  kTileRows = 4,
+  kTileVec = 5,
+  kTiles = 6
+};
 struct TileShape {
   int bm, bn, bk, waves;
   bool pairs;  // a wave holds whole checkpoint blocks
 };
 constexpr TileShape kTileShape[kTiles] = {
     {256, 256, 64, 4, true},  {128, 128, 64, 4, true}, {64, 64, 64, 4, true},
-    {16, 64, 128, 4, false}, {16, 16, 64, 8, true}};
+    {16, 64, 128, 4, false}, {16, 16, 64, 8, true},    {2, 16, 8, 16, true}};
+
+template <int DT, int MR>
+void vec_launch(const LinearArgs& g, hipStream_t s) {
+  const auto grid = [&](int bn) { return (uint32_t)((g.N + bn - 1) / bn); };
+  if (!g.codes && grid(16) <= 256)
+    linear_vec_kernel<DT, MR, 16><<<grid(16), 1024, 0, s>>>(g);
+  else if (grid(32) <= 256)
+    linear_vec_kernel<DT, MR, 32><<<grid(32), 1024, 0, s>>>(g);
+  else
+    linear_vec_kernel<DT, MR, 64><<<grid(64), 1024, 0, s>>>(g);
+}
 
 template <int DT, int LA, int LB>
 hipError_t linear_launch_tile(int tile, bool direct, const LinearArgs& g, hipStream_t s) {
@@ -986,6 +1095,14 @@ hipError_t linear_launch_tile(int tile, bool direct, const LinearArgs& g, hipStr
           linear_rows_kernel<DT, LB, 32><<<dim3((uint32_t)((g.N + 31) / 32)), 512, 0, s>>>(g);
         else
           linear_rows_kernel<DT, LB, 16><<<grid, 512, 0, s>>>(g);
+      }
+      break;
+    case kTileVec:
+      if constexpr (LA == 0 && LB == 1) {
+        if (g.M == 1)
+          vec_launch<DT, 1>(g, s);
+        else
+          vec_launch<DT, 2>(g, s);
       }
       break;
     default:

@@ -265,7 +265,7 @@ struct Plan {
   bool direct, partial, copy_a, copy_b, guard;
 };
 
-// MMAOPS_LINEAR_TILE (0 to 4) and MMAOPS_LINEAR_SPLITS: diagnostic
+// MMAOPS_LINEAR_TILE (0 to 5) and MMAOPS_LINEAR_SPLITS: diagnostic
 // overrides of the choice below, read on every call, so that each variant
 // can be tested on any shape.
 int env_int(const char* name, int lo, int hi) {
@@ -333,12 +333,25 @@ Plan linear_plan(const Product& p, bool saves) {
   // and 6.2; 1 x 8192 x 4096 19.8 and 18.2; 16 x 512 x 8192 13.1 and 9.7)
   const bool rows_fit = p.M <= 16 && p.la == 0 && fa && fb && p.K > 0 && p.K % 64 == 0 &&
                         (p.lb == 0 || p.N % 8 == 0);
+  // One or two rows against rows of the weight, through registers: where
+  // direct loads would need copies of them, while one workgroup for each CU
+  // is enough and K is short (1 x 255 x 2047 9.3 us, with copies 16.5; 1 x
+  // 16383 x 2047 20.5 and 24.3; but 1 x 1023 x 8191 29.5 and 26.3, 1 x 50001
+  // x 128 12.5 and 8.6), but more than the one step that the tile of few rows
+  // needs no second launch for (1 x 16383 x 127: 8.0 and 6.6, z saved 8.2 and
+  // 9.5).
+  const bool vec_fit =
+      p.M <= 2 && p.la == 0 && p.lb == 1 && p.K > 0 && p.N <= (int64_t(1) << 25);
   const int env_tile = env_int("MMAOPS_LINEAR_TILE", 0, kTiles - 1);
   const int env_splits = env_int("MMAOPS_LINEAR_SPLITS", 1, 4096);
   q.tile = kTileFew;
   q.splits = 1;
   q.direct = true;
-  if (env_tile == kTileRows ? rows_fit
+  const bool vec_wins =
+      !(fa && fb) && p.K <= 2048 && (p.K > 128 || saves) && p.N <= 64 * kCUs;
+  if (vec_fit && (env_tile < 0 ? vec_wins : env_tile == kTileVec)) {
+    q.tile = kTileVec;
+  } else if (env_tile == kTileRows ? rows_fit
                             : env_tile < 0 && rows_fit && p.N <= 16 * kCUs &&
                                   p.K <= (p.lb == 0 ? 4096 : 1024)) {
     q.tile = kTileRows;
@@ -372,8 +385,8 @@ Plan linear_plan(const Product& p, bool saves) {
       }
     }
   }
-  q.copy_a = q.direct && !fa;
-  q.copy_b = q.direct && !fb;
+  q.copy_a = q.direct && !fa && q.tile != kTileVec;
+  q.copy_b = q.direct && !fb && q.tile != kTileVec;
   q.guard = q.direct && ((p.la == 1 && p.M % 8 && !q.copy_a) ||
                          (p.lb == 1 && p.N % 8 && !q.copy_b));
   q.partial = q.splits > 1 || (saves && !kTileShape[q.tile].pairs);

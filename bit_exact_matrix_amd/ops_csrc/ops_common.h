@@ -193,7 +193,8 @@ __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(
       __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kRor4 = 0x124, kRor8 = 0x128;
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141;
+constexpr int kRor2 = 0x122, kRor4 = 0x124, kRor8 = 0x128;
 
 // Sum over the 64 lanes of a wave, the same bits in every lane: each step
 // adds two values that both lanes of a pair hold.
@@ -206,6 +207,19 @@ __device__ __forceinline__ float wave_sum(float v) {
   auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
   p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+// a's sums in the lower half and b's in the upper, over the two halves; the
+// same for even and odd rows of 16 lanes.
+__device__ __forceinline__ float swap_add32(float a, float b) {
+  const auto p =
+      __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+__device__ __forceinline__ float swap_add16(float a, float b) {
+  const auto p =
+      __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
   return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 

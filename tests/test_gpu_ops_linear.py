@@ -8,7 +8,7 @@ import ops_reference as ref
 from test_gpu_parity import say, torch_dev  # noqa: F401
 
 pytestmark = pytest.mark.gpu
-TILES = {"big": "0", "mid": "1", "small": "2", "few": "3", "rows": "4"}
+TILES = {"big": "0", "mid": "1", "small": "2", "few": "3", "rows": "4", "vec": "5"}
 ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
 
 
@@ -55,7 +55,7 @@ def check_linear(torch, dev, m, n, k, dtype, layout, act, pad, wide_out=False, s
     assert none is None
 
 
-SHAPES = [(1, 1, 1), (1, 64, 128), (5, 136, 1088), (16, 50, 7), (17, 33, 130), (64, 64, 64), (65, 129, 191),
+SHAPES = [(1, 1, 1), (1, 64, 128), (2, 40, 4200), (2, 8200, 9), (1, 4099, 37), (5, 136, 1088), (16, 50, 7), (17, 33, 130), (64, 64, 64), (65, 129, 191),
           (130, 72, 8), (300, 260, 640), (256, 512, 72), (257, 264, 320)]
 
 
