@@ -55,8 +55,9 @@ def check_linear(torch, dev, m, n, k, dtype, layout, act, pad, wide_out=False, s
     assert none is None
 
 
-SHAPES = [(1, 1, 1), (1, 64, 128), (2, 40, 4200), (2, 8200, 9), (1, 4099, 37), (5, 136, 1088), (16, 50, 7), (17, 33, 130), (64, 64, 64), (65, 129, 191),
-          (130, 72, 8), (300, 260, 640), (256, 512, 72), (257, 264, 320)]
+SHAPES = [(1, 1, 1), (1, 64, 128), (2, 40, 4200), (2, 8200, 9), (1, 4099, 37), (5, 136, 1088),
+          (16, 50, 7), (17, 33, 130), (64, 64, 64), (65, 129, 191), (130, 72, 8), (300, 260, 640),
+          (256, 512, 72), (257, 264, 320)]
 
 
 @pytest.mark.parametrize("tile", TILES)
