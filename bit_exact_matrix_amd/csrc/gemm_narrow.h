@@ -72,10 +72,13 @@ struct alignas(16) NStageA {
 // before the barrier); the waits for the copies are explicit.  The memory
 // clobber keeps LDS accesses on their side of the statement, and the
 // instruction writes no register, so nothing the compiler allocates can
-// change under it while it is in flight.
+// change under it while it is in flight.  The instruction set asks for one
+// wait state between a write of M0 and the load that uses it, which nothing
+// inserts inside an asm block: the s_nop.
 __device__ __forceinline__ void copy16_to_lds(const void* src, uint32_t lds) {
   asm volatile(
       "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
       "global_load_lds_dwordx4 %0, off"
       :
       : "v"(src), "s"(lds)

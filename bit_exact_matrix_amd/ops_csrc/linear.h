@@ -87,9 +87,12 @@ using lds_char = __attribute__((address_space(3))) char;
 // 16 bytes a lane from base + off to LDS at lds + 16 * lane (lds and base
 // wave-uniform).  Written out so that the compiler does not wait for it
 // before every LDS read; the waits are explicit.  It writes no register.
+// The instruction set asks for one wait state between a write of M0 and the
+// load that uses it, which nothing inserts inside an asm block: the s_nop.
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint32_t lds) {
   asm volatile(
       "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
       "global_load_lds_dwordx4 %0, %1"
       :
       : "v"(off), "s"(base), "s"(lds)
