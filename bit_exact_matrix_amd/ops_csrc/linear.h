@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "ops_common.h"
+#include "plan.h"
 
 namespace mmaops {
 
@@ -50,6 +51,7 @@ struct LinearArgs {
   // partial[split][M][N] and linear_finish_kernel does the rest
   int splits;
   int tiles_m, tiles_n;
+  int grid_x;  // few rows: tiles of one z of the grid
   // the last whole step goes through registers too: its last row's last
   // chunk would pass the end of an operand
   int guard;
@@ -571,7 +573,9 @@ template <int DT, int BM, int BN, int BK, int WM, int WN, int LA, int LB, int ST
           bool DIRECT, int WAVES_EU>
 __global__ __launch_bounds__(WM* WN * 64, WAVES_EU) void linear_kernel(LinearArgs g) {
   __shared__ __attribute__((aligned(1024))) char smem[kRingBytes<BM, BN, BK, STAGES>];
-  small_product<DT, BM, BN, BK, WM, WN, LA, LB, STAGES, DIRECT>(g, blockIdx.x, blockIdx.y, smem);
+  const int block = (int)(blockIdx.x + blockIdx.z * (uint32_t)g.grid_x);
+  if (block >= g.tiles_m * g.tiles_n) return;  // the whole workgroup
+  small_product<DT, BM, BN, BK, WM, WN, LA, LB, STAGES, DIRECT>(g, block, blockIdx.y, smem);
 }
 
 // A small backward pass's second launch: the tiles of dz W^T (layouts 0, LB),
@@ -1043,24 +1047,6 @@ __global__ __launch_bounds__(64) void linear_finish_kernel(LinearArgs g) {
 }
 
 // ------------------------------------------------------------ variants
-// Tile sizes, workgroup shapes and how they are picked: linear_plan.
-enum {
-  kTileBig = 0,
-  kTileMid = 1,
-  kTileSmall = 2,
-  kTileFew = 3,
-  kTileRows = 4,
-  kTileVec = 5,
-  kTiles = 6
-};
-struct TileShape {
-  int bm, bn, bk, waves;
-  bool pairs;  // a wave holds whole checkpoint blocks
-};
-constexpr TileShape kTileShape[kTiles] = {
-    {256, 256, 64, 4, true},  {128, 128, 64, 4, true}, {64, 64, 64, 4, true},
-    {16, 64, 128, 4, false}, {16, 16, 64, 8, true},    {2, 16, 8, 16, true}};
-
 template <int DT, int MR>
 void vec_launch(const LinearArgs& g, hipStream_t s) {
   const auto grid = [&](int bn) { return (uint32_t)((g.N + bn - 1) / bn); };
@@ -1097,7 +1083,7 @@ hipError_t linear_launch_tile(int tile, bool direct, const LinearArgs& g, hipStr
         if (g.codes)
           linear_rows_kernel<DT, LB, 32><<<dim3((uint32_t)((g.N + 31) / 32)), 512, 0, s>>>(g);
         else
-          linear_rows_kernel<DT, LB, 16><<<grid, 512, 0, s>>>(g);
+          linear_rows_kernel<DT, LB, 16><<<dim3((uint32_t)((g.N + 15) / 16)), 512, 0, s>>>(g);
       }
       break;
     case kTileVec:
@@ -1108,11 +1094,17 @@ hipError_t linear_launch_tile(int tile, bool direct, const LinearArgs& g, hipStr
           vec_launch<DT, 2>(g, s);
       }
       break;
-    default:
+    default: {
+      // a grid has fewer than 2^32 lanes in x
+      constexpr uint32_t kMost = 1u << 23;
+      LinearArgs f = g;
+      f.grid_x = (int)(grid.x < kMost ? grid.x : kMost);
+      const dim3 few((uint32_t)f.grid_x, grid.y, (grid.x + kMost - 1) / kMost);
       if (direct)
-        linear_kernel<DT, 16, 64, 128, 1, 4, LA, LB, 3, true, 2><<<grid, 256, 0, s>>>(g);
+        linear_kernel<DT, 16, 64, 128, 1, 4, LA, LB, 3, true, 2><<<few, 256, 0, s>>>(f);
       else
-        linear_kernel<DT, 16, 64, 128, 1, 4, LA, LB, 2, false, 2><<<grid, 256, 0, s>>>(g);
+        linear_kernel<DT, 16, 64, 128, 1, 4, LA, LB, 2, false, 2><<<few, 256, 0, s>>>(f);
+    }
   }
   return hipGetLastError();
 }

@@ -2,12 +2,12 @@
 // argument checks, the choice of kernels, and the layer norm, checkpoint
 // and activation-gradient kernels.
 #include <stdio.h>
-#include <stdlib.h>
 #include <string.h>
 
 #include "../../include/mmaops.h"
 #include "linear.h"
 #include "norm.h"
+#include "plan.h"
 #include "saved.h"
 
 using namespace mmaops;
@@ -17,8 +17,6 @@ namespace {
 static_assert(kFP16 == MMAEMU_DTYPE_FP16 && kBF16 == MMAEMU_DTYPE_BF16 &&
                   kFP32 == MMAOPS_DTYPE_FP32,
               "the kernels' type numbers are the ABI's");
-
-constexpr int kCUs = 256;
 
 thread_local char g_hip_error[256] = "no HIP error recorded";
 
@@ -70,8 +68,6 @@ struct Views {
   }
 };
 
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
 // rows x cols of elements with leading dimension ld: sizes that 64-bit byte
 // offsets, the kernels' 32-bit column counters and a grid of fewer than 2^32
 // lanes (16 for each column, of the column sums) hold
@@ -88,7 +84,6 @@ bool any_type(int dt) { return dt == kFP16 || dt == kBF16 || dt == kFP32; }
 bool half_type(int dt) { return dt == kFP16 || dt == kBF16; }
 
 int64_t scale_cols(int64_t cols) { return (cols + kBlock - 1) / kBlock; }
-int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // ------------------------------------------------------------ layer norm
 // How a row is held: lanes a row, vectors a lane, rows a workgroup.
@@ -248,170 +243,6 @@ hipError_t restore_to(int dt, const uint8_t* codes, const uint8_t* scales, void*
 }
 
 // ---------------------------------------------------------------- products
-// A product C (M x N) = A B with inner size K, its operands' layouts and
-// how it is run.
-struct Product {
-  int64_t M, N, K;
-  int la, lb;
-  const void *a, *b;
-  int64_t lda, ldb;
-};
-
-// direct: direct loads from both operands.  What they cannot be loaded from
-// directly is copied to aligned rows first (copy_a, copy_b); for few rows,
-// where that reads the weight twice, the tile may go through registers.
-struct Plan {
-  int tile, splits;
-  bool direct, partial, copy_a, copy_b, guard;
-};
-
-// MMAOPS_LINEAR_TILE (0 to 5) and MMAOPS_LINEAR_SPLITS: diagnostic
-// overrides of the choice below, read on every call, so that each variant
-// can be tested on any shape.
-int env_int(const char* name, int lo, int hi) {
-  const char* v = getenv(name);
-  if (!v || !*v) return -1;
-  char* end = nullptr;
-  const long x = strtol(v, &end, 10);
-  return end && *end == '\0' && x >= lo && x <= hi ? (int)x : -1;
-}
-
-// An estimate of a product's time on one MI355X, in us: `n` workgroups of a
-// tile, each `steps` long.  Fitted to times on the GPU from 33 x 4096 x 4096
-// to 2048 x 4096 x 4096, 64 x 1024 x 1024 to 8192 x 256 x 1024 and 256 x
-// 256 x 65536 (bf16, X W).  What the tiles take there, each side measured:
-//   512 x 4096 x 4096    small 31  mid 33  big 77
-//   1024 x 4096 x 4096   small 57  mid 35  big 79
-//   2048 x 4096 x 4096   small 106 mid 59  big 86
-//   4096 x 4096 x 1024             mid 38  big 36
-//   64 x 1024 x 1024     few 6.4   small 8.5
-//   512 x 512 x 8192     small 36, its inner size split in four 19
-double tile_time(int tile, int64_t n, int64_t steps) {
-  const int64_t full = (n + kCUs - 1) / kCUs;  // workgroups of the fullest CU
-  const double even = (double)n / kCUs;
-  switch (tile) {
-    case kTileBig: return 8.0 + steps * 1.45 * full;
-    case kTileMid: return 4.6 + steps * (full / 2 * 0.86 + full % 2 * 0.47);
-    case kTileSmall: return 4.6 + steps * (even > 1.3 ? even * 0.2 : 0.26);
-    default: return 4.5 + steps * (full > 1 ? full * 0.24 : 0.3);
-  }
-}
-
-// The tile of few rows through registers: a step waits for its loads, until
-// several workgroups share a CU (6 x 2135 x 132, W stored N x K: 33 us in 17
-// steps; copied to aligned rows and loaded directly, 12).
-double few_through_registers_time(int64_t n, int64_t steps) {
-  const double even = (double)n / kCUs;
-  return 4.5 + steps * (even > 3.6 ? even * 0.5 : 1.8);
-}
-
-// an operand of `elements` copied to aligned rows: a launch, read and written
-double copy_time(int64_t elements) { return 3.0 + (double)elements * 4 / 5e6; }
-
-// the second kernel of a split product: its launch, and the partial sums
-// written and read
-double join_time(int64_t M, int64_t N, int64_t splits) {
-  return 4.5 + (double)M * N * splits * 8 / 5e6;
-}
-
-Plan linear_plan(const Product& p, bool saves) {
-  Plan q;
-  // direct loads take 16-byte pieces: rows that start on 16 bytes, and
-  // 32-bit offsets within a tile
-  auto fits = [](const void* a, int64_t ld) {
-    return aligned(a, 16) && ld % 8 == 0 && ld <= (int64_t(1) << 22);
-  };
-  const bool fa = fits(p.a, p.lda), fb = fits(p.b, p.ldb);
-  auto tiles = [&](int t) {
-    const TileShape& s = kTileShape[t];
-    return ((p.M + s.bm - 1) / s.bm) * ((p.N + s.bn - 1) / s.bn);
-  };
-  // all of K in one workgroup: whole steps, from direct loads that need no
-  // guard, one workgroup for each CU at most, while K is short enough (bf16,
-  // weights from memory, rows against few: 1 x 4096 x 4096 W stored N x K
-  // 10.5 us and 12.4, K x N 18.9 and 14.0; 1 x 4096 x 1024 4.9 and 5.8, 5.8
-  // and 6.2; 1 x 8192 x 4096 19.8 and 18.2; 16 x 512 x 8192 13.1 and 9.7)
-  const bool rows_fit = p.M <= 16 && p.la == 0 && fa && fb && p.K > 0 && p.K % 64 == 0 &&
-                        (p.lb == 0 || p.N % 8 == 0);
-  // One or two rows against rows of the weight, through registers: where
-  // direct loads would need copies of them, while one workgroup for each CU
-  // is enough and K is short (1 x 255 x 2047 9.3 us, with copies 16.5; 1 x
-  // 16383 x 2047 20.5 and 24.3; but 1 x 1023 x 8191 29.5 and 26.3, 1 x 50001
-  // x 128 12.5 and 8.6), but more than the one step that the tile of few rows
-  // needs no second launch for (1 x 16383 x 127: 8.0 and 6.6, z saved 8.2 and
-  // 9.5).
-  const bool vec_fit =
-      p.M <= 2 && p.la == 0 && p.lb == 1 && p.K > 0 && p.N <= (int64_t(1) << 25);
-  const int env_tile = env_int("MMAOPS_LINEAR_TILE", 0, kTiles - 1);
-  const int env_splits = env_int("MMAOPS_LINEAR_SPLITS", 1, 4096);
-  q.tile = kTileFew;
-  q.splits = 1;
-  q.direct = true;
-  const bool vec_wins =
-      !(fa && fb) && p.K <= 2048 && (p.K > 128 || saves) && p.N <= 64 * kCUs;
-  if (vec_fit && (env_tile < 0 ? vec_wins : env_tile == kTileVec)) {
-    q.tile = kTileVec;
-  } else if (env_tile == kTileRows ? rows_fit
-                            : env_tile < 0 && rows_fit && p.N <= 16 * kCUs &&
-                                  p.K <= (p.lb == 0 ? 4096 : 1024)) {
-    q.tile = kTileRows;
-  } else {
-    double best = 1e300;
-    const double copies = (fa ? 0.0 : copy_time(p.M * p.K)) + (fb ? 0.0 : copy_time(p.N * p.K));
-    for (int v = 0; v <= kTileFew + 1; ++v) {  // the last: few rows through registers
-      const int t = v < kTileFew ? v : kTileFew;
-      const bool direct = v <= kTileFew;
-      if (env_tile >= 0 ? t != (env_tile < kTileFew ? env_tile : kTileFew)
-                        : t == kTileFew ? p.M > 128 : p.M <= 16)
-        continue;
-      if (!direct && fa && fb) continue;
-      const int64_t steps = (p.K + kTileShape[t].bk - 1) / kTileShape[t].bk, n = tiles(t);
-      if (t != kTileBig && env_tile < 0 && n * kTileShape[t].waves * 64 > UINT32_MAX)
-        continue;  // more lanes than a grid has
-      for (int s = 1; s <= 32; s += s < 4 ? 1 : s / 2) {
-        const int k = env_splits >= 0 ? (int)(env_splits < steps ? env_splits : steps) : s;
-        if (env_splits < 0 && s > 1 && steps / s < (direct ? 4 : 1)) break;
-        const int64_t run = (steps + s - 1) / s;
-        const double time = (direct ? tile_time(t, n * s, run) + copies
-                                    : few_through_registers_time(n * s, run)) +
-                            (s > 1 ? join_time(p.M, p.N, s) : 0.0);
-        if (time < best) {
-          best = time;
-          q.tile = t;
-          q.direct = direct;
-          q.splits = k < 1 ? 1 : k;
-        }
-        if (env_splits >= 0) break;
-      }
-    }
-  }
-  q.copy_a = q.direct && !fa && q.tile != kTileVec;
-  q.copy_b = q.direct && !fb && q.tile != kTileVec;
-  q.guard = q.direct && ((p.la == 1 && p.M % 8 && !q.copy_a) ||
-                         (p.lb == 1 && p.N % 8 && !q.copy_b));
-  q.partial = q.splits > 1 || (saves && !kTileShape[q.tile].pairs);
-  return q;
-}
-
-// Rows and row length of an operand as it is stored.
-struct Stored {
-  int64_t rows, cols, ld;  // ld: of its aligned copy
-};
-Stored stored(int layout, int64_t len, int64_t K) {
-  const int64_t rows = layout == 0 ? len : K, cols = layout == 0 ? K : len;
-  return {rows, cols, (cols + 7) / 8 * 8};
-}
-
-// What a product takes of the workspace: the partial sums, then the copies.
-int64_t partial_bytes(const Product& p, const Plan& q) {
-  return q.partial ? up256(p.M * p.N * q.splits * 4) : 0;
-}
-int64_t copy_bytes(bool copy, const Stored& t) { return copy ? up256(t.rows * t.ld * 2) : 0; }
-int64_t product_bytes(const Product& p, const Plan& q) {
-  return partial_bytes(p, q) + copy_bytes(q.copy_a, stored(p.la, p.M, p.K)) +
-         copy_bytes(q.copy_b, stored(p.lb, p.N, p.K));
-}
-
 // x (16-bit elements) to rows of t.ld elements at y
 hipError_t align_rows(const void* x, int64_t ldx, void* y, const Stored& t, hipStream_t s) {
   if (t.rows == 0 || t.cols == 0) return hipSuccess;

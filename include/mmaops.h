@@ -52,8 +52,8 @@
  *   aligned, contents undefined, free again once the stream has run the
  *   call), of at least the size that its ..._workspace function returns
  *   for the same sizes, or for a product the same arguments (an operand
- *   whose rows do not start on 16 bytes is copied to the workspace for
- *   some shapes).  A smaller one is MMAEMU_ERR_SCRATCH.  Calls can
+ *   whose rows do not start on 16 bytes, or lie too far apart, is copied
+ *   to the workspace for some shapes).  A smaller one is MMAEMU_ERR_SCRATCH.  Calls can
  *   so be captured into a graph, and need no synchronisation.
  *
  * TYPES
