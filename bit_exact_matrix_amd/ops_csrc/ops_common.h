@@ -440,9 +440,11 @@ __device__ __forceinline__ void decode(const Codes<V>& c, int scale, float (&v)[
 
 // The codes of V consecutive elements held by each lane, where 32 / V
 // neighbouring lanes hold a block, from the lane's largest magnitude pattern
-// (FP32 bits of |v|).  Returns the block's scale, the same in its lanes.
+// (FP32 bits of |v|).  Elements from n on are not the block's: what they hold
+// (a product's tile has sums there) does not count.  Returns the block's
+// scale, the same in its lanes.
 template <int DT, int V>
-__device__ __forceinline__ int encode_with(float (&v)[V], uint32_t mag, Codes<V>& c) {
+__device__ __forceinline__ int encode_with(float (&v)[V], uint32_t mag, int n, Codes<V>& c) {
   constexpr uint32_t limit = save_limit(DT);
   mag = lanes_max<kBlock / V>(mag);
   if (mag > limit) {
@@ -455,7 +457,7 @@ __device__ __forceinline__ int encode_with(float (&v)[V], uint32_t mag, Codes<V>
     for (int i = 0; i < V; ++i) {
       const uint32_t u = __float_as_uint(v[i]), m = u & 0x7FFFFFFFu;
       const uint32_t t = m < 0x7F800000u ? (m < limit ? m : limit) : 0u;
-      mag = t > mag ? t : mag;
+      mag = t > mag && i < n ? t : mag;
       v[i] = __uint_as_float(m < 0x7F800000u ? (u & 0x80000000u) | t : 0x7FC00000u);
     }
     mag = lanes_max<kBlock / V>(mag);
@@ -478,7 +480,7 @@ __device__ __forceinline__ int encode(float (&v)[V], int n, Codes<V>& c) {
     const uint32_t m = i < n ? __float_as_uint(v[i]) & 0x7FFFFFFFu : 0u;
     mag = m > mag ? m : mag;
   }
-  return encode_with<DT, V>(v, mag, c);
+  return encode_with<DT, V>(v, mag, n, c);
 }
 
 // of elements as they are in memory (0 where there are none)
@@ -503,7 +505,7 @@ __device__ __forceinline__ int encode(const Pack<DT, V>& q, Codes<V>& c) {
   }
   float v[V];
   unpack(q, v);
-  return encode_with<DT, V>(v, mag, c);
+  return encode_with<DT, V>(v, mag, V, c);
 }
 
 }  // namespace mmaops
