@@ -919,9 +919,9 @@ __global__ __launch_bounds__(512, 2) void linear_rows_kernel(LinearArgs g) {
 
 // One or two rows against a weight stored K x N whose rows direct loads
 // cannot take (odd lengths): in one launch, through registers.  A lane has 8
-// columns of 8 consecutive rows of the weight, all on their way at once (128
-// KB a workgroup), and its own sums of MR x 8 products.  The lanes' sums meet
-// by swaps, the waves' in LDS in wave order.  A row's piece of 32 bytes costs
+// columns of 8 consecutive rows of the weight, all on their way at once (up
+// to 128 KB a workgroup), and its own sums of MR x 8 products.  The lanes' sums
+// meet by swaps, the waves' in LDS in wave order.  A row's piece of 32 bytes costs
 // a CU about 4 cycles and one of 128 bytes 5, so BN = 16 columns only while
 // that gives each CU one workgroup, then 32, then 64 (1 x 4097 x 4096: 18.9,
 // 15.2 and 23.2 us; 1 x 11009 x 4095: 39.9, 33.5 and 25.6).  One row, bf16,
@@ -929,23 +929,28 @@ __global__ __launch_bounds__(512, 2) void linear_rows_kernel(LinearArgs g) {
 // registers: N x K 1499 x 1023 8.7 us and 13.7, 2135 x 132 5.4 and 7.3, 4097
 // x 4096 15.2 and 21.6.  Aligned weights: 4096 x 4096 14.8 here, 13.0 with K
 // split over workgroups.  Four rows: more products and sums than registers,
-// 11.7 and 14.0, 22.0 and 25.2, but 42 and 32 at 11009 x 4095.
-template <int DT, int MR, int BN>
-__global__ __launch_bounds__(1024) void linear_vec_kernel(LinearArgs g) {
-  constexpr int NW = 16, kLanes = BN / 8, kAtOnce = NW * 64 / kLanes;  // runs of 8 rows
-  __shared__ __attribute__((aligned(16))) float smem[NW * MR * BN];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// 11.7 and 14.0, 22.0 and 25.2, but 42 and 32 at 11009 x 4095.  The order of
+// the sums goes with BN, so where z is saved as blocks of 32 columns a
+// workgroup holds two times 16 (PARTS, of NW waves each), and the output's
+// bits are those of a call that saves nothing.
+template <int DT, int MR, int BN, int PARTS, int NW>
+__global__ __launch_bounds__(PARTS* NW * 64) void linear_vec_kernel(LinearArgs g) {
+  constexpr int kLanes = BN / 8, kAtOnce = NW * 64 / kLanes;  // runs of 8 rows
+  constexpr int kCols = BN * PARTS;
+  __shared__ __attribute__((aligned(16))) float smem[NW * MR * kCols];
+  const int lane = threadIdx.x & 63;
+  const int part = (threadIdx.x >> 6) / NW, wave = (threadIdx.x >> 6) % NW;
   int tm, tn;
   tile_of(1, (int)gridDim.x, blockIdx.x, tm, tn);
-  const int64_t n0 = (int64_t)tn * BN;
-  const int64_t c = n0 + (lane % kLanes) * 8;
+  const int64_t n0 = (int64_t)tn * kCols;
+  const elem_t<DT>* const a = (const elem_t<DT>*)g.a;
+  const int64_t c = n0 + part * BN + (lane % kLanes) * 8;
   const int n = g.N - c < 8 ? (int)(g.N - c) : 8;
   const elem_t<DT>* const b = (const elem_t<DT>*)g.b + c;
-  const elem_t<DT>* const a = (const elem_t<DT>*)g.a;
   float v[MR * 8];
 #pragma unroll
   for (int i = 0; i < MR * 8; ++i) v[i] = 0.0f;
-  for (int64_t k = (int64_t)(threadIdx.x / kLanes) * 8; k < g.K; k += kAtOnce * 8) {
+  for (int64_t k = (int64_t)((wave * 64 + lane) / kLanes) * 8; k < g.K; k += kAtOnce * 8) {
     const int have = g.K - k < 8 ? (int)(g.K - k) : 8;
     Pack<DT, 8> w[8], x[MR];
     if (n == 8 && have == 8) {
@@ -987,14 +992,14 @@ __global__ __launch_bounds__(1024) void linear_vec_kernel(LinearArgs g) {
       q[i] += dpp<kRor8>(q[i]);
     }
     if ((lane & 15) < kLanes) {
-      float* const o = smem + (wave * MR + m) * BN + (lane & 15) * 8 + (lane >> 5) * 4 +
-                       (lane >> 4 & 1) * 2;
+      float* const o = smem + (wave * MR + m) * kCols + part * BN + (lane & 15) * 8 +
+                       (lane >> 5) * 4 + (lane >> 4 & 1) * 2;
       o[0] = q[0];
       o[1] = q[1];
     }
   }
   __syncthreads();
-  finish_rows<DT, MR, BN, NW>(g, (const lds_char*)smem, n0);
+  finish_rows<DT, MR, kCols, NW>(g, (const lds_char*)smem, n0);
 }
 
 // The runs' sums added in run order, then the epilogue: four columns a
@@ -1050,12 +1055,16 @@ __global__ __launch_bounds__(64) void linear_finish_kernel(LinearArgs g) {
 template <int DT, int MR>
 void vec_launch(const LinearArgs& g, hipStream_t s) {
   const auto grid = [&](int bn) { return (uint32_t)((g.N + bn - 1) / bn); };
-  if (!g.codes && grid(16) <= 256)
-    linear_vec_kernel<DT, MR, 16><<<grid(16), 1024, 0, s>>>(g);
-  else if (grid(32) <= 256)
-    linear_vec_kernel<DT, MR, 32><<<grid(32), 1024, 0, s>>>(g);
-  else
-    linear_vec_kernel<DT, MR, 64><<<grid(64), 1024, 0, s>>>(g);
+  if (grid(16) > 256) {
+    if (grid(32) <= 256)
+      linear_vec_kernel<DT, MR, 32, 1, 16><<<grid(32), 1024, 0, s>>>(g);
+    else
+      linear_vec_kernel<DT, MR, 64, 1, 16><<<grid(64), 1024, 0, s>>>(g);
+  } else if (g.codes) {
+    linear_vec_kernel<DT, MR, 16, 2, 8><<<grid(32), 1024, 0, s>>>(g);
+  } else {
+    linear_vec_kernel<DT, MR, 16, 1, 8><<<grid(16), 512, 0, s>>>(g);
+  }
 }
 
 template <int DT, int LA, int LB>

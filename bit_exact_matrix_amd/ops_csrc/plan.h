@@ -152,8 +152,9 @@ inline Plan linear_plan(const Product& p, bool saves) {
   // is enough and K is short (1 x 255 x 2047 9.3 us, with copies 16.5; 1 x
   // 16383 x 2047 20.5 and 24.3; but 1 x 1023 x 8191 29.5 and 26.3, 1 x 50001
   // x 128 12.5 and 8.6), but more than the one step that the tile of few rows
-  // needs no second launch for (1 x 16383 x 127: 8.0 and 6.6, z saved 8.2 and
-  // 9.5).
+  // needs no second launch for (1 x 16383 x 127: 8.0 and 6.6; with z saved it
+  // needs one, 8.2 and 9.5, but what is saved does not choose the order of
+  // the sums).
   const bool vec_fit =
       p.M <= 2 && p.la == 0 && p.lb == 1 && p.K > 0 && p.N <= (int64_t(1) << 25);
   const int env_tile = env_int("MMAOPS_LINEAR_TILE", 0, kTiles - 1);
@@ -163,7 +164,7 @@ inline Plan linear_plan(const Product& p, bool saves) {
   q.direct = true;
   q.copy_a = q.copy_b = false;
   const bool few_as_is = load_a(kTileFew) == kAsItIs && load_b(kTileFew) == kAsItIs;
-  const bool vec_wins = !few_as_is && p.K <= 2048 && (p.K > 128 || saves) && p.N <= 64 * kCUs;
+  const bool vec_wins = !few_as_is && p.K <= 2048 && p.K > 128 && p.N <= 64 * kCUs;
   if (vec_fit && (env_tile < 0 ? vec_wins : env_tile == kTileVec)) {
     q.tile = kTileVec;
   } else if (env_tile == kTileRows ? rows_fit

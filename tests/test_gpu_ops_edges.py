@@ -1,15 +1,22 @@
 """Edges of the native operators: blocks of a checkpoint that end inside the
-matrix and hold values that are not finite."""
+matrix and hold values that are not finite, results beside other outputs."""
 import math
 
 import pytest
 
 import bit_exact_matrix_amd as mm
 import ops_reference as ref
-from test_gpu_ops_linear import TILES
+from test_gpu_ops_linear import TILES, matrix, operands
 from test_gpu_parity import say, torch_dev  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+def bits(t):
+    """The words of a tensor, so that signed zeros and NaN compare too."""
+    import torch
+    size = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()]
+    return t.contiguous().view(size)
 
 
 # ------------------------------------------------------- ragged blocks
@@ -50,3 +57,31 @@ def test_checkpoint_of_a_ragged_block_with_special_values(torch_dev, monkeypatch
             got = ck.codes.double()
             assert torch.equal(torch.isnan(got), torch.isnan(codes))
             assert torch.equal(got.nan_to_num(0), codes.nan_to_num(0)), (m, n, k, special)
+
+
+# --------------------------------------- the same bits beside other outputs
+@pytest.mark.parametrize("tile", [None, *TILES])
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+def test_outputs_do_not_depend_on_what_is_kept(torch_dev, monkeypatch, tile, layout):
+    """y of a forward pass that keeps z is that of one that does not, so
+    that a pass and its recomputation compare word for word."""
+    torch, dev = torch_dev
+    if tile:
+        monkeypatch.setenv("MMAOPS_LINEAR_TILE", TILES[tile])
+    shapes = [(1, 64, 96), (1, 255, 100), (2, 1499, 127), (1, 1499, 1023), (2, 4097, 300),
+              (2, 9000, 200), (1, 255, 2047), (16, 264, 512), (7, 96, 1024), (33, 96, 2048),
+              (130, 260, 200), (300, 1000, 264)]
+    for i, (m, n, k) in enumerate(shapes):
+        for pad in (0, 3):
+            dtype = torch.bfloat16 if i % 2 else torch.float16
+            x, w = operands(torch, dev, m, n, k, dtype, layout, i, pad)
+            bias = torch.randn(n, device=dev)
+            res = matrix(torch, dev, m, n, dtype, i + 7, pad)
+            say("linear beside z", tile, layout, m, n, k, pad)
+            for act in ("none", "silu"):
+                a = dict(activation=act, residual=res)
+                y, _ = mm.linear(x, w, bias, **a)
+                whole, z = mm.linear(x, w, bias, keep="full", **a)
+                saved, ck = mm.linear(x, w, bias, keep="checkpoint", **a)
+                assert torch.equal(bits(y), bits(whole)), (m, n, k, pad, act)
+                assert torch.equal(bits(y), bits(saved)), (m, n, k, pad, act)
