@@ -602,21 +602,32 @@ __global__ __launch_bounds__(256, 2) void linear_pair_kernel(PairArgs p) {
   } else if (b < n1 + n2) {
     small_product<DT, 64, 64, 64, 2, 2, 1, 1, 3, true>(p.dw, b - n1, 0, smem);
   } else {
-    float(&meet)[4][64] = *(float(*)[4][64])smem;
+    // in the runs and the order of column_sum_kernel, for the same bits
+    float(&meet)[16][64] = *(float(*)[16][64])smem;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t c = (int64_t)(b - n1 - n2) * 64 + lane;
-    const int run = (p.count + 3) / 4, q0 = wave * run;
-    const int q1 = q0 + run < p.count ? q0 + run : p.count;
-    float s = 0.0f;
+    const int run = (p.count + 15) / 16;
+    // four of the sixteen runs a wave, side by side; past a run's end + 0
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c < p.cols) {
-#pragma unroll 16
-      for (int q = q0; q < q1; ++q) s += p.partial[q * p.cols + c];
+#pragma unroll 4
+      for (int q = 0; q < run; ++q) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = (wave * 4 + i) * run + q;
+          s[i] += row < p.count ? p.partial[row * p.cols + c] : 0.0f;
+        }
+      }
     }
-    meet[wave][lane] = s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) meet[wave * 4 + i][lane] = s[i];
     __syncthreads();
-    if (wave == 0 && c < p.cols)
-      store_any(p.dbias, c, ((meet[0][lane] + meet[1][lane]) + meet[2][lane]) + meet[3][lane],
-                p.dbias_dt);
+    if (wave == 0 && c < p.cols) {
+      float sum = meet[0][lane];
+#pragma unroll
+      for (int r = 1; r < 16; ++r) sum += meet[r][lane];
+      store_any(p.dbias, c, sum, p.dbias_dt);
+    }
   }
 }
 

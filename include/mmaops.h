@@ -7,9 +7,13 @@
  * arithmetic (FP32 sums, one rounding of each output): the layer norm
  * before a product, the product with its epilogue, the 8-bit checkpoints
  * that a forward pass leaves, and the backward passes that use them.  The
- * same call on the same inputs gives the same bits, so a forward pass and
- * its recomputation can be compared word for word (AEGIS, "Redundancy
- * already exists in the training computation").
+ * same call on the same inputs gives the same bits, and an output's bits do
+ * not depend on which others are asked for, so a forward pass and its
+ * recomputation can be compared word for word (AEGIS, "Redundancy already
+ * exists in the training computation").  The order of a product's sums, and
+ * so the last bits, goes with the sizes (M too: a row's result beside other
+ * rows is not that of the row alone), the weight's layout, and with whether
+ * the operands' rows start on 16 bytes and how far apart they are.
  *
  * OPERATORS
  *   mma_layer_norm            for each row: mu = mean(x),

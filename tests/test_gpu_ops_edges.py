@@ -85,3 +85,19 @@ def test_outputs_do_not_depend_on_what_is_kept(torch_dev, monkeypatch, tile, lay
                 saved, ck = mm.linear(x, w, bias, keep="checkpoint", **a)
                 assert torch.equal(bits(y), bits(whole)), (m, n, k, pad, act)
                 assert torch.equal(bits(y), bits(saved)), (m, n, k, pad, act)
+
+
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+def test_bias_gradient_does_not_depend_on_the_other_gradients(torch_dev, layout):
+    torch, dev = torch_dev
+    for i, (m, n, k) in enumerate([(17, 24, 40), (299, 260, 640), (1000, 65, 129),
+                                   (512, 512, 512), (2100, 520, 264)]):
+        x, w = operands(torch, dev, m, n, k, torch.bfloat16, layout, i, 0)
+        dy = matrix(torch, dev, m, n, torch.bfloat16, i + 3)
+        z = matrix(torch, dev, m, n, torch.bfloat16, i + 4)
+        say("bias gradient beside others", layout, m, n, k)
+        runs = [mm.linear_backward(dy, x, w, z, activation="silu", need_dx=dx, need_dw=dw,
+                                   bias_dtype=torch.float32)[2]
+                for dx in (True, False) for dw in (True, False)]
+        for other in runs[1:]:
+            assert torch.equal(bits(runs[0]), bits(other)), (m, n, k)
