@@ -299,6 +299,13 @@ __device__ __forceinline__ float act_apply(float z, int act) {
   }
 }
 
+// z within [-top, top], where what it is multiplied with is 0 beyond: an
+// infinity (a pre-activation past its 16-bit type's range) must not become
+// NaN there.  NaN comes through the other factor.
+__device__ __forceinline__ float bounded(float z, float top) {
+  return __builtin_amdgcn_fmed3f(z, -top, top);
+}
+
 // d act / d z
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
@@ -306,7 +313,7 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     case kActGelu: {
       float e;
       const float q = normal_tail(__builtin_fabsf(z), e);
-      return __builtin_fmaf(z * e, kInvSqrt2Pi, z > 0.0f ? 1.0f - q : q);
+      return __builtin_fmaf(bounded(z, 30.0f) * e, kInvSqrt2Pi, z > 0.0f ? 1.0f - q : q);
     }
     case kActGeluTanh: {
       // 0 or 1 beyond 12, where the product of a zero and a large power
@@ -318,7 +325,7 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     }
     case kActSilu: {
       const float s = logistic(z);
-      return s * (1.0f + z * (1.0f - s));
+      return s * (1.0f + bounded(z, 100.0f) * (1.0f - s));
     }
     default: return 1.0f;
   }

@@ -150,7 +150,8 @@ int64_t mma_linear_workspace(const mma_linear_args *args);
  * X and Z: matrices or checkpoints; neither Z nor its checkpoint is read
  * where activation is NONE.  dX, dW, dbias: any of them NULL to leave it
  * out.  dz enters the two products rounded to dtype; dbias sums it before
- * that rounding. */
+ * that rounding.  Where a kept Z is infinite (past the range of its 16 bits)
+ * act' is its limit, 0 or 1. */
 typedef struct {
   int32_t dtype;        /* of dY, X, W, Z and dX */
   int32_t dw_dtype;     /* of dW: dtype or FP32 */

@@ -1,12 +1,13 @@
 """Edges of the native operators: blocks of a checkpoint that end inside the
-matrix and hold values that are not finite, results beside other outputs."""
+matrix and hold values that are not finite, results beside other outputs,
+activations at infinity."""
 import math
 
 import pytest
 
 import bit_exact_matrix_amd as mm
 import ops_reference as ref
-from test_gpu_ops_linear import TILES, matrix, operands
+from test_gpu_ops_linear import ACTS, TILES, matrix, operands
 from test_gpu_parity import say, torch_dev  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -101,3 +102,28 @@ def test_bias_gradient_does_not_depend_on_the_other_gradients(torch_dev, layout)
                 for dx in (True, False) for dw in (True, False)]
         for other in runs[1:]:
             assert torch.equal(bits(runs[0]), bits(other)), (m, n, k)
+
+
+# ------------------------------------------------------------ activations
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_slopes_at_infinity(torch_dev, dt):
+    """The slopes' limits, 0 and 1: a forward pass in 16 bits keeps a
+    pre-activation past its type's range as an infinity."""
+    torch, dev = torch_dev
+    dtype = torch.float16 if dt == "fp16" else torch.bfloat16
+    z = torch.tensor([[-math.inf, math.inf, math.nan]], device=dev).to(dtype)
+    dy, x = torch.ones_like(z), torch.ones((1, 1), dtype=dtype, device=dev)
+    for act in ACTS[1:]:
+        say("slopes at infinity", dt, act)
+        dx, _, db = mm.linear_backward(dy, x, torch.ones_like(z), z, activation=act,
+                                       bias_dtype=torch.float32)
+        assert db[:2].tolist() == [0.0, 1.0], act
+        assert act == "relu" or math.isnan(float(db[2])), act
+    big = torch.full((3, 64), 3e4, dtype=torch.float16, device=dev)
+    w = torch.ones((64, 40), dtype=torch.float16, device=dev)
+    w[:, ::2] = -1
+    for act in ACTS[1:]:
+        _, z = mm.linear(big, w, activation=act, keep="full")
+        assert torch.isinf(z).all()
+        _, _, db = mm.linear_backward(torch.ones_like(z), big, w, z, activation=act)
+        assert (db[::2] == 0).all() and (db[1::2] == 3).all(), act
