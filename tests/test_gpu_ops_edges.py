@@ -1,6 +1,6 @@
 """Edges of the native operators: blocks of a checkpoint that end inside the
 matrix and hold values that are not finite, results beside other outputs,
-activations at infinity."""
+activations at infinity and to the last bits of float32."""
 import math
 
 import pytest
@@ -127,3 +127,45 @@ def test_slopes_at_infinity(torch_dev, dt):
         assert torch.isinf(z).all()
         _, _, db = mm.linear_backward(torch.ones_like(z), big, w, z, activation=act)
         assert (db[::2] == 0).all() and (db[1::2] == 3).all(), act
+
+
+def every_half(torch, dev, top):
+    """Every float16 number of magnitude up to top, as a row."""
+    v = torch.arange(65536, dtype=torch.int32, device=dev).to(torch.int16).view(torch.float16)
+    return v[v.abs() <= top].reshape(1, -1)
+
+
+def test_gelu_to_float32(torch_dev):
+    """gelu(z) = max(z, 0) - |z| Q(|z|) with the normal tail Q as 2 to the
+    power of its logarithm, which is held in float32 and grows as z^2 / 2: a
+    few roundings of it (6 with the power's and the sum's) are a relative
+    error of 6 U (1 + z^2 / 2), of the result's magnitude where z < 0 and
+    less of it elsewhere.  An approximation to 1.5e-7 of 1 exceeds it."""
+    torch, dev = torch_dev
+    z = every_half(torch, dev, 6.0).t().contiguous()
+    one = torch.ones((1, 1), dtype=torch.float16, device=dev)
+    say("gelu to float32")
+    y, kept = mm.linear(z, one, activation="gelu", keep="full", out_dtype=torch.float32)
+    assert torch.equal(kept, z)
+    want = ref.act(z.double(), "gelu")
+    ref.close(y, want, 6 * ref.U * (1 + z.double() ** 2 / 2) * want.abs(), "gelu")
+    # past 13 nothing is left of the tail
+    far = torch.tensor([[13.5], [20.0], [300.0], [6e4]], dtype=torch.float16, device=dev)
+    y, _ = mm.linear(far, one, activation="gelu", out_dtype=torch.float32)
+    assert torch.equal(y, far.float())
+    y, _ = mm.linear(-far, one, activation="gelu", out_dtype=torch.float32)
+    assert not y.any()
+
+
+def test_gelu_slope_to_float32(torch_dev):
+    """Phi(z) + z phi(z): each term below 1, in a few roundings (4) of values
+    below 1."""
+    torch, dev = torch_dev
+    z = every_half(torch, dev, 12.0)
+    one = torch.ones((1, 1), dtype=torch.float16, device=dev)
+    say("gelu's slope to float32")
+    _, _, db = mm.linear_backward(torch.ones_like(z), one, torch.ones_like(z), z,
+                                  activation="gelu", need_dx=False, need_dw=False,
+                                  bias_dtype=torch.float32)
+    want = ref.act_slope(z.double(), "gelu")[0]
+    ref.close(db, want, torch.full_like(want, 4 * ref.U), "gelu's slope")
