@@ -102,10 +102,11 @@ NormPlan norm_plan(int64_t cols, int V) {
   return {0, 0};
 }
 
-// Workgroups of 256 lanes or a row's, as many as the CUs hold at once.
+// Workgroups of a row's lanes (four rows of one wave), as many as the CUs
+// hold at once.
 template <int DT, int PDT, int GT, int NV>
 void norm_run(const NormArgs& a, hipStream_t s) {
-  constexpr int G = GT < 256 ? 256 / GT : 1;
+  constexpr int G = GT == 64 ? 4 : 1;
   const int64_t groups = (a.rows + G - 1) / G;
   constexpr int kPerCU = 2048 / (GT * G);
   const uint32_t grid = (uint32_t)(groups < kCUs * kPerCU ? groups : kCUs * kPerCU);

@@ -1,6 +1,7 @@
 """Edges of the native operators: blocks of a checkpoint that end inside the
 matrix and hold values that are not finite, results beside other outputs,
-activations at infinity and to the last bits of float32."""
+activations at infinity and to the last bits of float32, rows of equal
+values."""
 import math
 
 import pytest
@@ -169,3 +170,49 @@ def test_gelu_slope_to_float32(torch_dev):
                                   bias_dtype=torch.float32)
     want = ref.act_slope(z.double(), "gelu")[0]
     ref.close(db, want, torch.full_like(want, 4 * ref.U), "gelu's slope")
+
+
+# ------------------------------------------------- rows without spread
+@pytest.mark.parametrize("cols", [5, 77, 1000, 8200, 20000])
+@pytest.mark.parametrize("dt", ["fp16", "bf16", "fp32"])
+def test_rows_of_equal_values(torch_dev, dt, cols):
+    """A row of equal values c has y = b, also where its float32 sum is not
+    exact.  Where c is more than four times sqrt(eps) the mean is corrected:
+    it is off by no more than its own rounding, U |c|, and a few U of what was
+    corrected; elsewhere its few roundings (8 here) are 8 U 4 of y."""
+    torch, dev = torch_dev
+    dtype = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}[dt]
+    c = torch.tensor([[12345.678], [-0.1], [1e-3], [3.0], [60000.0], [1.1]], device=dev).to(dtype)
+    x = c.expand(len(c), cols).contiguous()
+    w = torch.ones(cols, device=dev)
+    b = torch.randn(cols, device=dev)
+    say("rows of equal values", dt, cols)
+    y, mean, rstd, _ = mm.layer_norm(x, w, b, eps=1e-5)
+    exact = c[:, 0].double()
+    off = (mean.double() - exact).abs()
+    assert (off <= torch.where(exact.abs() > 4 * 1e-5 ** 0.5, 2, 8) * ref.U * exact.abs()).all()
+    off = (y.double() - b.double()).abs()
+    assert (off <= 32 * ref.U + ref.ROUND[dtype] * b.double().abs() * 2).all()
+
+
+def test_rows_of_small_spread(torch_dev):
+    """Rows with an offset of 10^2 to 10^5 times their spread, against
+    float64: the mean's own rounding (U |mean|) moves y by U |mean| rstd, and
+    so do the elements' differences from it; a row beside them is not
+    touched."""
+    torch, dev = torch_dev
+    g = torch.Generator(device=dev).manual_seed(3)
+    for cols in (77, 700, 1000, 3000, 9000, 20000):
+        x = torch.randn((9, cols), generator=g, device=dev)
+        alone = mm.layer_norm(x[4:5].contiguous())[0]
+        offset = torch.tensor([1e2, -1e3, 1e4, 1e5, 0, 3, 5, -1e5, 1e4], device=dev)[:, None]
+        x += offset
+        say("rows of small spread", cols)
+        y, mean, rstd, _ = mm.layer_norm(x)
+        assert torch.equal(y[4:5], alone)
+        xd = x.double()
+        m = xd.mean(1, keepdim=True)
+        r = 1 / torch.sqrt((xd - m).square().mean(1, keepdim=True) + 1e-5)
+        want = (xd - m) * r
+        room = 4 * ref.U * m.abs() * r + 64 * ref.U * (want.abs() + 1)
+        ref.close(y, want, room, "y")
