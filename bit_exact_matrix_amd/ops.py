@@ -146,7 +146,8 @@ def _start():
     # where this torch has it (making a Stream object takes 2.7 us)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda i: torch.cuda.current_stream(i).cuda_stream)
-    _torch, _dt = torch, types
+    _dt = types
+    _torch = torch  # last: what another thread's call looks at
 
 
 def _matrix(t, what, dtype=None, shape=None, dev=None):
