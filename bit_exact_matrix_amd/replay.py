@@ -65,15 +65,16 @@ def backward(dy, s: Saved, p: Block):
 
 def emulated_rows(x, p: Block, rows, model="hopper"):
     """Rows of h w1 + b1 (float32) as the emulated GPU computes the product,
-    and as the native product does."""
+    and of the native product of the step: over all rows, for the number of
+    rows chooses the kernel and the order of its sums."""
     import torch
     h, _, _, _ = ops.layer_norm(x, p.norm_w, p.norm_b)
-    h = h[rows].contiguous()
+    native, _ = ops.linear(h, p.w1, p.b1, out_dtype=torch.float32)
     c = p.b1.float().expand(len(rows), -1).contiguous()
     dtype = "bf16" if x.dtype == torch.bfloat16 else "fp16"
-    d, _ = gemm(model, dtype, h.view(torch.int16), p.w1.contiguous().view(torch.int16), c)
-    native, _ = ops.linear(h, p.w1, p.b1, out_dtype=torch.float32)
-    return d, native
+    d, _ = gemm(model, dtype, h[rows].contiguous().view(torch.int16),
+                p.w1.contiguous().view(torch.int16), c)
+    return d, native[rows]
 
 
 def make(rows, dim, hidden, dtype, seed=0, device="cuda"):
