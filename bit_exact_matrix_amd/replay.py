@@ -6,8 +6,8 @@ The forward pass runs on the native operators and leaves 8-bit checkpoints
 of x, of the pre-activation h w1 + b1 and of a; the backward pass uses them
 (and makes h again from the checkpoint of x).  Two things are then checked:
 
-  repeats     the step run twice gives the same bits everywhere, gradients
-              included: the forward/recompute comparison of the AEGIS
+  repeats     the step run twice gives the same bits everywhere, in what it
+              saves as in its output and gradients: the forward/recompute comparison of the AEGIS
               chapter ("Redundancy already exists in the training
               computation"), which a provider's step must pass too
   emulated    sampled rows of the first product, emulated as a Hopper or
@@ -77,6 +77,20 @@ def emulated_rows(x, p: Block, rows, model="hopper"):
     return d, native[rows]
 
 
+def outputs(y, s: Saved, dx, grads: Block):
+    """Every tensor that a step leaves."""
+    saved = [t for part in s for t in (part[:2] if isinstance(part, ops.Checkpoint) else (part,))]
+    return [y, dx, *grads, *saved]
+
+
+def same_bits(a, b):
+    """Whether two tensors are the same word for word: a zero of the other
+    sign differs, a NaN does not."""
+    import torch
+    word = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[a.element_size()]
+    return a.dtype == b.dtype and torch.equal(a.contiguous().view(word), b.contiguous().view(word))
+
+
 def make(rows, dim, hidden, dtype, seed=0, device="cuda"):
     """A block of random parameters, an input and a gradient of its output."""
     import torch
@@ -99,8 +113,8 @@ def replay(rows=4096, dim=1024, hidden=4096, dtype="bf16", model="hopper", seed=
     for _ in range(2):
         y, saved = forward(x, p)
         dx, grads = backward(dy, saved, p)
-        runs.append([y, dx, *grads])
-    same = all(torch.equal(a, b) for a, b in zip(*runs))
+        runs.append(outputs(y, saved, dx, grads))
+    same = all(same_bits(a, b) for a, b in zip(*runs))
     sample = torch.linspace(0, rows - 1, min(rows, 16), device=x.device).long()
     emulated, native = emulated_rows(x, p, sample, model)
     kept = [saved.x, saved.z, saved.a]
