@@ -7,8 +7,10 @@ current stream, and there is no CPU fallback.
 
 ``layer_norm``, ``layer_norm_backward``, ``linear``, ``linear_backward``,
 ``checkpoint`` and ``restore`` take torch tensors (matrices; a row stride
-larger than the row is taken as it is).  The raw C entry points (``EXPORTED``)
-take integers exactly as the C functions do.
+larger than the row is taken as it is).  They take no part in autograd:
+results never require grad, whatever the arguments do, and gradients come from
+the two backward functions, which the program calls itself.  The raw C entry
+points (``EXPORTED``) take integers exactly as the C functions do.
 """
 from __future__ import annotations
 
@@ -274,7 +276,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, checkpoint=False, stream=Non
     of x's type or float32 (both the same), or None.  checkpoint=True also
     saves x in 8 bits, in the same pass.
     Returns (y, mean, rstd, saved): mean and rstd are float32 vectors that
-    layer_norm_backward takes, saved a Checkpoint of x or None.
+    layer_norm_backward takes, saved a Checkpoint of x or None.  Outside
+    autograd: y never requires grad.
     """
     call = _Call(x, "x", stream)
     px, ldx = _matrix(x, "x")
@@ -396,7 +399,8 @@ def linear(x, w, bias=None, activation=None, residual=None, keep=None, out_dtype
     activation: one of ACTIVATIONS; out_dtype: x's type (the default) or
     float32.  keep="checkpoint" also saves z = x w + bias in 8 bits,
     keep="full" returns it in x's type: what linear_backward needs of it.
-    Returns (y, kept), kept None without keep.
+    Returns (y, kept), kept None without keep.  Outside autograd: y never
+    requires grad.
     """
     call = _Call(x, "x", stream)
     dt, dev = x.dtype, call.dev
@@ -444,7 +448,10 @@ def linear_backward(dy, x, w, z=None, activation=None, need_dx=True, need_dw=Tru
     kept (a matrix or a Checkpoint), needed with an activation.  Returns
     (dx, dw, dbias), None for those not needed: dx of dy's type, dw laid out
     as w is, of dw_dtype (w's type or float32), dbias of bias_dtype (the
-    same choice).  The residual's gradient is dy.
+    same choice).  The residual's gradient is dy.  The gradient of the
+    pre-activation enters both products rounded to dy's type, which the matrix
+    cores take (dbias sums it before): the error of dx and dw in that type is
+    about 1.4 times that of rounding them alone.
     """
     call = _Call(dy, "dy", stream)
     dt, dev = dy.dtype, call.dev

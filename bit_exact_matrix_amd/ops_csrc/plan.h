@@ -220,7 +220,9 @@ inline Plan linear_plan(const Product& p, bool saves) {
 inline int64_t partial_bytes(const Product& p, const Plan& q) {
   return q.partial ? up256(p.M * p.N * q.splits * 4) : 0;
 }
-inline int64_t copy_bytes(bool copy, const Stored& t) { return copy ? up256(t.rows * t.ld * 2) : 0; }
+inline int64_t copy_bytes(bool copy, const Stored& t) {
+  return copy ? up256(t.rows * t.ld * 2) : 0;
+}
 inline int64_t product_bytes(const Product& p, const Plan& q) {
   return partial_bytes(p, q) + copy_bytes(q.copy_a, stored(p.la, p.M, p.K)) +
          copy_bytes(q.copy_b, stored(p.lb, p.N, p.K));

@@ -34,13 +34,16 @@
  *           of two, -117 <= e <= 120, with max |x| <= 448 * 2^e over the
  *           block's finite elements (e = -117 for a block without any)
  *   A code is x / 2^e rounded to nearest, ties to even; a code restores to
- *   code * 2^e, which every element type here holds exactly.  Magnitudes
- *   above 61440 (FP16) or 1.875 * 2^127 are saved as that bound, so that
- *   no code restores to an infinity.  NaN and infinities are saved as the
- *   code 0xFF, NaN (E4M3 has no infinity), and do not enter the block's maximum.  Where an
- *   operator reads a checkpoint, codes and scales stand in the place of
- *   the matrix, which is then NULL.  codes are read and written in whole
- *   words where they and the row length allow it; no alignment is asked.
+ *   code * 2^e, which the type that was saved holds exactly (a
+ *   pre-activation that mma_linear saves as FP16 comes from FP32 sums: below
+ *   FP16's 2^-24 its restored matrix is rounded, what mma_linear_backward
+ *   reads of it is not).  Magnitudes above 61440 (FP16) or 1.875 * 2^127 are
+ *   saved as that bound, so that no code restores to an infinity.  NaN and
+ *   infinities are saved as the code 0xFF, NaN (E4M3 has no infinity), and
+ *   do not enter the block's maximum.  Where an operator reads a checkpoint,
+ *   codes and scales stand in the place of the matrix, which is then NULL.
+ *   codes are read and written in whole words where they and the row length
+ *   allow it; no alignment is asked.
  *
  * MEMORY
  *   Every pointer is a DEVICE pointer on the current HIP device, owned by

@@ -216,3 +216,19 @@ def test_rows_of_small_spread(torch_dev):
         want = (xd - m) * r
         room = 4 * ref.U * m.abs() * r + 64 * ref.U * (want.abs() + 1)
         ref.close(y, want, room, "y")
+
+
+# ------------------------------------------------------- beside autograd
+def test_results_are_outside_autograd(torch_dev):
+    """As documented: arguments that require grad are taken, and give results
+    that do not."""
+    torch, dev = torch_dev
+    x = torch.randn((4, 64), device=dev).bfloat16().requires_grad_()
+    w = torch.randn((64, 32), device=dev).bfloat16().requires_grad_()
+    v = torch.ones(64, device=dev, requires_grad=True)
+    y, _ = mm.linear(x, w)
+    h, mean, rstd, _ = mm.layer_norm(x, v, v)
+    grads = mm.linear_backward(y, x, w) + mm.layer_norm_backward(h, x, v, mean, rstd)
+    assert not any(t.requires_grad for t in (y, h, mean, rstd, *grads))
+    for f in (mm.ops, mm.linear, mm.layer_norm):
+        assert "autograd" in f.__doc__
