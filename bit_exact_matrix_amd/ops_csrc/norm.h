@@ -21,9 +21,9 @@
 // adds those in workgroup order: the result does not depend on which
 // workgroup ran first.
 //
-// Measured, 8192 x 4096 bf16: forward 27 us (134 MB, 5.0 TB/s), with the
-// checkpoint 31 us (169 MB, 5.4 TB/s); backward 42 us (201 MB, 4.8 TB/s) and
-// 4.6 us for the partial sums.  A copy of 256 MiB reaches 5.4 TB/s.
+// Measured, 8192 x 4096 bf16 (medians): forward 26 us (134 MB, 5.2 TB/s), with
+// the checkpoint 32 us (169 MB, 5.3 TB/s); backward 42 us (201 MB, 4.8 TB/s) and
+// 4.8 us for the partial sums.  A copy of 256 MiB reaches 5.4 TB/s.
 #ifndef MMAOPS_NORM_H
 #define MMAOPS_NORM_H
 
@@ -66,7 +66,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* lds, int& turn) {
 // A row whose mean is more than four times its spread, var + eps: its mean is
 // corrected by d = mean (x - mu), and the variance by d^2.  Below, mu's error
 // moves y by a few times 4 * 2^-24.  (For every row: the forward pass of 8192
-// x 4096 bf16 with checkpoint takes 36 us, so 32.)
+// x 4096 bf16 with checkpoint took 36 us, so 32.)
 __device__ __forceinline__ bool row_far(float mu, float var, float eps) {
   return mu * mu > 16.0f * (var + eps);
 }

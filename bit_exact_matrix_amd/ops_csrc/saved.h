@@ -8,8 +8,8 @@
 //
 // Measured: 8192 x 4096 bf16 (102 MB) saved in 20 us, restored in 16 us (from
 // memory 19 and 18, 5.4 TB/s); the gradient of gelu with the bias's, 4096 x
-// 4096 bf16 from a checkpoint (84 MB), in 22 us: its arithmetic, about 30
-// instructions an element, is near what memory takes (16 us).
+// 4096 bf16 from a checkpoint (84 MB), in 27 us: its arithmetic, about 40
+// instructions an element, takes longer than memory does (16 us).
 #ifndef MMAOPS_SAVED_H
 #define MMAOPS_SAVED_H
 
