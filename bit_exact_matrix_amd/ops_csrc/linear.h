@@ -649,9 +649,9 @@ __global__ __launch_bounds__(256, 2) void linear_pair_kernel(PairArgs p) {
 // so a load has 1,200 to 2,400 cycles to land.  Loads every 4 slots or fewer
 // wait for the vector memory pipe (8192^3: every 2, 844 us, 4, 792, 5, 782).
 // What is left: 8192^3 bf16 takes 768 us (X W), 751 (X W^T) and 774 (X^T
-// dY), 1.42 to 1.46 PFLOP/s, at 1.8 GHz under this load with the matrix
-// cores busy 71% of the cycles; a fifth of the rest is the epilogue.  A row of 64 elements is a
-// whole 128-byte line; steps of 32 with a ring of four stages kept the
+// dY), 1.42 to 1.46 PFLOP/s, at 1.6 to 1.8 GHz under this load with the matrix
+// cores busy 71% (X W) and 76% (X W^T) of the cycles.  A row of 64 elements is
+// a whole 128-byte line; steps of 32 with a ring of four stages kept the
 // vector memory pipe busier than the products (8192^3, both operands with K
 // fastest: 922 us against 856).
 template <int DT, int LA, int LB, int BM, int BN, int STAGES>
