@@ -538,7 +538,7 @@ __global__ __launch_bounds__(256) void norm_long_dw_kernel(NormArgs a, int64_t r
 // 16 runs and then in run order.  lane = column; blockIdx.y picks one of
 // the interleaved matrices (row p of matrix y starts at (p * gridDim.y + y)
 // * cols).
-__global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, int count,
+static __global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, int count,
                                                           int64_t cols, void* out0, void* out1,
                                                           int dt) {
   __shared__ float meet[16][64];

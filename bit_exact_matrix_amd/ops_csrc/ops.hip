@@ -5,6 +5,8 @@
 #include <string.h>
 
 #include "../../include/mmaops.h"
+#include "checks.h"
+#include "launch.h"
 #include "linear.h"
 #include "norm.h"
 #include "plan.h"
@@ -20,70 +22,14 @@ static_assert(kFP16 == MMAEMU_DTYPE_FP16 && kBF16 == MMAEMU_DTYPE_BF16 &&
 
 thread_local char g_hip_error[256] = "no HIP error recorded";
 
-int hip_fail(hipError_t e, const char* where) {
+}  // namespace
+
+int mmaops::hip_fail(hipError_t e, const char* where) {
   snprintf(g_hip_error, sizeof g_hip_error, "HIP error in %s: %s", where, hipGetErrorString(e));
   return MMAEMU_ERR_HIP;
 }
 
-// ------------------------------------------------------ argument checks
-// A matrix (or vector, rows = 1) as a call reads or writes it.
-struct View {
-  uintptr_t p;
-  int64_t rows, row_bytes, ld_bytes;
-  int64_t span() const { return (rows - 1) * ld_bytes + row_bytes; }
-  bool any() const { return p && rows > 0 && row_bytes > 0; }
-};
-
-View view(const void* p, int64_t rows, int64_t cols, int64_t ld, int esz) {
-  return View{(uintptr_t)p, rows, cols * esz, ld * esz};
-}
-
-// Two matrices overlap if their spans do, unless they are side by side in
-// rows of the same stride (column ranges of one buffer).
-bool overlap(const View& a, const View& b) {
-  if (!a.any() || !b.any()) return false;
-  const View &lo = a.p <= b.p ? a : b, &hi = a.p <= b.p ? b : a;
-  if ((uintptr_t)lo.p + (uintptr_t)lo.span() <= hi.p) return false;
-  if (a.rows > 1 && b.rows > 1 && a.ld_bytes == b.ld_bytes) {
-    const int64_t at = (int64_t)((hi.p - lo.p) % (uintptr_t)a.ld_bytes);
-    if (at >= lo.row_bytes && at + hi.row_bytes <= a.ld_bytes) return false;
-  }
-  return true;
-}
-
-constexpr int kMaxViews = 16;
-struct Views {
-  View in[kMaxViews], out[kMaxViews];
-  int ni = 0, no = 0;
-  void reads(const View& v) { in[ni++] = v; }
-  void writes(const View& v) { out[no++] = v; }
-  bool clash() const {
-    for (int i = 0; i < no; ++i) {
-      for (int j = 0; j < i; ++j)
-        if (overlap(out[i], out[j])) return true;
-      for (int j = 0; j < ni; ++j)
-        if (overlap(out[i], in[j])) return true;
-    }
-    return false;
-  }
-};
-
-// rows x cols of elements with leading dimension ld: sizes that 64-bit byte
-// offsets, the kernels' 32-bit column counters and a grid of fewer than 2^32
-// lanes (16 for each column, of the column sums) hold
-constexpr int64_t kMaxCols = int64_t(1) << 27, kMaxRows = int64_t(1) << 40;
-
-bool shape_ok(int64_t rows, int64_t cols, int64_t ld) {
-  if (rows < 0 || cols < 0 || rows > kMaxRows || cols > kMaxCols) return false;
-  if (rows == 0 || cols == 0) return true;
-  return (ld >= cols || rows == 1) && ld >= 0 && ld <= INT64_MAX / 8 / rows;
-}
-
-bool param_type_ok(int dtype, int pdt) { return pdt == dtype || pdt == kFP32; }
-bool any_type(int dt) { return dt == kFP16 || dt == kBF16 || dt == kFP32; }
-bool half_type(int dt) { return dt == kFP16 || dt == kBF16; }
-
-int64_t scale_cols(int64_t cols) { return (cols + kBlock - 1) / kBlock; }
+namespace {
 
 // ------------------------------------------------------------ layer norm
 // How a row is held: lanes a row, vectors a lane, rows a workgroup.
@@ -188,20 +134,16 @@ hipError_t norm_backward_launch(const NormArgs& a, int groups, hipStream_t s) {
   return hipGetLastError();
 }
 
-// FN<DT, PDT>(...) for the call's types
-#define MMAOPS_BY_TYPES(dt, pdt, FN, ...)                                          \
-  ((dt) == kFP32   ? FN<kFP32, kFP32>(__VA_ARGS__)                                 \
-   : (dt) == kFP16 ? ((pdt) == kFP32 ? FN<kFP16, kFP32>(__VA_ARGS__)               \
-                                     : FN<kFP16, kFP16>(__VA_ARGS__))              \
-                   : ((pdt) == kFP32 ? FN<kBF16, kFP32>(__VA_ARGS__)               \
-                                     : FN<kBF16, kBF16>(__VA_ARGS__)))
+}  // namespace
 
-hipError_t column_sums(const float* partial, int count, int64_t cols, void* out0, void* out1,
-                       int two, int dt, hipStream_t s) {
+hipError_t mmaops::column_sums(const float* partial, int count, int64_t cols, void* out0,
+                               void* out1, int two, int dt, hipStream_t s) {
   const dim3 grid((uint32_t)((cols + 63) / 64), two ? 2u : 1u);
   column_sum_kernel<<<grid, 1024, 0, s>>>(partial, count, cols, out0, out1, dt);
   return hipGetLastError();
 }
+
+namespace {
 
 // ------------------------------------------------------------ checkpoints
 // Lanes a row (a power of two from 16 to 256, as a shift) and the grid.
@@ -236,8 +178,10 @@ hipError_t restore_launch(const uint8_t* codes, const uint8_t* scales, void* y, 
   return hipGetLastError();
 }
 
-hipError_t restore_to(int dt, const uint8_t* codes, const uint8_t* scales, void* y, int64_t ldy,
-                      int64_t rows, int64_t cols, hipStream_t s) {
+}  // namespace
+
+hipError_t mmaops::restore_to(int dt, const uint8_t* codes, const uint8_t* scales, void* y,
+                              int64_t ldy, int64_t rows, int64_t cols, hipStream_t s) {
   return dt == kFP16   ? restore_launch<kFP16>(codes, scales, y, ldy, rows, cols, s)
          : dt == kBF16 ? restore_launch<kBF16>(codes, scales, y, ldy, rows, cols, s)
                        : restore_launch<kFP32>(codes, scales, y, ldy, rows, cols, s);
@@ -245,7 +189,8 @@ hipError_t restore_to(int dt, const uint8_t* codes, const uint8_t* scales, void*
 
 // ---------------------------------------------------------------- products
 // x (16-bit elements) to rows of t.ld elements at y
-hipError_t align_rows(const void* x, int64_t ldx, void* y, const Stored& t, hipStream_t s) {
+hipError_t mmaops::align_rows(const void* x, int64_t ldx, void* y, const Stored& t,
+                              hipStream_t s) {
   if (t.rows == 0 || t.cols == 0) return hipSuccess;
   int shift;
   dim3 grid;
@@ -254,6 +199,8 @@ hipError_t align_rows(const void* x, int64_t ldx, void* y, const Stored& t, hipS
                                     shift);
   return hipGetLastError();
 }
+
+namespace {
 
 // A product's arguments, with its operands copied where the plan says so.
 hipError_t linear_fill(const Product& p, const Plan& q, LinearArgs& g, void* ws,
@@ -480,13 +427,18 @@ __global__ void zero_rows_kernel(void* p, int64_t ld, int64_t rows, int64_t cols
     store_any(p, i / cols * ld + i % cols, 0.0f, dt);
 }
 
-hipError_t zero_rows(void* p, int64_t ld, int64_t rows, int64_t cols, int dt, hipStream_t s) {
+}  // namespace
+
+hipError_t mmaops::zero_rows(void* p, int64_t ld, int64_t rows, int64_t cols, int dt,
+                             hipStream_t s) {
   if (!p || rows == 0 || cols == 0) return hipSuccess;
   const int64_t blocks = (rows * cols + 255) / 256;
   zero_rows_kernel<<<(uint32_t)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(p, ld, rows, cols,
                                                                              dt);
   return hipGetLastError();
 }
+
+namespace {
 
 hipError_t backward_run(const mma_linear_backward_args& r, void* ws, hipStream_t s) {
   const int64_t wr = r.w_transposed ? r.N : r.K, wc = r.w_transposed ? r.K : r.N;
@@ -781,7 +733,8 @@ const char* mma_ops_strerror(int code) {
     case MMAEMU_ERR_DTYPE:
       return "unsupported element type (products take FP16 and BF16; a parameter or output "
              "type is the operands' or FP32)";
-    case MMAEMU_ERR_UNSUPPORTED: return "unknown activation, or a flag other than 0 or 1";
+    case MMAEMU_ERR_UNSUPPORTED: 
+      return "unknown activation, a flag other than 0 or 1, or a probability outside [0, 1]";
     case MMAEMU_ERR_SHAPE:
       return "bad shape (negative or too large, a leading dimension below the row length, or "
              "a layer norm over no columns)";

@@ -60,9 +60,9 @@ __global__ __launch_bounds__(256) void restore_kernel(const uint8_t* codes,
 
 // A matrix of 16-bit elements copied to rows of ldy elements that start on
 // 16 bytes, for the direct loads of a product.
-__global__ __launch_bounds__(256) void align_kernel(const uint16_t* x, int64_t ldx, uint16_t* y,
-                                                    int64_t ldy, int64_t rows, int64_t cols,
-                                                    int shift) {
+static __global__ __launch_bounds__(256) void align_kernel(const uint16_t* x, int64_t ldx,
+                                                           uint16_t* y, int64_t ldy, int64_t rows,
+                                                           int64_t cols, int shift) {
   constexpr int V = 8;
   const int lane = threadIdx.x & ((1 << shift) - 1), g = threadIdx.x >> shift;
   const int64_t step = (int64_t)gridDim.x * (256 >> shift);
