@@ -23,7 +23,8 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 BLOCK = 32  # elements of a checkpoint block
 EXPORTED = ("mma_layer_norm", "mma_layer_norm_backward", "mma_layer_norm_backward_workspace",
             "mma_checkpoint", "mma_restore", "mma_linear", "mma_linear_workspace",
-            "mma_linear_backward", "mma_linear_backward_workspace", "mma_ops_strerror")
+            "mma_linear_backward", "mma_linear_backward_workspace", "mma_dropout",
+            "mma_ops_strerror")
 
 # mma_linear_args and mma_linear_backward_args
 _LINEAR = struct.Struct("6i3q13Q")
@@ -62,6 +63,7 @@ def _load():
         from . import load_library
         lib = load_library()
         vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+        f64, u64 = ctypes.c_double, ctypes.c_uint64
         types = {
             "mma_layer_norm": [i32, i32, vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, i64, i64,
                                f32, vp],
@@ -74,6 +76,7 @@ def _load():
             "mma_linear_workspace": [vp],
             "mma_linear_backward": [vp, vp, i64, vp],
             "mma_linear_backward_workspace": [vp],
+            "mma_dropout": [i32, vp, i64, vp, i64, vp, i64, i64, i64, f64, u64, u64, vp, vp],
             "mma_ops_strerror": [i32],
         }
         fns = {}
@@ -124,6 +127,10 @@ def mma_linear_backward(args, workspace, workspace_bytes, hip_stream):
 
 def mma_linear_backward_workspace(args):
     return _load()["mma_linear_backward_workspace"](args)
+
+
+def mma_dropout(*args):
+    return _load()["mma_dropout"](*args)
 
 
 def mma_ops_strerror(code) -> str:

@@ -26,6 +26,23 @@
  *   mma_linear_backward       dz = dY act'(z), db = sum over rows of dz,
  *                             dX = dz W^T, dW = X^T dz
  *   mma_checkpoint, mma_restore   x to 8 bits and back
+ *   mma_dropout               y = m x / (1 - p) + residual, m 0 with
+ *                             probability p, else 1; its backward pass is
+ *                             the same of dY
+ *
+ * DROPOUT
+ *   A mask is never stored: it is a function of an element's place and the
+ *   call's seed and offset, and the backward pass, or a replay, makes it again.
+ *   Philox4x32 with ten rounds (Salmon, Moraes, Dror, Shaw, "Parallel random
+ *   numbers: as easy as 1, 2, 3", 2011) of the counter (row * 2^24 + column /
+ *   8, offset), both of 64 bits with the lower word first, under the key seed
+ *   (the lower word first) gives four words for eight columns; column c has
+ *   half c mod 2 (the lower one first) of word (c mod 8) / 2.  An element is kept where
+ *   these 16 bits are at least T = round(65536 p), and 1 / (1 - p) is 65536 /
+ *   (65536 - T) (0 where T = 65536): p is met to within 2^-17, the mean
+ *   exactly.  What is dropped is 0 whatever it was.  state: NULL, or device
+ *   memory with (seed, offset) that the call reads when it runs, in the place
+ *   of its two arguments: a captured graph draws anew when they change.
  *
  * CHECKPOINTS
  *   codes   rows x cols E4M3 codes (OCP "FN"), contiguous
@@ -185,6 +202,12 @@ typedef struct {
 int mma_linear_backward(const mma_linear_backward_args *args, void *workspace,
                         int64_t workspace_bytes, void *hip_stream);
 int64_t mma_linear_backward_workspace(const mma_linear_backward_args *args);
+
+/* Y = drop(X) + residual (rows x cols of dtype; residual may be NULL); p in
+ * [0, 1].  With dY as X and no residual, the gradient of X. */
+int mma_dropout(int dtype, const void *X, int64_t ldx, const void *residual, int64_t ldr, void *Y,
+                int64_t ldy, int64_t rows, int64_t cols, double p, uint64_t seed, uint64_t offset,
+                const uint64_t *state, void *hip_stream);
 
 /* Text for a return code of these functions (thread-local for
  * MMAEMU_ERR_HIP).  Never NULL. */
