@@ -316,4 +316,5 @@ def tiles(model, dtype, A, B, C=None, D=None, xorsum=False, stream=None):
 # ------------------------------------- native training operators (mmaops.h)
 from .ops import (Checkpoint, MmaOpsError, checkpoint, layer_norm,  # noqa: E402
                   layer_norm_backward, linear, linear_backward, restore)
-from .block import dropout, dropout_backward  # noqa: E402
+from .block import (ResidualParams, ResidualStats, dropout, dropout_backward,  # noqa: E402
+                    residual_norm, residual_norm_backward)

@@ -7,10 +7,18 @@ program calls itself.
 """
 from __future__ import annotations
 
+import struct
 from operator import index
+from typing import NamedTuple
 
 from . import ops
-from .ops import _Call, _done, _load, _matrix
+from .ops import _Call, _done, _load, _matrix, _vector
+
+NORMS = {None: 0, "layer": 1, "rms": 2}
+
+# mma_residual_norm_args and mma_residual_norm_backward_args
+_JOIN = struct.Struct("4i2fd3Q2q17Q")
+_JOIN_BACKWARD = struct.Struct("4ifid3Q2q25Q")
 
 
 def _known(dt, what):
@@ -75,3 +83,137 @@ def dropout_backward(dy, p, seed=0, offset=0, stream=None):
     """The gradient of dropout's x: mask dy / (1 - p), with the mask of the
     forward pass's p, seed and offset.  The residual's gradient is dy."""
     return dropout(dy, p, seed, offset, None, stream)
+
+
+class ResidualParams(NamedTuple):
+    """The vectors of residual_norm, cols values each or None, all of the
+    matrices' type or all float32; the backward pass returns their gradients
+    in the same places."""
+    gate: object = None
+    post_weight: object = None
+    post_bias: object = None
+    pre_weight: object = None
+    pre_bias: object = None
+
+
+class ResidualStats(NamedTuple):
+    """What residual_norm_backward needs of the forward pass's norms: float32
+    vectors, None where there is no such norm, the means of an rms norm too."""
+    post_mean: object
+    post_rstd: object
+    mean: object
+    rstd: object
+
+
+def _norm_kind(name, what):
+    if name not in NORMS:
+        raise ValueError(f"{what}: unknown norm {name!r}: None, 'layer' or 'rms'")
+    return NORMS[name]
+
+
+def _params(params, post, pre, dt, cols, dev):
+    """(the five pointers, the vectors' type)."""
+    if not isinstance(params, ResidualParams):
+        raise TypeError("params is a ResidualParams")
+    pointers, kind = [], None
+    for name, t in zip(ResidualParams._fields, params):
+        if t is not None and not (post if name.startswith("post") else
+                                  pre if name.startswith("pre") else True):
+            raise ValueError(f"{name} without that norm")
+        p, k = _vector(t, name, cols, dev, (dt, ops._torch.float32))
+        if k is not None:
+            if kind is not None and t.dtype != kind:
+                raise TypeError("the vectors must be of one type")
+            kind = t.dtype
+        pointers.append(p or 0)
+    return pointers, dt if kind is None else kind
+
+
+def residual_norm(x, branch, params=ResidualParams(), post=None, pre=None, scale=1.0, eps=1e-5,
+                  dropout=0.0, seed=0, offset=0, stream=None):
+    """A block's output into the residual stream, and the norm before the next
+    block, on the current stream (mma_residual_norm):
+
+        r = scale x + gate drop(post(branch)),  h = pre(r)
+
+    x, branch: rows x cols, float16, bfloat16 or float32; post, pre: "layer",
+    "rms" or None; params: a ResidualParams; dropout, seed, offset: as in
+    ``dropout``, whose mask it is.  h is made from r before its rounding.
+    Returns (r, h, ResidualStats); h is None without a pre norm.  Outside
+    autograd: the results never require grad.
+    """
+    call = _Call(x, "x", stream)
+    px, ldx = _matrix(x, "x")
+    dt, dev = x.dtype, call.dev
+    t = _known(dt, "x")
+    rows, cols = x.shape
+    pb, ldb = _matrix(branch, "branch", dt, (rows, cols), dev)
+    kp, kr = _norm_kind(post, "post"), _norm_kind(pre, "pre")
+    vectors, vt = _params(params, kp, kr, dt, cols, dev)
+    p, seed, offset, state = _seeds(dropout, seed, offset, dev)
+    f32 = ops._torch.float32
+    with call:
+        r = call.empty((rows, cols), dt)
+        h = call.empty((rows, cols), dt) if kr else None
+        stats = ResidualStats(*(call.empty((rows,), f32) if there else None
+                                for there in (kp == 1, kp, kr == 1, kr)))
+        args = _JOIN.pack(t, ops._dt[vt], kp, kr, scale, eps, p, seed, offset, state or 0, rows,
+                          cols, px, ldx, pb, ldb, *vectors, r.data_ptr(), cols,
+                          h.data_ptr() if kr else 0, cols,
+                          *(0 if s is None else s.data_ptr() for s in stats))
+        rc = _load()["mma_residual_norm"](args, call.raw)
+    _done(rc, "mma_residual_norm")
+    return r, h, stats
+
+
+def residual_norm_backward(dr, dh, r, branch, params, stats, post=None, pre=None, scale=1.0,
+                           dropout=0.0, seed=0, offset=0, need_dx=True, need_dbranch=True,
+                           need_dparams=True, stream=None):
+    """Gradients of residual_norm on the current stream.
+
+    dr, dh: the gradients of r and h; dr may be None (0) where there is a pre
+    norm, dh is None without one.  r, stats: what the forward pass returned (r
+    may be None without a pre norm); branch, params, post, pre, scale, dropout,
+    seed, offset: what it was called with (branch may be None without a post norm
+    and a gate).  Returns (dx, dbranch, ResidualParams of the vectors'
+    gradients); what is not needed, or belongs to no vector, is None.
+    """
+    kp, kr = _norm_kind(post, "post"), _norm_kind(pre, "pre")
+    lead = dh if kr else dr
+    call = _Call(lead, "dh" if kr else "dr", stream)
+    _matrix(lead, "dh" if kr else "dr")
+    dt, dev = lead.dtype, call.dev
+    t = _known(dt, "dh" if kr else "dr")
+    rows, cols = shape = tuple(lead.shape)
+    if not kr and dh is not None:
+        raise ValueError("dh without a pre norm")
+    if not isinstance(stats, ResidualStats):
+        raise TypeError("stats is a ResidualStats")
+    f32 = ops._torch.float32
+
+    def matrix(m, what):
+        return (0, 0) if m is None else _matrix(m, what, dt, shape, dev)
+
+    matrices = (*matrix(dr, "dr"), *matrix(dh, "dh"), *matrix(r if kr else None, "r"),
+                *matrix(branch, "branch"))
+    vectors, vt = _params(params, kp, kr, dt, cols, dev)
+    pointers = [_vector(s, n, rows, dev, (f32,))[0] or 0
+                for n, s in zip(ResidualStats._fields, stats)]
+    p, seed, offset, state = _seeds(dropout, seed, offset, dev)
+    fns = _load()
+    with call:
+        dx = call.empty(shape, dt) if need_dx else None
+        db = call.empty(shape, dt) if need_dbranch else None
+        grads = ResidualParams(*(call.empty((cols,), vt) if need_dparams and v is not None
+                                 else None for v in params))
+        args = _JOIN_BACKWARD.pack(
+            t, ops._dt[vt], kp, kr, scale, 0, p, seed, offset, state or 0, rows, cols, *matrices,
+            *vectors[:4], *pointers, dx.data_ptr() if need_dx else 0, cols,
+            db.data_ptr() if need_dbranch else 0, cols,
+            *(0 if g is None else g.data_ptr() for g in grads))
+        size = fns["mma_residual_norm_backward_workspace"](args)
+        ws = call.workspace(size)
+        rc = fns["mma_residual_norm_backward"](args, ws.data_ptr() if size else None, size,
+                                               call.raw)
+    _done(rc, "mma_residual_norm_backward")
+    return dx, db, grads

@@ -24,7 +24,8 @@ BLOCK = 32  # elements of a checkpoint block
 EXPORTED = ("mma_layer_norm", "mma_layer_norm_backward", "mma_layer_norm_backward_workspace",
             "mma_checkpoint", "mma_restore", "mma_linear", "mma_linear_workspace",
             "mma_linear_backward", "mma_linear_backward_workspace", "mma_dropout",
-            "mma_ops_strerror")
+            "mma_residual_norm", "mma_residual_norm_backward",
+            "mma_residual_norm_backward_workspace", "mma_ops_strerror")
 
 # mma_linear_args and mma_linear_backward_args
 _LINEAR = struct.Struct("6i3q13Q")
@@ -77,6 +78,9 @@ def _load():
             "mma_linear_backward": [vp, vp, i64, vp],
             "mma_linear_backward_workspace": [vp],
             "mma_dropout": [i32, vp, i64, vp, i64, vp, i64, i64, i64, f64, u64, u64, vp, vp],
+            "mma_residual_norm": [vp, vp],
+            "mma_residual_norm_backward": [vp, vp, i64, vp],
+            "mma_residual_norm_backward_workspace": [vp],
             "mma_ops_strerror": [i32],
         }
         fns = {}
@@ -131,6 +135,20 @@ def mma_linear_backward_workspace(args):
 
 def mma_dropout(*args):
     return _load()["mma_dropout"](*args)
+
+
+def mma_residual_norm(args, hip_stream):
+    """args: the bytes of an mma_residual_norm_args."""
+    return _load()["mma_residual_norm"](args, hip_stream)
+
+
+def mma_residual_norm_backward(args, workspace, workspace_bytes, hip_stream):
+    """args: the bytes of an mma_residual_norm_backward_args."""
+    return _load()["mma_residual_norm_backward"](args, workspace, workspace_bytes, hip_stream)
+
+
+def mma_residual_norm_backward_workspace(args):
+    return _load()["mma_residual_norm_backward_workspace"](args)
 
 
 def mma_ops_strerror(code) -> str:

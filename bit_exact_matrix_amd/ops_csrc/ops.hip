@@ -734,7 +734,8 @@ const char* mma_ops_strerror(int code) {
       return "unsupported element type (products take FP16 and BF16; a parameter or output "
              "type is the operands' or FP32)";
     case MMAEMU_ERR_UNSUPPORTED: 
-      return "unknown activation, a flag other than 0 or 1, or a probability outside [0, 1]";
+      return "unknown activation or norm, a flag other than 0 or 1, or a probability outside "
+             "[0, 1]";
     case MMAEMU_ERR_SHAPE:
       return "bad shape (negative or too large, a leading dimension below the row length, or "
              "a layer norm over no columns)";

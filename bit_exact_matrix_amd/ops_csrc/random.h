@@ -85,6 +85,16 @@ struct Drop {
       v[i] = u >= threshold ? v[i] * up : 0.0f;
     }
   }
+
+  // 0 where it is dropped, without the factor
+  template <int V>
+  __device__ __forceinline__ void clear(const uint32_t (&w)[V / 2], float (&v)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint32_t u = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+      v[i] = u >= threshold ? v[i] : 0.0f;
+    }
+  }
 };
 
 // y = drop(x) + residual, each element read and written once.  A workgroup

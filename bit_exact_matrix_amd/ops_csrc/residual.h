@@ -1,0 +1,379 @@
+// residual.h -- the sum of a block's output into the residual stream, with the
+// norms after and before a block, forward and backward.
+//
+// Mathematics.  v = post(b), r = scale x + gate drop(v), h = pre(r).  A norm is
+// a layer norm (norm.h), y = (x - mu) / sqrt(var + eps) w + bias, or an rms norm,
+// the same with mu = 0.  Backward, with xh = (x - mu) rstd and q = dy w:
+//   norm'(dy) = rstd (q - mean(q) - xh mean(q xh)), without mean(q) for rms
+//   t = dr + pre'(dh);  dx = scale t;  db = post'(gate drop(t))
+// and the vectors' gradients from four column sums over the rows,
+//   p1 = sum dh rh, p0 = sum dh, s1 = sum drop(t) bh, s0 = sum drop(t):
+//   dpre_w = p1, dpre_b = p0, dpost_w = gate s1, dpost_b = gate s0,
+//   dgate = post_w s1 + post_b s0
+// (bh = b where there is no post norm).  All in FP32; h is made from r as it
+// is before r's rounding.
+#ifndef MMAOPS_RESIDUAL_H
+#define MMAOPS_RESIDUAL_H
+
+#include "random.h"
+
+namespace mmaops {
+
+enum { kNormNone = 0, kNormLayer = 1, kNormRms = 2 };
+
+struct JoinArgs {
+  const void* x;
+  const void* branch;
+  int64_t ldx, ldb;
+  const void *gate, *post_w, *post_b, *pre_w, *pre_b;  // or NULL each
+  void* r;  // backward: the forward pass's, read
+  void* h;
+  int64_t ldr, ldh;
+  float *post_mean, *post_rstd, *mean, *rstd;
+  int64_t rows;
+  int cols, post, pre;
+  float scale, eps;
+  DropArgs drop;
+  // backward
+  const void *dr, *dh;
+  void *dx, *db;
+  int64_t lddr, lddh, lddx, lddb;
+  float* partial;  // [groups][4][cols]: p1, p0, s1, s0
+  float* means;    // long rows: [rows][2], the means of pre'
+};
+
+// V elements of a parameter at column c, `fill` where there is none
+template <int PDT, int V>
+__device__ __forceinline__ void param(const void* p, int c, int n, float fill, float (&v)[V]) {
+  if (p && n > 0) {
+    unpack(load_pack<PDT, V>((const elem_t<PDT>*)p + c, n), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = fill;
+  }
+}
+
+// --------------------------------------------------- rows of any length
+// One workgroup a row, the row read again for each of its sums.
+
+// Mean and rstd of a row whose elements fn(c, n, v) gives, 0 past its end.
+template <int GT, int V, typename FN>
+__device__ __forceinline__ void row_stats(FN fn, int cols, bool layer, float eps, float* lds,
+                                          int& turn, float& mean, float& rstd) {
+  const float n_f = (float)cols;
+  float s[1], mu = 0.0f;
+  if (layer) {
+    s[0] = 0.0f;
+    for (int c = threadIdx.x * V; c < cols; c += GT * V) {
+      float v[V];
+      fn(c, cols - c, v);
+      s[0] += pair_sum(v);
+    }
+    row_sum<GT, 1>(s, lds, turn);
+    mu = s[0] / n_f;
+  }
+  auto centred = [&](bool square) {
+    s[0] = 0.0f;
+    for (int c = threadIdx.x * V; c < cols; c += GT * V) {
+      float v[V];
+      fn(c, cols - c, v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[i] = c + i < cols ? v[i] - mu : 0.0f;
+        if (square) v[i] *= v[i];
+      }
+      s[0] += pair_sum(v);
+    }
+    row_sum<GT, 1>(s, lds, turn);
+    return s[0] / n_f;
+  };
+  float var = centred(true);
+  mean = mu;
+  if (layer && row_far(mu, var, eps)) row_correct(centred(false), mean, var);
+  rstd = 1.0f / sqrtf(var + eps);
+}
+
+template <int DT, int PDT>
+__global__ __launch_bounds__(1024) void join_long_kernel(JoinArgs a) {
+  constexpr int V = kVec<DT>, GT = 1024;
+  using E = elem_t<DT>;
+  __shared__ float lds[2 * 16];
+  int turn = 0;
+  const Drop drop(a.drop);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const E* const x = (const E*)a.x + row * a.ldx;
+    const E* const b = (const E*)a.branch + row * a.ldb;
+    float pm = 0.0f, pr = 1.0f, m = 0.0f, q = 1.0f;
+    if (a.post != kNormNone)
+      row_stats<GT, V>([&](int c, int n, float (&v)[V]) { unpack(load_pack<DT, V>(b + c, n), v); },
+                       a.cols, a.post == kNormLayer, a.eps, lds, turn, pm, pr);
+    auto sum = [&](int c, int n, float (&v)[V]) {
+      float t[V], u[V];
+      unpack(load_pack<DT, V>(b + c, n), v);
+      if (a.post != kNormNone) {
+        param<PDT, V>(a.post_w, c, n, 1.0f, t);
+        param<PDT, V>(a.post_b, c, n, 0.0f, u);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = (v[i] - pm) * pr * t[i] + u[i];
+      }
+      if (drop.threshold) {
+        uint32_t w[V / 2];
+        drop.halves<V>(row, c, w);
+        drop.apply<V>(w, v);
+      }
+      param<PDT, V>(a.gate, c, n, 1.0f, t);
+      unpack(load_pack<DT, V>(x + c, n), u);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = i < n ? u[i] * a.scale + t[i] * v[i] : 0.0f;
+    };
+    if (a.pre != kNormNone)
+      row_stats<GT, V>(sum, a.cols, a.pre == kNormLayer, a.eps, lds, turn, m, q);
+    for (int c = threadIdx.x * V; c < a.cols; c += GT * V) {
+      const int n = a.cols - c;
+      float v[V], w[V], u[V];
+      sum(c, n, v);
+      store_pack<DT, V>((E*)a.r + row * a.ldr + c, pack<DT, V>(v), n);
+      if (a.pre == kNormNone) continue;
+      param<PDT, V>(a.pre_w, c, n, 1.0f, w);
+      param<PDT, V>(a.pre_b, c, n, 0.0f, u);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = (v[i] - m) * q * w[i] + u[i];
+      store_pack<DT, V>((E*)a.h + row * a.ldh + c, pack<DT, V>(v), n);
+    }
+    if (threadIdx.x == 0) {
+      if (a.post_mean) a.post_mean[row] = pm;
+      if (a.post_rstd) a.post_rstd[row] = pr;
+      if (a.mean) a.mean[row] = m;
+      if (a.rstd) a.rstd[row] = q;
+    }
+  }
+}
+
+// What the backward pass knows of a row before its sums.
+struct JoinRow {
+  float pm, pr, m, q;  // statistics
+  __device__ __forceinline__ JoinRow(const JoinArgs& a, int64_t row) {
+    pm = a.post == kNormLayer ? a.post_mean[row] : 0.0f;
+    pr = a.post != kNormNone ? a.post_rstd[row] : 1.0f;
+    m = a.pre == kNormLayer ? a.mean[row] : 0.0f;
+    q = a.pre != kNormNone ? a.rstd[row] : 1.0f;
+  }
+};
+
+// dh, rh = (r - m) q and t = dr + pre'(dh) of V columns, 0 past the row's
+// end; m0 and m1 are the means of dh w and of dh w rh.
+template <int DT, int PDT, int V>
+__device__ __forceinline__ void join_t(const JoinArgs& a, const JoinRow& s, int64_t row, int c,
+                                       int n, float m0, float m1, float (&dh)[V], float (&rh)[V],
+                                       float (&t)[V]) {
+  using E = elem_t<DT>;
+  if (a.dr) {
+    unpack(load_pack<DT, V>((const E*)a.dr + row * a.lddr + c, n), t);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) t[i] = 0.0f;
+  }
+  if (a.pre == kNormNone) return;
+  float w[V];
+  unpack(load_pack<DT, V>((const E*)a.dh + row * a.lddh + c, n), dh);
+  unpack(load_pack<DT, V>((const E*)a.r + row * a.ldr + c, n), rh);
+  param<PDT, V>(a.pre_w, c, n, 1.0f, w);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    rh[i] = i < n ? (rh[i] - s.m) * s.q : 0.0f;
+    if (i < n) t[i] += s.q * (dh[i] * w[i] - m0 - rh[i] * m1);
+  }
+}
+
+// drop(t), and bh = (b - pm) pr where the branch is read.  For the column sums
+// bh is 0 where it was dropped, whatever it was: without a post norm an
+// infinity there has no part in the gate's gradient.
+template <int DT, int V, bool SUMS>
+__device__ __forceinline__ void join_branch(const JoinArgs& a, const JoinRow& s, const Drop& drop,
+                                            int64_t row, int c, int n, float (&t)[V],
+                                            float (&bh)[V]) {
+  if (a.branch) {
+    unpack(load_pack<DT, V>((const elem_t<DT>*)a.branch + row * a.ldb + c, n), bh);
+#pragma unroll
+    for (int i = 0; i < V; ++i) bh[i] = i < n ? (bh[i] - s.pm) * s.pr : 0.0f;
+  }
+  if (drop.threshold) {
+    uint32_t w[V / 2];
+    drop.halves<V>(row, c, w);
+    drop.apply<V>(w, t);
+    if (SUMS) drop.clear<V>(w, bh);
+  }
+}
+
+template <int DT, int PDT>
+__global__ __launch_bounds__(1024) void join_long_dx_kernel(JoinArgs a) {
+  constexpr int V = kVec<DT>, GT = 1024;
+  using E = elem_t<DT>;
+  __shared__ float lds[2 * 16 * 2];
+  int turn = 0;
+  const Drop drop(a.drop);
+  const float n_f = (float)a.cols;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const JoinRow st(a, row);
+    float s[2] = {0.0f, 0.0f}, m0 = 0.0f, m1 = 0.0f, k0 = 0.0f, k1 = 0.0f;
+    if (a.pre != kNormNone) {
+      for (int c = threadIdx.x * V; c < a.cols; c += GT * V) {
+        const int n = a.cols - c;
+        float dh[V], rh[V], w[V];
+        unpack(load_pack<DT, V>((const E*)a.dh + row * a.lddh + c, n), dh);
+        unpack(load_pack<DT, V>((const E*)a.r + row * a.ldr + c, n), rh);
+        param<PDT, V>(a.pre_w, c, n, 1.0f, w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          rh[i] = i < n ? (rh[i] - st.m) * st.q : 0.0f;
+          dh[i] *= w[i];
+          rh[i] *= dh[i];
+        }
+        s[0] += pair_sum(dh);
+        s[1] += pair_sum(rh);
+      }
+      row_sum<GT, 2>(s, lds, turn);
+      m0 = a.pre == kNormLayer ? s[0] / n_f : 0.0f;
+      m1 = s[1] / n_f;
+    }
+    if (a.means && threadIdx.x == 0) {
+      a.means[row * 2] = m0;
+      a.means[row * 2 + 1] = m1;
+    }
+    // q = drop(t) gate w and bh of a vector
+    auto inner = [&](int c, int n, float (&t)[V], float (&q)[V], float (&bh)[V]) {
+      float dh[V], rh[V], g[V], w[V];
+      join_t<DT, PDT, V>(a, st, row, c, n, m0, m1, dh, rh, t);
+#pragma unroll
+      for (int i = 0; i < V; ++i) q[i] = t[i];
+      join_branch<DT, V, false>(a, st, drop, row, c, n, q, bh);
+      param<PDT, V>(a.gate, c, n, 1.0f, g);
+      param<PDT, V>(a.post_w, c, n, 1.0f, w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) q[i] = i < n ? q[i] * g[i] * w[i] : 0.0f;
+    };
+    if (a.post != kNormNone && a.db) {
+      s[0] = s[1] = 0.0f;
+      for (int c = threadIdx.x * V; c < a.cols; c += GT * V) {
+        float t[V], q[V], bh[V];
+        inner(c, a.cols - c, t, q, bh);
+#pragma unroll
+        for (int i = 0; i < V; ++i) bh[i] *= q[i];
+        s[0] += pair_sum(q);
+        s[1] += pair_sum(bh);
+      }
+      row_sum<GT, 2>(s, lds, turn);
+      k0 = a.post == kNormLayer ? s[0] / n_f : 0.0f;
+      k1 = s[1] / n_f;
+    }
+    if (!a.dx && !a.db) continue;
+    for (int c = threadIdx.x * V; c < a.cols; c += GT * V) {
+      const int n = a.cols - c;
+      float t[V], q[V], bh[V];
+      inner(c, n, t, q, bh);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (a.post != kNormNone) q[i] = st.pr * (q[i] - k0 - bh[i] * k1);
+        t[i] *= a.scale;
+      }
+      if (a.dx) store_pack<DT, V>((E*)a.dx + row * a.lddx + c, pack<DT, V>(t), n);
+      if (a.db) store_pack<DT, V>((E*)a.db + row * a.lddb + c, pack<DT, V>(q), n);
+    }
+  }
+}
+
+// Partial column sums over a run of rows, for the columns of one workgroup
+// (64 lanes of V columns each, four waves over the rows).
+template <int DT, int PDT>
+__global__ __launch_bounds__(256) void join_long_sums_kernel(JoinArgs a, int64_t run) {
+  constexpr int V = kVec<DT>;
+  __shared__ float meet[4][4][64 * V];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = (blockIdx.x * 64 + lane) * V, n = a.cols - c;
+  const int64_t r0 = blockIdx.y * run, r1 = r0 + run < a.rows ? r0 + run : a.rows;
+  const Drop drop(a.drop);
+  float sum[4][V];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[k][i] = 0.0f;
+  if (n > 0)
+    for (int64_t row = r0 + wave; row < r1; row += 4) {
+      const JoinRow st(a, row);
+      float dh[V], rh[V], t[V], bh[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) dh[i] = rh[i] = bh[i] = 0.0f;
+      join_t<DT, PDT, V>(a, st, row, c, n, a.means[row * 2], a.means[row * 2 + 1], dh, rh, t);
+      join_branch<DT, V, true>(a, st, drop, row, c, n, t, bh);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        sum[0][i] += dh[i] * rh[i];
+        sum[1][i] += dh[i];
+        sum[2][i] += t[i] * bh[i];
+        sum[3][i] += t[i];
+      }
+    }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) meet[k][wave][i * 64 + lane] = sum[k][i];
+  __syncthreads();
+  float* const out = a.partial + ((int64_t)blockIdx.y * 4 + wave) * a.cols;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float s = 0.0f;
+    for (int q = 0; q < 4; ++q) s += meet[wave][q][i * 64 + lane];
+    if (i < n) out[c + i] = s;
+  }
+}
+
+// -------------------------------------------------- the vectors' gradients
+struct JoinSums {
+  const float* partial;  // [count][4][cols]
+  int count, dt;
+  int64_t cols;
+  const void *gate, *post_w, *post_b;
+  bool post;
+  void *dgate, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
+};
+
+// The groups' sums in group order within each of 16 runs and then in run
+// order: 64 columns a workgroup, a run a wave.
+static __global__ __launch_bounds__(1024) void join_sums_kernel(JoinSums a) {
+  __shared__ float meet[4][16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  const int run = (a.count + 15) / 16;
+  const int p0 = wave * run, p1 = p0 + run < a.count ? p0 + run : a.count;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < a.cols) {
+    const float* const p = a.partial + c;
+#pragma unroll 4
+    for (int q = p0; q < p1; ++q)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += p[((int64_t)q * 4 + k) * a.cols];
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) meet[k][wave][lane] = s[k];
+  __syncthreads();
+  if (wave || c >= a.cols) return;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    s[k] = meet[k][0][lane];
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s[k] += meet[k][w][lane];
+  }
+  const float g = a.gate ? load_any(a.gate, c, a.dt) : 1.0f;
+  if (a.dpre_w) store_any(a.dpre_w, c, s[0], a.dt);
+  if (a.dpre_b) store_any(a.dpre_b, c, s[1], a.dt);
+  if (a.dpost_w) store_any(a.dpost_w, c, g * s[2], a.dt);
+  if (a.dpost_b) store_any(a.dpost_b, c, g * s[3], a.dt);
+  if (a.dgate) {
+    const float w = a.post && a.post_w ? load_any(a.post_w, c, a.dt) : 1.0f;
+    const float b = a.post && a.post_b ? load_any(a.post_b, c, a.dt) : 0.0f;
+    store_any(a.dgate, c, w * s[2] + b * s[3], a.dt);
+  }
+}
+
+}  // namespace mmaops
+#endif

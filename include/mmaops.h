@@ -29,6 +29,15 @@
  *   mma_dropout               y = m x / (1 - p) + residual, m 0 with
  *                             probability p, else 1; its backward pass is
  *                             the same of dY
+ *   mma_residual_norm         v = post(branch), R = scale X + gate drop(v),
+ *                             H = pre(R): the sum of a block's output into
+ *                             the residual stream, with the norm after that
+ *                             block and the one before the next, each a layer
+ *                             norm, an rms norm (a layer norm with mu = 0) or
+ *                             none; H is made from R before its rounding
+ *   mma_residual_norm_backward   t = dR + pre'(dH), dX = scale t,
+ *                             dbranch = post'(gate drop(t)), and the gradients
+ *                             of the five vectors, sums over the rows
  *
  * DROPOUT
  *   A mask is never stored: it is a function of an element's place and the
@@ -208,6 +217,84 @@ int64_t mma_linear_backward_workspace(const mma_linear_backward_args *args);
 int mma_dropout(int dtype, const void *X, int64_t ldx, const void *residual, int64_t ldr, void *Y,
                 int64_t ldy, int64_t rows, int64_t cols, double p, uint64_t seed, uint64_t offset,
                 const uint64_t *state, void *hip_stream);
+
+enum { MMAOPS_NORM_NONE = 0, MMAOPS_NORM_LAYER = 1, MMAOPS_NORM_RMS = 2 };
+
+/* R = scale X + gate drop(post(branch)), H = pre(R), for matrices rows x cols
+ * of dtype, cols at least 1. */
+typedef struct {
+  int32_t dtype;
+  int32_t param_dtype;     /* of the five vectors: dtype or FP32 */
+  int32_t post, pre;       /* MMAOPS_NORM_... */
+  float scale;
+  float eps;               /* of both norms */
+  double p;                /* of dropout, in [0, 1] */
+  uint64_t seed, offset;
+  const uint64_t *state;   /* NULL, or (seed, offset) on the device */
+  int64_t rows, cols;
+  const void *X;
+  int64_t ldx;
+  const void *branch;
+  int64_t ldb;
+  const void *gate;        /* cols values, or NULL (1) */
+  const void *post_weight; /* or NULL (1); not read without that norm */
+  const void *post_bias;   /* or NULL (0) */
+  const void *pre_weight;
+  const void *pre_bias;
+  void *R;
+  int64_t ldr;
+  void *H;                 /* not written without a pre norm */
+  int64_t ldh;
+  float *post_mean;        /* rows floats each, or NULL; a mean is written by */
+  float *post_rstd;        /* a layer norm only */
+  float *mean;
+  float *rstd;
+} mma_residual_norm_args;
+
+int mma_residual_norm(const mma_residual_norm_args *args, void *hip_stream);
+
+/* Its backward pass, with the forward pass's settings and statistics (a
+ * mean for a layer norm only).  dR may be NULL (0) where there is a pre norm; dH and R
+ * are read with one only.  branch is read with a post norm or for dgate.  dX, dbranch and
+ * the vectors' gradients (of param_dtype): any of them NULL to leave it out. */
+typedef struct {
+  int32_t dtype, param_dtype, post, pre;
+  float scale;
+  int32_t reserved;        /* 0 */
+  double p;
+  uint64_t seed, offset;
+  const uint64_t *state;
+  int64_t rows, cols;
+  const void *dR;
+  int64_t lddr;
+  const void *dH;
+  int64_t lddh;
+  const void *R;
+  int64_t ldr;
+  const void *branch;
+  int64_t ldb;
+  const void *gate;
+  const void *post_weight;
+  const void *post_bias;
+  const void *pre_weight;
+  const float *post_mean;
+  const float *post_rstd;
+  const float *mean;
+  const float *rstd;
+  void *dX;
+  int64_t lddx;
+  void *dbranch;
+  int64_t lddb;
+  void *dgate;
+  void *dpost_weight;
+  void *dpost_bias;
+  void *dpre_weight;
+  void *dpre_bias;
+} mma_residual_norm_backward_args;
+
+int mma_residual_norm_backward(const mma_residual_norm_backward_args *args, void *workspace,
+                               int64_t workspace_bytes, void *hip_stream);
+int64_t mma_residual_norm_backward_workspace(const mma_residual_norm_backward_args *args);
 
 /* Text for a return code of these functions (thread-local for
  * MMAEMU_ERR_HIP).  Never NULL. */

@@ -51,3 +51,124 @@ def mask(rows, cols, p, seed, offset, dev):
 def dropped(x, m):
     """What is dropped is 0, an infinity or NaN too."""
     return torch.where(m > 0, x * m, torch.zeros_like(x))
+
+
+# --------------------------------------------- sum into the residual stream
+def _one(v, n, dev, fill=1.0):
+    return (torch.full((n,), fill, dtype=torch.float64, device=dev) if v is None else v.double())
+
+
+def norm(x, kind, w, b, eps, ex=None):
+    """(y, mean, rstd, bound of y, of mean, of rstd relative); ex: how far each
+    element of x may be off already (None: not at all)."""
+    n = x.shape[1]
+    w, b = _one(w, n, x.device), _one(b, n, x.device, 0.0)
+    mean = x.sum(1) / n if kind == "layer" else torch.zeros_like(x[:, 0])
+    d = x - mean[:, None]
+    rstd = 1.0 / torch.sqrt((d * d).sum(1) / n + eps)
+    y = d * rstd[:, None] * w + b
+    size = x.abs().mean(1)
+    em = DEPTH * U * size if kind == "layer" else torch.zeros_like(size)
+    # d is off by em and a rounding, the variance by 2 |d| em and DEPTH U
+    er = DEPTH * U + rstd * (em + U * size)
+    ey = ((rstd * em)[:, None] + (d * rstd[:, None]).abs() * (er[:, None] + 4 * U)
+          + U * (x * rstd[:, None]).abs()) * w.abs() + 2 * U * (y.abs() + b.abs())
+    if ex is not None:
+        # to first order: d moves by ed, the variance by 2 mean |d| ed, and
+        # twice that for what is of higher order
+        ed = ex + (ex.mean(1, keepdim=True) if kind == "layer" else 0.0)
+        rel = rstd ** 2 * (d.abs() * ed).mean(1)
+        ey = ey + 2 * w.abs() * rstd[:, None] * (ed + d.abs() * rel[:, None])
+        em = em + (ex.mean(1) if kind == "layer" else 0.0)
+        er = er + 2 * rel
+    return y, mean, rstd, ey, em, er
+
+
+def residual_norm(x, branch, p, post, pre, scale, eps, m):
+    """Dictionaries of values and bounds; m: the mask with its factor, or None."""
+    x, b = x.double(), branch.double()
+    n, dev = x.shape[1], x.device
+    val, off = {}, {}
+    v, ev = b, torch.zeros_like(b)
+    if post:
+        v, mean, rstd, ev, em, er = norm(b, post, p.post_weight, p.post_bias, eps)
+        val["post_mean"], off["post_mean"] = mean, em
+        val["post_rstd"], off["post_rstd"] = rstd, er * rstd
+    if m is not None:
+        v, ev = dropped(v, m), torch.where(m > 0, ev * m, torch.zeros_like(ev))
+    g = _one(p.gate, n, dev)
+    val["r"] = r = scale * x + g * v
+    off["r"] = ex = 4 * U * ((scale * x).abs() + (g * v).abs()) + g.abs() * ev
+    if pre:
+        h, mean, rstd, eh, em, er = norm(r, pre, p.pre_weight, p.pre_bias, eps, ex)
+        val["h"], off["h"] = h, eh
+        val["mean"], off["mean"] = mean, em
+        val["rstd"], off["rstd"] = rstd, er * rstd
+    return val, off
+
+
+def residual_norm_backward(dr, dh, r, branch, p, stats, post, pre, scale, m):
+    """The same for the gradients: dx, dbranch and the vectors' names."""
+    lead = dh if pre else dr
+    n, dev = lead.shape[1], lead.device
+    val, off = {}, {}
+    t = torch.zeros(lead.shape, dtype=torch.float64, device=dev) if dr is None else dr.double()
+    et = torch.zeros_like(t)
+    if pre:
+        d, rr, q = dh.double(), r.double(), stats.rstd.double()[:, None]
+        mu = stats.mean.double()[:, None] if pre == "layer" else torch.zeros_like(q)
+        rh, erh = (rr - mu) * q, 3 * U * (rr.abs() + mu.abs()) * q
+        hq = d * _one(p.pre_weight, n, dev)
+        m1, em1 = (hq * rh).mean(1, keepdim=True), (DEPTH * U * (hq * rh).abs()
+                                                    + hq.abs() * erh).mean(1, keepdim=True)
+        m0 = hq.mean(1, keepdim=True) if pre == "layer" else torch.zeros_like(m1)
+        em0 = (DEPTH * U * hq.abs().mean(1, keepdim=True) if pre == "layer"
+               else torch.zeros_like(m1))
+        et = (6 * U * (t.abs() + q * (hq.abs() + m0.abs() + (rh * m1).abs()))
+              + q * (em0 + rh.abs() * em1 + erh * m1.abs()))
+        t = t + q * (hq - m0 - rh * m1)
+        val["pre_weight"] = (d * rh).sum(0)
+        off["pre_weight"] = (d.abs() * erh + (DEPTH + 4) * U * (d * rh).abs()).sum(0)
+        val["pre_bias"], off["pre_bias"] = d.sum(0), DEPTH * U * d.abs().sum(0)
+    val["dx"], off["dx"] = scale * t, abs(scale) * et + 2 * U * (scale * t).abs()
+    td, etd = t, et
+    if m is not None:
+        td = dropped(t, m)
+        etd = et * m + 2 * U * td.abs()
+    g = _one(p.gate, n, dev)
+    if branch is None:
+        val["dbranch"], off["dbranch"] = td * g, etd * g.abs() + 2 * U * (td * g).abs()
+        return val, off
+    b = branch.double()
+    if post:
+        k = stats.post_rstd.double()[:, None]
+        mu = stats.post_mean.double()[:, None] if post == "layer" else torch.zeros_like(k)
+    else:
+        k, mu = torch.ones_like(b[:, :1]), torch.zeros_like(b[:, :1])
+    bh, ebh = (b - mu) * k, 3 * U * (b.abs() + mu.abs()) * k
+    w, wb = ((_one(p.post_weight, n, dev), _one(p.post_bias, n, dev, 0.0)) if post else
+             (torch.ones_like(g), torch.zeros_like(g)))
+    qq = td * g * w
+    eqq = etd * (g * w).abs() + 3 * U * qq.abs()
+    if post:
+        k1 = (qq * bh).mean(1, keepdim=True)
+        ek1 = (DEPTH * U * (qq * bh).abs() + eqq * bh.abs() + qq.abs() * ebh).mean(1, keepdim=True)
+        k0, ek0 = torch.zeros_like(k1), torch.zeros_like(k1)
+        if post == "layer":
+            k0 = qq.mean(1, keepdim=True)
+            ek0 = (DEPTH * U * qq.abs() + eqq).mean(1, keepdim=True)
+        val["dbranch"] = k * (qq - k0 - bh * k1)
+        off["dbranch"] = k * (eqq + ek0 + bh.abs() * ek1 + ebh * k1.abs()
+                              + 6 * U * (qq.abs() + k0.abs() + (bh * k1).abs()))
+    else:
+        val["dbranch"], off["dbranch"] = qq, eqq
+    kept = bh if m is None else dropped(bh, (m > 0).double())
+    s1, s0 = (td * kept).sum(0), td.sum(0)
+    e1 = (etd * kept.abs() + td.abs() * ebh + (DEPTH + 4) * U * (td * kept).abs()).sum(0)
+    e0 = (etd + DEPTH * U * td.abs()).sum(0)
+    val["gate"] = w * s1 + wb * s0
+    off["gate"] = w.abs() * e1 + wb.abs() * e0 + 3 * U * ((w * s1).abs() + (wb * s0).abs())
+    if post:
+        val["post_weight"], off["post_weight"] = g * s1, g.abs() * e1 + U * (g * s1).abs()
+        val["post_bias"], off["post_bias"] = g * s0, g.abs() * e0 + U * (g * s0).abs()
+    return val, off
