@@ -317,4 +317,4 @@ def tiles(model, dtype, A, B, C=None, D=None, xorsum=False, stream=None):
 from .ops import (Checkpoint, MmaOpsError, checkpoint, layer_norm,  # noqa: E402
                   layer_norm_backward, linear, linear_backward, restore)
 from .block import (ResidualParams, ResidualStats, dropout, dropout_backward,  # noqa: E402
-                    residual_norm, residual_norm_backward)
+                    gated_linear, gated_linear_backward, residual_norm, residual_norm_backward)

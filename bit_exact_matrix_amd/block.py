@@ -12,9 +12,13 @@ from operator import index
 from typing import NamedTuple
 
 from . import ops
-from .ops import _Call, _done, _load, _matrix, _vector
+from .ops import Checkpoint, _activation, _Call, _done, _load, _matrix, _saved, _vector, _weight
 
 NORMS = {None: 0, "layer": 1, "rms": 2}
+
+# mma_gated_linear_args and mma_gated_linear_backward_args
+_GATED = struct.Struct("6i3q18Q")
+_GATED_BACKWARD = struct.Struct("6i3q26Q")
 
 # mma_residual_norm_args and mma_residual_norm_backward_args
 _JOIN = struct.Struct("4i2fd3Q2q17Q")
@@ -217,3 +221,141 @@ def residual_norm_backward(dr, dh, r, branch, params, stats, post=None, pre=None
                                                call.raw)
     _done(rc, "mma_residual_norm_backward")
     return dx, db, grads
+
+
+def _weights(w_gate, w_up, dt, dev):
+    """(pointer and ld of both, transposed)."""
+    pg, ldg, tg = _weight(w_gate, "w_gate", dt, dev)
+    pu, ldu, tu = _weight(w_up, "w_up", dt, dev)
+    if w_up.shape != w_gate.shape:
+        raise ValueError(f"w_up must have shape {tuple(w_gate.shape)}, got {tuple(w_up.shape)}")
+    if tg != tu:
+        # of one row or column both ways of reading a weight are right
+        if 1 in w_up.shape:
+            pu, ldu, tu = (*_matrix(w_up.t() if tg else w_up, "w_up", dt, None, dev), tg)
+        else:
+            raise ValueError("w_gate and w_up must be stored alike")
+    return pg, ldg, pu, ldu, tg
+
+
+def gated_linear(x, w_gate, w_up, bias_gate=None, bias_up=None, activation="silu", keep=None,
+                 out_dtype=None, stream=None):
+    """y = act(x w_gate + bias_gate) * (x w_up + bias_up) on the current stream
+    (mma_gated_linear).
+
+    x: M x K, float16 or bfloat16; w_gate, w_up: K x N of the same type, both
+    row-major or both the transposed view of a row-major N x K matrix; biases: N
+    values of x's type or float32 (both the same), or None; activation: one of
+    ops.ACTIVATIONS; out_dtype: x's type (the default) or float32.
+    keep="checkpoint" also saves both products (with their biases) in 8 bits,
+    keep="full" returns them in x's type: what gated_linear_backward needs.
+    Returns (y, kept): kept is the pair of the gate's product and the other, or
+    None.  Outside autograd: y never requires grad.
+    """
+    call = _Call(x, "x", stream)
+    torch, dt, dev = ops._torch, x.dtype, call.dev
+    if dt != torch.bfloat16 and dt != torch.float16:
+        raise TypeError(f"x: expected float16 or bfloat16, got {dt}")
+    px, ldx = _matrix(x, "x")
+    pg, ldg, pu, ldu, wt = _weights(w_gate, w_up, dt, dev)
+    m, k = x.shape
+    k2, n = w_gate.shape
+    if k != k2:
+        raise ValueError("inner dimensions differ")
+    act = _activation(activation)
+    od = dt if out_dtype is None else out_dtype
+    if od != dt and od != torch.float32:
+        raise TypeError(f"out_dtype: expected {dt} or float32, got {od}")
+    if keep not in (None, "full", "checkpoint"):
+        raise ValueError("keep is None, 'full' or 'checkpoint'")
+    bg, gt = _vector(bias_gate, "bias_gate", n, dev, (dt, torch.float32))
+    bu, ut = _vector(bias_up, "bias_up", n, dev, (dt, torch.float32))
+    if gt is not None and ut is not None and gt != ut:
+        raise TypeError("bias_gate and bias_up must be of one type")
+    t = ops._dt[dt]
+    bt = gt if gt is not None else ut if ut is not None else t
+    fns = _load()
+    with call:
+        y = call.empty((m, n), od)
+        kept, whole, saved = None, (0, n, 0, n), (0, 0, 0, 0)
+        if keep == "full":
+            kept = call.empty((m, n), dt), call.empty((m, n), dt)
+            whole = kept[0].data_ptr(), n, kept[1].data_ptr(), n
+        elif keep == "checkpoint":
+            kept = call.checkpoint((m, n), dt), call.checkpoint((m, n), dt)
+            saved = tuple(p.data_ptr() for c in kept for p in (c.codes, c.scales))
+        args = _GATED.pack(t, ops._dt[od], bt, act, wt, 0, m, n, k, px, ldx, pg, ldg, pu, ldu,
+                           bg or 0, bu or 0, y.data_ptr(), n, *whole, *saved)
+        size = fns["mma_gated_linear_workspace"](args)
+        ws = call.workspace(size)
+        rc = fns["mma_gated_linear"](args, ws.data_ptr() if size else None, size, call.raw)
+    _done(rc, "mma_gated_linear")
+    return y, kept
+
+
+def gated_linear_backward(dy, x, w_gate, w_up, kept, activation="silu", need_dx=True,
+                          need_dw=True, need_dbias=True, dw_dtype=None, bias_dtype=None,
+                          stream=None):
+    """Gradients of gated_linear on the current stream
+    (mma_gated_linear_backward).
+
+    dy: M x N; x: M x K or its Checkpoint; w_gate, w_up as in gated_linear; kept:
+    the pair that it returned (two matrices or two Checkpoints).  Returns (dx,
+    dw_gate, dw_up, dbias_gate, dbias_up), None for those not needed: dx of dy's
+    type, the weights' laid out as they are, of dw_dtype (their type or
+    float32), the biases' of bias_dtype (the same choice).  The gradients of the
+    two products enter the others rounded to dy's type, which the matrix cores
+    take (the biases' sum them before): the error of dx and the weights'
+    gradients in that type is about 1.4 times that of rounding them alone.
+    """
+    call = _Call(dy, "dy", stream)
+    torch, dt, dev = ops._torch, dy.dtype, call.dev
+    if dt != torch.bfloat16 and dt != torch.float16:
+        raise TypeError(f"dy: expected float16 or bfloat16, got {dt}")
+    pd, ldd = _matrix(dy, "dy")
+    pg, ldg, pu, ldu, wt = _weights(w_gate, w_up, dt, dev)
+    m, n = dy.shape
+    k, n2 = w_gate.shape
+    if n != n2:
+        raise ValueError("dy and the weights differ in their columns")
+    act = _activation(activation)
+    wd, bd = dw_dtype or dt, bias_dtype or dt
+    for d, what in ((wd, "dw_dtype"), (bd, "bias_dtype")):
+        if d != dt and d != torch.float32:
+            raise TypeError(f"{what}: expected {dt} or float32, got {d}")
+    px = ldx = xc = xs = 0
+    if isinstance(x, Checkpoint):
+        xc, xs = _saved(x, "x", (m, k), dt, dev)
+    else:
+        px, ldx = _matrix(x, "x", dt, (m, k), dev)
+    if not isinstance(kept, (tuple, list)) or isinstance(kept, Checkpoint) or len(kept) != 2:
+        raise TypeError("kept is the pair that gated_linear returned")
+    whole, saved = (0, 0, 0, 0), (0, 0, 0, 0)
+    if isinstance(kept[0], Checkpoint) != isinstance(kept[1], Checkpoint):
+        raise TypeError("kept: two matrices or two Checkpoints")
+    if isinstance(kept[0], Checkpoint):
+        saved = (*_saved(kept[0], "kept[0]", (m, n), dt, dev),
+                 *_saved(kept[1], "kept[1]", (m, n), dt, dev))
+    else:
+        whole = (*_matrix(kept[0], "kept[0]", dt, (m, n), dev),
+                 *_matrix(kept[1], "kept[1]", dt, (m, n), dev))
+    t = ops._dt[dt]
+    fns = _load()
+    with call:
+        dx = call.empty((m, k), dt) if need_dx else None
+        dw = [None, None]
+        if need_dw:
+            dw = [call.empty((n, k), wd).t() if wt else call.empty((k, n), wd) for _ in range(2)]
+        db = [call.empty((n,), bd) if need_dbias else None for _ in range(2)]
+        ldw = k if wt else n
+        args = _GATED_BACKWARD.pack(
+            t, ops._dt[wd], ops._dt[bd], act, wt, 0, m, n, k, pd, ldd, px, ldx, xc, xs, pg, ldg,
+            pu, ldu, *whole, *saved, dx.data_ptr() if need_dx else 0, k,
+            *((dw[0].data_ptr(), ldw, dw[1].data_ptr(), ldw) if need_dw else (0, 0, 0, 0)),
+            *((db[0].data_ptr(), db[1].data_ptr()) if need_dbias else (0, 0)))
+        size = fns["mma_gated_linear_backward_workspace"](args)
+        ws = call.workspace(size)
+        rc = fns["mma_gated_linear_backward"](args, ws.data_ptr() if size else None, size,
+                                              call.raw)
+    _done(rc, "mma_gated_linear_backward")
+    return dx, *dw, *db

@@ -19,7 +19,8 @@ OUT = os.path.join(HERE, "libmmaemu.so")
 
 # the native training operators (include/mmaops.h), linked into the library
 OPS_CSRC = os.path.join(HERE, "ops_csrc")
-OPS_SOURCES = ("ops.hip", "linear_fp16.hip", "linear_bf16.hip", "block.hip")
+OPS_SOURCES = ("ops.hip", "linear_fp16.hip", "linear_bf16.hip", "block.hip", "gated_fp16.hip",
+               "gated_bf16.hip")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -23,8 +23,10 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 BLOCK = 32  # elements of a checkpoint block
 EXPORTED = ("mma_layer_norm", "mma_layer_norm_backward", "mma_layer_norm_backward_workspace",
             "mma_checkpoint", "mma_restore", "mma_linear", "mma_linear_workspace",
-            "mma_linear_backward", "mma_linear_backward_workspace", "mma_dropout",
-            "mma_residual_norm", "mma_residual_norm_backward",
+            "mma_linear_backward", "mma_linear_backward_workspace", "mma_gated_linear",
+            "mma_gated_linear_workspace", "mma_gated_linear_backward",
+            "mma_gated_linear_backward_workspace", "mma_dropout", "mma_residual_norm",
+            "mma_residual_norm_backward",
             "mma_residual_norm_backward_workspace", "mma_ops_strerror")
 
 # mma_linear_args and mma_linear_backward_args
@@ -77,6 +79,10 @@ def _load():
             "mma_linear_workspace": [vp],
             "mma_linear_backward": [vp, vp, i64, vp],
             "mma_linear_backward_workspace": [vp],
+            "mma_gated_linear": [vp, vp, i64, vp],
+            "mma_gated_linear_workspace": [vp],
+            "mma_gated_linear_backward": [vp, vp, i64, vp],
+            "mma_gated_linear_backward_workspace": [vp],
             "mma_dropout": [i32, vp, i64, vp, i64, vp, i64, i64, i64, f64, u64, u64, vp, vp],
             "mma_residual_norm": [vp, vp],
             "mma_residual_norm_backward": [vp, vp, i64, vp],
@@ -131,6 +137,24 @@ def mma_linear_backward(args, workspace, workspace_bytes, hip_stream):
 
 def mma_linear_backward_workspace(args):
     return _load()["mma_linear_backward_workspace"](args)
+
+
+def mma_gated_linear(args, workspace, workspace_bytes, hip_stream):
+    """args: the bytes of an mma_gated_linear_args."""
+    return _load()["mma_gated_linear"](args, workspace, workspace_bytes, hip_stream)
+
+
+def mma_gated_linear_workspace(args):
+    return _load()["mma_gated_linear_workspace"](args)
+
+
+def mma_gated_linear_backward(args, workspace, workspace_bytes, hip_stream):
+    """args: the bytes of an mma_gated_linear_backward_args."""
+    return _load()["mma_gated_linear_backward"](args, workspace, workspace_bytes, hip_stream)
+
+
+def mma_gated_linear_backward_workspace(args):
+    return _load()["mma_gated_linear_backward_workspace"](args)
 
 
 def mma_dropout(*args):

@@ -5,6 +5,7 @@
 
 #include "../../include/mmaops.h"
 #include "checks.h"
+#include "gated.h"
 #include "launch.h"
 #include "residual.h"
 
@@ -182,6 +183,317 @@ hipError_t join_backward_launch(const JoinArgs& a, int groups, hipStream_t s) {
   return hipGetLastError();
 }
 
+// -------------------------------------------------------- gated layer
+GatedLaunches launches(int dt) { return dt == kFP16 ? gated_fp16() : gated_bf16(); }
+
+// A pair's arguments, with its operands copied where the plan says so.
+hipError_t paired_fill(const Paired& q, const Plan& r, LinearArgs& g, const void*& a2,
+                       const void*& b2, void* ws, hipStream_t s) {
+  const Product& p = q.p;
+  const TileShape& t = kTileShape[r.tile];
+  const int cols = paired_columns(q.kind, r.tile);
+  g.a = p.a;
+  g.b = p.b;
+  g.lda = p.lda;
+  g.ldb = p.ldb;
+  a2 = q.a2 ? q.a2 : p.a;
+  b2 = q.b2 ? q.b2 : p.b;
+  char* at = (char*)ws + paired_partial_bytes(q, r);
+  auto copy = [&](const void*& one, const void*& two, bool second, int64_t ld2, int64_t& ld,
+                  const Stored& st) {
+    hipError_t e = align_rows(one, ld, at, st, s);
+    one = at;
+    at += copy_bytes(true, st);
+    if (second && e == hipSuccess) {
+      e = align_rows(two, ld2, at, st, s);
+      two = at;
+      at += copy_bytes(true, st);
+    } else {
+      two = one;
+    }
+    ld = st.ld;
+    return e;
+  };
+  if (r.copy_a) {
+    const hipError_t e =
+        copy(g.a, a2, q.a2 != nullptr, q.lda2, g.lda, stored(p.la, p.M, p.K));
+    if (e != hipSuccess) return e;
+  }
+  if (r.copy_b) {
+    const hipError_t e =
+        copy(g.b, b2, q.b2 != nullptr, q.ldb2, g.ldb, stored(p.lb, p.N, p.K));
+    if (e != hipSuccess) return e;
+  }
+  g.M = p.M;
+  g.N = p.N;
+  g.K = p.K;
+  g.splits = r.splits;
+  g.guard = r.guard;
+  g.tiles_m = (int)((p.M + t.bm - 1) / t.bm);
+  g.tiles_n = (int)((p.N + cols - 1) / cols);
+  g.partial = r.partial ? (float*)ws : nullptr;
+  return hipSuccess;
+}
+
+// sizes whose products and tile counts the 64-bit and 31-bit counters hold
+bool gated_shape_ok(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kMax = kMaxCols;
+  if (M < 0 || N < 0 || K < 0 || M > kMax || N > kMax || K > kMax) return false;
+  return ((M + 15) / 16) * ((N + 15) / 16) <= INT32_MAX / 2 &&
+         ((M + 15) / 16) * ((K + 15) / 16) <= INT32_MAX / 2 &&
+         ((N + 15) / 16) * ((K + 15) / 16) <= INT32_MAX / 2;
+}
+
+Paired gated_product(const mma_gated_linear_args& r) {
+  return Paired{kGated,
+                Product{r.M, r.N, r.K, 0, r.w_transposed ? 0 : 1, r.X, r.Wg, r.ldx, r.ldwg},
+                nullptr, r.Wu, 0, r.ldwu};
+}
+
+int64_t gated_need(const mma_gated_linear_args& r) {
+  if (r.M == 0 || r.N == 0) return 0;
+  const Paired q = gated_product(r);
+  return paired_bytes(q, paired_plan(q, r.g_codes != nullptr));
+}
+
+template <typename ARGS>
+int gated_head(const ARGS& r, int out_dtype) {
+  if (!half_type(r.dtype)) return MMAEMU_ERR_DTYPE;
+  if (!param_type_ok(r.dtype, out_dtype) || !param_type_ok(r.dtype, r.bias_dtype))
+    return MMAEMU_ERR_DTYPE;
+  if (r.activation < MMAOPS_ACT_NONE || r.activation > MMAOPS_ACT_SILU || r.reserved ||
+      (r.w_transposed & ~1))
+    return MMAEMU_ERR_UNSUPPORTED;
+  return gated_shape_ok(r.M, r.N, r.K) ? MMAEMU_OK : MMAEMU_ERR_SHAPE;
+}
+
+int check_gated(const mma_gated_linear_args& r, int64_t ws_bytes, const void* ws,
+                bool sizes_only) {
+  const int rc = gated_head(r, r.out_dtype);
+  if (rc || sizes_only) return rc;
+  const int64_t wr = r.w_transposed ? r.N : r.K, wc = r.w_transposed ? r.K : r.N;
+  if (!shape_ok(r.M, r.K, r.ldx) || !shape_ok(wr, wc, r.ldwg) || !shape_ok(wr, wc, r.ldwu) ||
+      !shape_ok(r.M, r.N, r.ldy) || (r.G && !shape_ok(r.M, r.N, r.ldg)) ||
+      (r.U && !shape_ok(r.M, r.N, r.ldu)))
+    return MMAEMU_ERR_SHAPE;
+  if (r.M == 0 || r.N == 0) return MMAEMU_OK;
+  if (!r.Y || (r.K && (!r.X || !r.Wg || !r.Wu)) || !r.G != !r.U || !r.g_codes != !r.g_scales ||
+      !r.g_codes != !r.u_codes || !r.g_codes != !r.u_scales)
+    return MMAEMU_ERR_NULL;
+  const int oe = elem_bytes(r.out_dtype), be = elem_bytes(r.bias_dtype);
+  if (!aligned(r.X, 2) || !aligned(r.Wg, 2) || !aligned(r.Wu, 2) || !aligned(r.Y, oe) ||
+      !aligned(r.G, 2) || !aligned(r.U, 2) || !aligned(r.bias_g, be) || !aligned(r.bias_u, be) ||
+      (ws && !aligned(ws, 256)))
+    return MMAEMU_ERR_ALIGN;
+  const int64_t need = gated_need(r);
+  if (need && (!ws || ws_bytes < need)) return MMAEMU_ERR_SCRATCH;
+  Views v;
+  if (r.K) {
+    v.reads(view(r.X, r.M, r.K, r.ldx, 2));
+    v.reads(view(r.Wg, wr, wc, r.ldwg, 2));
+    v.reads(view(r.Wu, wr, wc, r.ldwu, 2));
+  }
+  v.reads(view(r.bias_g, 1, r.N, 0, be));
+  v.reads(view(r.bias_u, 1, r.N, 0, be));
+  v.writes(view(r.Y, r.M, r.N, r.ldy, oe));
+  v.writes(view(r.G, r.M, r.N, r.ldg, 2));
+  v.writes(view(r.U, r.M, r.N, r.ldu, 2));
+  for (const uint8_t* codes : {r.g_codes, r.u_codes}) v.writes(view(codes, 1, r.M * r.N, 0, 1));
+  for (const uint8_t* scales : {r.g_scales, r.u_scales})
+    v.writes(view(scales, 1, r.M * scale_cols(r.N), 0, 1));
+  v.writes(view(need ? ws : nullptr, 1, need, 0, 1));
+  return v.clash() ? MMAEMU_ERR_ALIAS : MMAEMU_OK;
+}
+
+// The backward pass: what it needs of the workspace, piece by piece.
+struct GatedBackward {
+  Paired dx, dw;
+  Plan pdx, pdw;
+  bool has_dz;     // dg and du are written
+  int db_runs;     // rows of column sums, 0: no bias gradient
+  int64_t db_run;  // rows of one of them
+  int64_t dg_at, du_at, ldd, x_at, db_at, part_at, bytes;
+};
+
+GatedBackward gated_backward(const mma_gated_linear_backward_args& r, void* ws) {
+  GatedBackward b;
+  memset(&b, 0, sizeof b);
+  char* const base = (char*)ws;
+  int64_t at = 0;
+  b.has_dz = r.dX || r.dWg;
+  b.ldd = (r.N + 7) / 8 * 8;  // rows that start on 16 bytes: direct loads
+  if (b.has_dz) {
+    b.dg_at = at;
+    at += up256(r.M * b.ldd * 2);
+    b.du_at = at;
+    at += up256(r.M * b.ldd * 2);
+  }
+  if (r.x_codes && r.dWg) {
+    b.x_at = at;
+    at += up256(r.M * ((r.K + 7) / 8 * 8) * 2);
+  }
+  if (r.dbias_g || r.dbias_u) {
+    const int64_t cols = (r.N + 511) / 512;
+    int64_t runs = (8 * kCUs + cols - 1) / cols;
+    if (runs > (r.M + 7) / 8) runs = (r.M + 7) / 8;
+    b.db_run = (r.M + runs - 1) / runs;
+    b.db_runs = (int)((r.M + b.db_run - 1) / b.db_run);
+    b.db_at = at;
+    at += up256((int64_t)b.db_runs * 2 * r.N * 4);
+  }
+  const void *const dg = base + b.dg_at, *const du = base + b.du_at;
+  const void* const x = r.x_codes ? base + b.x_at : r.X;
+  const int64_t ldx = r.x_codes ? (r.K + 7) / 8 * 8 : r.ldx;
+  b.part_at = at;
+  int64_t part = 0;
+  if (r.dX) {
+    b.dx = Paired{kSummed,
+                  Product{r.M, r.K, r.N, 0, r.w_transposed ? 1 : 0, dg, r.Wg, b.ldd, r.ldwg}, du,
+                  r.Wu, b.ldd, r.ldwu};
+    b.pdx = paired_plan(b.dx, false);
+    part = paired_bytes(b.dx, b.pdx);
+  }
+  if (r.dWg) {
+    b.dw = r.w_transposed
+               ? Paired{kApart, Product{r.N, r.K, r.M, 1, 1, dg, x, b.ldd, ldx}, du, nullptr,
+                        b.ldd, 0}
+               : Paired{kApart, Product{r.K, r.N, r.M, 1, 1, x, dg, ldx, b.ldd}, nullptr, du, 0,
+                        b.ldd};
+    b.pdw = paired_plan(b.dw, false);
+    const int64_t w = paired_bytes(b.dw, b.pdw);
+    part = part > w ? part : w;
+  }
+  b.bytes = at + part;
+  return b;
+}
+
+int check_gated_backward(const mma_gated_linear_backward_args& r, int64_t ws_bytes, void* ws,
+                         bool sizes_only) {
+  const int rc = gated_head(r, r.dw_dtype);
+  if (rc || sizes_only) return rc;
+  const int64_t wr = r.w_transposed ? r.N : r.K, wc = r.w_transposed ? r.K : r.N;
+  if (!shape_ok(r.M, r.N, r.lddy) || (r.X && !shape_ok(r.M, r.K, r.ldx)) ||
+      (r.dX && (!shape_ok(wr, wc, r.ldwg) || !shape_ok(wr, wc, r.ldwu))) ||
+      (r.G && !shape_ok(r.M, r.N, r.ldg)) || (r.U && !shape_ok(r.M, r.N, r.ldu)) ||
+      (r.dX && !shape_ok(r.M, r.K, r.lddx)) || (r.dWg && !shape_ok(wr, wc, r.lddwg)) ||
+      (r.dWu && !shape_ok(wr, wc, r.lddwu)))
+    return MMAEMU_ERR_SHAPE;
+  if (!r.dWg != !r.dWu) return MMAEMU_ERR_NULL;
+  const bool any_dx = r.dX && r.M && r.K, any_dw = r.dWg && r.K && r.N;
+  const bool any_db = (r.dbias_g || r.dbias_u) && r.N;
+  if (!any_dx && !any_dw && !any_db) return MMAEMU_OK;
+  if (r.M && r.N) {
+    if (!r.dY || (any_dx && (!r.Wg || !r.Wu))) return MMAEMU_ERR_NULL;
+    if (!r.x_codes != !r.x_scales || (any_dw && !r.X == !r.x_codes)) return MMAEMU_ERR_NULL;
+    if (!r.g_codes != !r.g_scales || !r.g_codes != !r.u_codes || !r.g_codes != !r.u_scales ||
+        !r.G != !r.U || !r.G == !r.g_codes)
+      return MMAEMU_ERR_NULL;
+  }
+  const int we = elem_bytes(r.dw_dtype), be = elem_bytes(r.bias_dtype);
+  if (!aligned(r.dY, 2) || !aligned(r.X, 2) || !aligned(r.Wg, 2) || !aligned(r.Wu, 2) ||
+      !aligned(r.G, 2) || !aligned(r.U, 2) || !aligned(r.dX, 2) || !aligned(r.dWg, we) ||
+      !aligned(r.dWu, we) || !aligned(r.dbias_g, be) || !aligned(r.dbias_u, be) ||
+      (ws && !aligned(ws, 256)))
+    return MMAEMU_ERR_ALIGN;
+  const int64_t need = r.M && r.N ? gated_backward(r, ws).bytes : 0;
+  if (need && (!ws || ws_bytes < need)) return MMAEMU_ERR_SCRATCH;
+  Views v;
+  v.reads(view(r.dY, r.M, r.N, r.lddy, 2));
+  if (any_dw) {
+    v.reads(view(r.X, r.M, r.K, r.ldx, 2));
+    v.reads(view(r.x_codes, 1, r.M * r.K, 0, 1));
+    v.reads(view(r.x_scales, 1, r.M * scale_cols(r.K), 0, 1));
+  }
+  if (any_dx) {
+    v.reads(view(r.Wg, wr, wc, r.ldwg, 2));
+    v.reads(view(r.Wu, wr, wc, r.ldwu, 2));
+  }
+  v.reads(view(r.G, r.M, r.N, r.ldg, 2));
+  v.reads(view(r.U, r.M, r.N, r.ldu, 2));
+  for (const uint8_t* codes : {r.g_codes, r.u_codes}) v.reads(view(codes, 1, r.M * r.N, 0, 1));
+  for (const uint8_t* scales : {r.g_scales, r.u_scales})
+    v.reads(view(scales, 1, r.M * scale_cols(r.N), 0, 1));
+  v.writes(view(r.dX, r.M, r.K, r.lddx, 2));
+  v.writes(view(r.dWg, wr, wc, r.lddwg, we));
+  v.writes(view(r.dWu, wr, wc, r.lddwu, we));
+  v.writes(view(r.dbias_g, 1, r.N, 0, be));
+  v.writes(view(r.dbias_u, 1, r.N, 0, be));
+  v.writes(view(need ? ws : nullptr, 1, need, 0, 1));
+  return v.clash() ? MMAEMU_ERR_ALIAS : MMAEMU_OK;
+}
+
+hipError_t gated_backward_run(const mma_gated_linear_backward_args& r, void* ws, hipStream_t s) {
+  const int64_t wr = r.w_transposed ? r.N : r.K, wc = r.w_transposed ? r.K : r.N;
+  hipError_t e = hipSuccess;
+  if (r.M == 0 || r.N == 0) {  // sums over nothing
+    e = zero_rows(r.dX, r.lddx, r.M, r.K, r.dtype, s);
+    if (e == hipSuccess) e = zero_rows(r.dWg, r.lddwg, wr, wc, r.dw_dtype, s);
+    if (e == hipSuccess) e = zero_rows(r.dWu, r.lddwu, wr, wc, r.dw_dtype, s);
+    if (e == hipSuccess) e = zero_rows(r.dbias_g, r.N, 1, r.N, r.bias_dtype, s);
+    if (e == hipSuccess) e = zero_rows(r.dbias_u, r.N, 1, r.N, r.bias_dtype, s);
+    return e;
+  }
+  const GatedLaunches run = launches(r.dtype);
+  const GatedBackward b = gated_backward(r, ws);
+  char* const base = (char*)ws;
+  GateDzArgs d;
+  memset(&d, 0, sizeof d);
+  d.dy = r.dY;
+  d.lddy = r.lddy;
+  d.g = r.G;
+  d.u = r.U;
+  d.ldg = r.ldg;
+  d.ldu = r.ldu;
+  d.g_codes = r.g_codes;
+  d.g_scales = r.g_scales;
+  d.u_codes = r.u_codes;
+  d.u_scales = r.u_scales;
+  d.dg = b.has_dz ? base + b.dg_at : nullptr;
+  d.du = b.has_dz ? base + b.du_at : nullptr;
+  d.ldd = b.ldd;
+  d.partial = b.db_runs ? (float*)(base + b.db_at) : nullptr;
+  d.M = r.M;
+  d.N = r.N;
+  d.act = r.activation;
+  d.run = b.db_run;
+  int64_t runs = b.db_runs;
+  if (!runs) {
+    runs = (r.M + 7) / 8 < 4096 ? (r.M + 7) / 8 : 4096;
+    d.run = (r.M + runs - 1) / runs;
+  }
+  e = run.dz(d, runs, s);
+  if (e == hipSuccess && b.db_runs)
+    e = column_sums(d.partial, b.db_runs, r.N, r.dbias_g, r.dbias_u, 1, r.bias_dtype, s);
+  if (e == hipSuccess && r.dWg && r.K && r.x_codes)
+    e = restore_to(r.dtype, r.x_codes, r.x_scales, base + b.x_at, (r.K + 7) / 8 * 8, r.M, r.K, s);
+  if (e == hipSuccess && r.dX && r.K) {
+    LongArgs g;
+    memset(&g, 0, sizeof g);
+    g.y = r.dX;
+    g.ldy = r.lddx;
+    g.out_dt = r.dtype;
+    e = paired_fill(b.dx, b.pdx, g, g.a2, g.b2, base + b.part_at, s);
+    if (e == hipSuccess) e = run.both(b.pdx.tile, b.pdx.direct, b.dx.p.lb, g, s);
+  }
+  if (e == hipSuccess && r.dWg && r.K) {
+    TwoArgs p;
+    memset(&p, 0, sizeof p);
+    const void *a2, *b2;
+    p.one.y = r.dWg;
+    p.one.ldy = r.lddwg;
+    p.one.out_dt = r.dw_dtype;
+    e = paired_fill(b.dw, b.pdw, p.one, a2, b2, base + b.part_at, s);
+    p.two = p.one;
+    p.two.a = a2;
+    p.two.b = b2;
+    p.two.y = r.dWu;
+    p.two.ldy = r.lddwu;
+    if (p.one.partial) p.two.partial += b.dw.p.M * b.dw.p.N * b.pdw.splits;
+    if (e == hipSuccess) e = run.two(b.pdw.tile, b.pdw.direct, p, s);
+  }
+  return e;
+}
+
 }  // namespace
 
 extern "C" {
@@ -314,6 +626,63 @@ int mma_residual_norm_backward(const mma_residual_norm_backward_args* args, void
     err = hipGetLastError();
   }
   return err == hipSuccess ? MMAEMU_OK : hip_fail(err, "mma_residual_norm_backward launch");
+}
+
+int64_t mma_gated_linear_workspace(const mma_gated_linear_args* args) {
+  if (!args || check_gated(*args, 0, nullptr, true) != MMAEMU_OK) return 0;
+  return gated_need(*args);
+}
+
+int mma_gated_linear(const mma_gated_linear_args* args, void* workspace, int64_t workspace_bytes,
+                     void* hip_stream) {
+  if (!args) return MMAEMU_ERR_NULL;
+  const mma_gated_linear_args& r = *args;
+  const int rc = check_gated(r, workspace_bytes, workspace, false);
+  if (rc || r.M == 0 || r.N == 0) return rc;
+  const hipStream_t s = (hipStream_t)hip_stream;
+  GateArgs g;
+  memset(&g, 0, sizeof g);
+  g.bias = r.bias_g;
+  g.bias2 = r.bias_u;
+  g.y = r.Y;
+  g.ldy = r.ldy;
+  g.z = r.G;
+  g.ldz = r.ldg;
+  g.z2 = r.U;
+  g.ldz2 = r.ldu;
+  g.codes = r.g_codes;
+  g.scales = r.g_scales;
+  g.codes2 = r.u_codes;
+  g.scales2 = r.u_scales;
+  g.bias_dt = r.bias_dtype;
+  g.out_dt = r.out_dtype;
+  g.act = r.activation;
+  const Paired q = gated_product(r);
+  const Plan plan = paired_plan(q, r.g_codes != nullptr);
+  const void* a2;
+  (void)hipGetLastError();
+  hipError_t err = paired_fill(q, plan, g, a2, g.b2, workspace, s);
+  if (err == hipSuccess) err = launches(r.dtype).gate(plan.tile, plan.direct, q.p.lb, g, s);
+  return err == hipSuccess ? MMAEMU_OK : hip_fail(err, "mma_gated_linear launch");
+}
+
+int64_t mma_gated_linear_backward_workspace(const mma_gated_linear_backward_args* args) {
+  if (!args || check_gated_backward(*args, 0, nullptr, true) != MMAEMU_OK) return 0;
+  if (args->M == 0 || args->N == 0) return 0;
+  return gated_backward(*args, nullptr).bytes;
+}
+
+int mma_gated_linear_backward(const mma_gated_linear_backward_args* args, void* workspace,
+                              int64_t workspace_bytes, void* hip_stream) {
+  if (!args) return MMAEMU_ERR_NULL;
+  const int rc = check_gated_backward(*args, workspace_bytes, workspace, false);
+  if (rc) return rc;
+  const mma_gated_linear_backward_args& r = *args;
+  if (!(r.dX && r.M && r.K) && !(r.dWg && r.K && r.N) && !((r.dbias_g || r.dbias_u) && r.N))
+    return MMAEMU_OK;
+  (void)hipGetLastError();
+  const hipError_t err = gated_backward_run(r, workspace, (hipStream_t)hip_stream);
+  return err == hipSuccess ? MMAEMU_OK : hip_fail(err, "mma_gated_linear_backward launch");
 }
 
 }  // extern "C"

@@ -67,6 +67,42 @@ struct LinearArgs {
   int bias_dt, out_dt, act;
 };
 
+// Products with more operands (gated.h):
+//   kGate  two right operands of the same shape: a tile has the same columns of
+//          both, the first half of its columns A B's and the second A B2's
+//   kLong  C = A B + A2 B2: an inner size of twice K, in two parts whose
+//          operands have leading dimensions alike
+// (No unnamed type may stand in a kernel's signature: host and device count
+// them apart, and the kernel's name is then another on either side.)
+constexpr int kPlain = 0, kGate = 1, kLong = 2;
+
+struct GateArgs : LinearArgs {
+  const void* b2;
+  const void* bias2;
+  void* z2;
+  int64_t ldz2;
+  uint8_t* codes2;
+  uint8_t* scales2;
+};
+struct LongArgs : LinearArgs {
+  const void* a2;
+  const void* b2;
+};
+template <int MODE>
+struct ArgsOf {
+  using type = LinearArgs;
+};
+template <>
+struct ArgsOf<kGate> {
+  using type = GateArgs;
+};
+template <>
+struct ArgsOf<kLong> {
+  using type = LongArgs;
+};
+template <int MODE>
+using args_t = typename ArgsOf<MODE>::type;
+
 template <int DT>
 struct Mfma;
 template <>
@@ -132,6 +168,11 @@ struct Tile {
   static constexpr int kPerWave = kLoads / NW;
   static_assert(kLoads % NW == 0, "every wave issues the same number of loads");
   static constexpr int kRow = LAYOUT == 0 ? BK / 8 : R / 8;  // chunks of a tile row
+
+  // where load i of a wave goes in the tile
+  static __device__ __forceinline__ uint32_t at(int wave, int i) {
+    return (wave * kPerWave + i) * 1024;
+  }
 
   static __device__ __forceinline__ int swap_of(int r) {
     if constexpr (LAYOUT == 0) return r & 7;
@@ -238,6 +279,57 @@ struct Tile {
     }
   }
 };
+
+// The tiles of two operands behind each other, R / 2 rows (or columns) of
+// each; a wave's FN fragments are FN / 2 of the first and the same ones of the
+// second, so that its sums of both stand in the same lanes.
+template <int R, int BK, int LAYOUT, int NW, int FN>
+struct GateTile {
+  using Half = Tile<R / 2, BK, LAYOUT, NW>;
+  static constexpr int kBytes = 2 * Half::kBytes;
+  static constexpr int kHalf = Half::kPerWave, kPerWave = 2 * kHalf;
+  static_assert(FN % 2 == 0, "fragments of both");
+
+  static __device__ __forceinline__ uint32_t at(int wave, int i) {
+    return i < kHalf ? Half::at(wave, i) : Half::kBytes + Half::at(wave, i - kHalf);
+  }
+  static __device__ __forceinline__ void offsets(int64_t ld, int have, int wave, int lane,
+                                                 uint32_t (&off)[kPerWave]) {
+    uint32_t o[kHalf];
+    Half::offsets(ld, have, wave, lane, o);
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) off[i] = off[kHalf + i] = o[i];
+  }
+  static __device__ __forceinline__ void fetch(const char* tile, const char* tile2, int64_t ld,
+                                               int have, int kn, int wave, int lane,
+                                               u32x4 (&v)[kPerWave]) {
+    u32x4 one[kHalf], two[kHalf];
+    Half::fetch(tile, ld, have, kn, wave, lane, one);
+    Half::fetch(tile2, ld, have, kn, wave, lane, two);
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+      v[i] = one[i];
+      v[kHalf + i] = two[i];
+    }
+  }
+  static __device__ __forceinline__ void put(lds_char* tile, int wave, int lane,
+                                             const u32x4 (&v)[kPerWave]) {
+#pragma unroll
+    for (int i = 0; i < kPerWave; ++i)
+      *(__attribute__((address_space(3))) u32x4*)(tile + at(wave, i) + lane * 16) = v[i];
+  }
+  static __device__ __forceinline__ uint32_t base(int r0, int lane) {
+    return Half::base(r0 / 2, lane);
+  }
+  template <typename F>
+  static __device__ __forceinline__ F frag(const lds_char* tile, uint32_t base, int kk, int i) {
+    return i < FN / 2 ? Half::template frag<F>(tile, base, kk, i)
+                      : Half::template frag<F>(tile + Half::kBytes, base, kk, i - FN / 2);
+  }
+};
+template <int MODE, int R, int BK, int LAYOUT, int NW, int FN>
+using right_tile = std::conditional_t<MODE == kGate, GateTile<R, BK, LAYOUT, NW, FN>,
+                                      Tile<R, BK, LAYOUT, NW>>;
 
 // ------------------------------------------------------------ epilogue
 // Pre-activation, activation, residual and store of V columns (n of them
@@ -413,6 +505,150 @@ __device__ __forceinline__ void store_tile(const LinearArgs& g, const f32x4 (&ac
   }
 }
 
+// The same of a gated product: the first half of a fragment row's columns are
+// the gate's sums, the second the other product's, of the same output columns.
+// A lane takes 8 columns of both.
+template <int DT, int V, int U>
+__device__ __forceinline__ void gate_finish(const GateArgs& g, int64_t m, int step, int64_t c,
+                                            int n, bool all, float (&v)[U * V],
+                                            const float (&u)[U * V]) {
+  using E = elem_t<DT>;
+  auto there = [&](int i) { return all || (m + i * step < g.M && n > 0); };
+  if (g.z) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (!there(i)) continue;
+      float o[V], w[V];
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        o[q] = v[i * V + q];
+        w[q] = u[i * V + q];
+      }
+      store_pack<DT, V>((E*)g.z + (m + i * step) * g.ldz + c, pack<DT, V>(o), n);
+      store_pack<DT, V>((E*)g.z2 + (m + i * step) * g.ldz2 + c, pack<DT, V>(w), n);
+    }
+  }
+  act_all(v, g.act, act_apply);
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (!there(i)) continue;
+    float o[V];
+#pragma unroll
+    for (int q = 0; q < V; ++q) o[q] = v[i * V + q] * u[i * V + q];
+    if (g.out_dt != kFP32)
+      store_pack<DT, V>((E*)g.y + (m + i * step) * g.ldy + c, pack<DT, V>(o), n);
+    else
+      store_pack<kFP32, V>((float*)g.y + (m + i * step) * g.ldy + c, pack<kFP32, V>(o), n);
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void gate_bias(const GateArgs& g, int64_t c, int n, float (&v)[V],
+                                          float (&w)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    v[i] = g.bias && i < n ? load_any(g.bias, c + i, g.bias_dt) : 0.0f;
+    w[i] = g.bias2 && i < n ? load_any(g.bias2, c + i, g.bias_dt) : 0.0f;
+  }
+}
+
+// the checkpoints of both, of V columns of one row
+template <int DT, int V>
+__device__ __forceinline__ void gate_save(const GateArgs& g, int64_t m, int64_t c, int n,
+                                          const float* v, const float* u) {
+  const int64_t at = m * ((g.N + kBlock - 1) / kBlock) + c / kBlock;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float o[V];
+#pragma unroll
+    for (int q = 0; q < V; ++q) o[q] = h ? u[q] : v[q];
+    Codes<V> k;
+    const int s = encode<DT, V>(o, n, k);
+    if (m < g.M && n > 0) {
+      store_codes<V>((h ? g.codes2 : g.codes) + m * g.N + c, k, n);
+      if (c % kBlock == 0) (h ? g.scales2 : g.scales)[at] = (uint8_t)s;
+    }
+  }
+}
+
+template <int DT, int FM, int FN, int PASS>
+__device__ __forceinline__ void gate_store_tile(const GateArgs& g, const f32x4 (&acc)[FM][FN],
+                                                lds_char* mem, int64_t m0, int64_t n0, int lane,
+                                                int split) {
+  using lds_f4 = __attribute__((address_space(3))) f32x4;
+  constexpr int kRow = FN * 64 + 16;
+  constexpr int kLanes = FN, kRows = 64 / kLanes;  // lanes a row, rows at once
+  constexpr int kPassRows = PASS * 16;
+  constexpr int kTurns = (kPassRows + kRows - 1) / kRows;
+  constexpr int U = kTurns < 4 ? kTurns : 4;
+  const int64_t c = n0 + (lane % kLanes) * 8;
+  const int n = g.N - c < 8 ? (int)(g.N - c) : 8;
+  const bool all = m0 + FM * 16 <= g.M && n0 + FN * 8 <= g.N;
+  auto put = [&](int i) {
+#pragma unroll
+    for (int h = 0; h < PASS; ++h)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        *(lds_f4*)(mem + (h * 16 + (lane & 15)) * kRow + j * 64 + (lane >> 4) * 16) =
+            acc[i + h][j];
+  };
+  auto get = [&](int r, int half, float* v) {
+    const lds_f4* const p =
+        (const lds_f4*)(mem + r * kRow + half * (FN * 32) + (lane % kLanes) * 32);
+    const f32x4 lo = p[0], hi = p[1];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = lo[q];
+      v[4 + q] = hi[q];
+    }
+  };
+  float bias[8], bias2[8];
+  if (!g.partial) gate_bias<8>(g, c, n, bias, bias2);
+  float* const out = g.partial + (int64_t)split * g.M * 2 * g.N + c;
+#pragma unroll
+  for (int i = 0; i < FM; i += PASS) {
+    put(i);
+#pragma unroll 1
+    for (int r = lane / kLanes; r < kPassRows; r += U * kRows) {
+      const int64_t m = m0 + i * 16 + r;
+      float v[U * 8], u[U * 8];
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        get(r + q * kRows, 0, v + q * 8);
+        get(r + q * kRows, 1, u + q * 8);
+      }
+      if (g.partial) {
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          const int64_t mq = m + q * kRows;
+          if (mq >= g.M || n <= 0) continue;
+          float o[8], w[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            o[k] = v[q * 8 + k];
+            w[k] = u[q * 8 + k];
+          }
+          store_pack<kFP32, 8>(out + mq * 2 * g.N, pack<kFP32, 8>(o), n);
+          store_pack<kFP32, 8>(out + (mq * 2 + 1) * g.N, pack<kFP32, 8>(w), n);
+        }
+        continue;
+      }
+#pragma unroll
+      for (int q = 0; q < U * 8; ++q) {
+        v[q] += bias[q % 8];
+        u[q] += bias2[q % 8];
+      }
+      if constexpr (FN % 4 == 0) {  // a block's lanes are here together
+        if (g.codes) {
+#pragma unroll
+          for (int q = 0; q < U; ++q) gate_save<DT, 8>(g, m + q * kRows, c, n, v + q * 8, u + q * 8);
+        }
+      }
+      gate_finish<DT, 8, U>(g, m, kRows, c, all ? 8 : n, all, v, u);
+    }
+  }
+}
+
 // Which tile workgroup b takes.  Workgroups go to the 8 XCDs in turn, so
 // workgroup i of an XCD is i * 8 + xcd; each XCD gets a run of consecutive
 // tiles, and tiles run down 8 rows before the next column, so that what
@@ -429,6 +665,21 @@ __device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int b, int& tm
   tn = in / down;
 }
 
+// The whole steps of BK of one split (and the part of a step that a plain or
+// gated product has at its end).  kLong: those of both parts, one after the
+// other; their ends are apart.
+struct Run {
+  int64_t s0, s1;
+};
+template <int BK, int MODE>
+__device__ __forceinline__ Run split_run(int64_t K, int tail, int splits, int split) {
+  int64_t steps = (K + BK - 1) / BK;
+  if constexpr (MODE == kLong) steps = 2 * (steps - (tail ? 1 : 0));
+  const int64_t per = (steps + splits - 1) / splits;
+  const int64_t s0 = split * per;
+  return {s0, s0 + per < steps ? s0 + per : steps};
+}
+
 template <int BM, int BN, int BK, int STAGES>
 constexpr int kRingBytes = STAGES * (BM + BN) * BK * 2;
 
@@ -436,14 +687,15 @@ constexpr int kRingBytes = STAGES * (BM + BN) * BK * 2;
 // CU hide each other's waits.  A ring of STAGES steps, one barrier a step;
 // DIRECT: direct loads, else through registers.
 template <int DT, int BM, int BN, int BK, int WM, int WN, int LA, int LB, int STAGES,
-          bool DIRECT>
-__device__ __forceinline__ void small_product(const LinearArgs& g, int block, int split,
+          bool DIRECT, int MODE = kPlain>
+__device__ __forceinline__ void small_product(const args_t<MODE>& g, int block, int split,
                                               char* smem) {
   constexpr int NW = WM * WN;
-  using TA = Tile<BM, BK, LA, NW>;
-  using TB = Tile<BN, BK, LB, NW>;
-  using F = typename Mfma<DT>::frag;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+  constexpr int kCols = MODE == kGate ? BN / 2 : BN;  // of the output
+  using TA = Tile<BM, BK, LA, NW>;
+  using TB = right_tile<MODE, BN, BK, LB, NW, FN>;
+  using F = typename Mfma<DT>::frag;
   constexpr int kStage = TA::kBytes + TB::kBytes;
   lds_char* const lds = (lds_char*)smem;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
@@ -453,19 +705,23 @@ __device__ __forceinline__ void small_product(const LinearArgs& g, int block, in
   const int wm = wave / WN, wn = wave % WN;
   int tm, tn;
   tile_of(g.tiles_m, g.tiles_n, block, tm, tn);
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * kCols;
   const int have_m = g.M - m0 < BM ? (int)(g.M - m0) : BM;
-  const int have_n = g.N - n0 < BN ? (int)(g.N - n0) : BN;
+  const int have_n = g.N - n0 < kCols ? (int)(g.N - n0) : kCols;
 
   // this split's steps of BK; the last of all may be a part of one
-  const int64_t steps = (g.K + BK - 1) / BK;
-  const int64_t per = (steps + g.splits - 1) / g.splits;
-  const int64_t s0 = split * per;
-  int64_t s1 = s0 + per < steps ? s0 + per : steps;
+  const int tail = g.K % BK ? (int)(g.K % BK) : g.guard ? BK : 0;
+  const Run run = split_run<BK, MODE>(g.K, tail, g.splits, split);
+  const int64_t steps = (g.K + BK - 1) / BK, s0 = run.s0;
+  int64_t s1 = run.s1;
   const int64_t a_step = (LA == 0 ? BK : BK * g.lda) * 2;
   const int64_t b_step = (LB == 0 ? BK : BK * g.ldb) * 2;
-  const char* a = (const char*)g.a + (LA == 0 ? m0 * g.lda : m0) * 2;
-  const char* b = (const char*)g.b + (LB == 0 ? n0 * g.ldb : n0) * 2;
+  const int64_t a_at = (LA == 0 ? m0 * g.lda : m0) * 2, b_at = (LB == 0 ? n0 * g.ldb : n0) * 2;
+  const char* a = (const char*)g.a + a_at;
+  const char* b = (const char*)g.b + b_at;
+  const char *a2 = nullptr, *b2 = nullptr;
+  if constexpr (MODE != kPlain) b2 = (const char*)g.b2 + b_at;
+  if constexpr (MODE == kLong) a2 = (const char*)g.a2 + a_at;
 
   f32x4 acc[FM][FN];
 #pragma unroll
@@ -491,21 +747,54 @@ __device__ __forceinline__ void small_product(const LinearArgs& g, int block, in
     }
   };
 
-  const int tail = g.K % BK ? (int)(g.K % BK) : g.guard ? BK : 0;
-  if (s0 < s1) {
-    u32x4 va[TA::kPerWave], vb[TB::kPerWave];
-    if (s1 == steps && tail) {  // the part of a step, before the others
-      s1 -= 1;
-      TA::fetch(a + s1 * a_step, g.lda, have_m, tail, wave, lane, va);
-      TB::fetch(b + s1 * b_step, g.ldb, have_n, tail, wave, lane, vb);
-      TA::put(lds, wave, lane, va);
-      TB::put(lds + TA::kBytes, wave, lane, vb);
-      __syncthreads();
-      compute(0);
-      __syncthreads();
+  // kn of a step's inner size through registers, from step s of pa and pb on
+  u32x4 va[TA::kPerWave], vb[TB::kPerWave];
+  auto fetch = [&](const char* pa, const char* pb, const char* pb2, int kn) {
+    TA::fetch(pa, g.lda, have_m, kn, wave, lane, va);
+    if constexpr (MODE == kGate)
+      TB::fetch(pb, pb2, g.ldb, have_n, kn, wave, lane, vb);
+    else
+      TB::fetch(pb, g.ldb, have_n, kn, wave, lane, vb);
+  };
+  auto part = [&](const char* pa, const char* pb, const char* pb2) {
+    fetch(pa, pb, pb2, tail);
+    TA::put(lds, wave, lane, va);
+    TB::put(lds + TA::kBytes, wave, lane, vb);
+    __syncthreads();
+    compute(0);
+    __syncthreads();
+  };
+  int until = 0;  // kLong: steps to the second part
+  if constexpr (MODE == kLong) {
+    const int64_t whole = steps - (tail ? 1 : 0);
+    if (tail && split == g.splits - 1) {
+      part(a + whole * a_step, b + whole * b_step, nullptr);
+      part(a2 + whole * a_step, b2 + whole * b_step, nullptr);
     }
-    a += s0 * a_step;
-    b += s0 * b_step;
+    until = s0 < whole ? (int)(whole - s0) : INT32_MAX;
+    a = s0 < whole ? a + s0 * a_step : a2 + (s0 - whole) * a_step;
+    b = s0 < whole ? b + s0 * b_step : b2 + (s0 - whole) * b_step;
+  }
+  auto advance = [&] {
+    a += a_step;
+    b += b_step;
+    if constexpr (MODE == kGate) b2 += b_step;
+    if constexpr (MODE == kLong)
+      if (--until == 0) {
+        a = a2;
+        b = b2;
+      }
+  };
+  if (s0 < s1) {
+    if constexpr (MODE != kLong) {
+      if (s1 == steps && tail) {  // the part of a step, before the others
+        s1 -= 1;
+        part(a + s1 * a_step, b + s1 * b_step, MODE == kGate ? b2 + s1 * b_step : nullptr);
+      }
+      a += s0 * a_step;
+      b += s0 * b_step;
+      if constexpr (MODE == kGate) b2 += s0 * b_step;
+    }
     const int n = (int)(s1 - s0);
     if constexpr (DIRECT) {
       constexpr int kPer = TA::kPerWave + TB::kPerWave;
@@ -516,9 +805,11 @@ __device__ __forceinline__ void small_product(const LinearArgs& g, int block, in
       auto issue = [&] {
         const uint32_t at = lds0 + put * kStage;
         TA::load(a, oa, at, wave);
-        TB::load(b, ob, at + TA::kBytes, wave);
-        a += a_step;
-        b += b_step;
+#pragma unroll
+        for (int i = 0; i < TB::kPerWave; ++i)
+          load_to_lds(uniform(MODE == kGate && i >= TB::kPerWave / 2 ? b2 : b), ob[i],
+                      at + TA::kBytes + TB::at(wave, i));
+        advance();
         put = put + 1 == STAGES ? 0 : put + 1;
       };
       for (int t = 0; t < STAGES - 1 && t < n; ++t) issue();
@@ -538,19 +829,14 @@ __device__ __forceinline__ void small_product(const LinearArgs& g, int block, in
       }
     } else {
       if (n > 0) {
-        TA::fetch(a, g.lda, have_m, BK, wave, lane, va);
-        TB::fetch(b, g.ldb, have_n, BK, wave, lane, vb);
+        fetch(a, b, b2, BK);
         TA::put(lds, wave, lane, va);
         TB::put(lds + TA::kBytes, wave, lane, vb);
       }
       __syncthreads();
       for (int t = 0; t < n; ++t) {
-        a += a_step;
-        b += b_step;
-        if (t + 1 < n) {
-          TA::fetch(a, g.lda, have_m, BK, wave, lane, va);
-          TB::fetch(b, g.ldb, have_n, BK, wave, lane, vb);
-        }
+        advance();
+        if (t + 1 < n) fetch(a, b, b2, BK);
         compute(t & 1);
         if (t + 1 < n) {
           lds_char* const to = lds + ((t + 1) & 1) * kStage;
@@ -565,8 +851,13 @@ __device__ __forceinline__ void small_product(const LinearArgs& g, int block, in
   constexpr int kPass = FM > 1 ? 2 : 1;
   static_assert(NW * kStoreBytes<FN, kPass> <= STAGES * kStage, "the epilogue's LDS");
   __syncthreads();
-  store_tile<DT, FM, FN, kPass>(g, acc, lds + wave * kStoreBytes<FN, kPass>, m0 + wm * (BM / WM),
-                                n0 + wn * (BN / WN), lane, split);
+  lds_char* const mem = lds + wave * kStoreBytes<FN, kPass>;
+  if constexpr (MODE == kGate)
+    gate_store_tile<DT, FM, FN, kPass>(g, acc, mem, m0 + wm * (BM / WM), n0 + wn * (kCols / WN),
+                                       lane, split);
+  else
+    store_tile<DT, FM, FN, kPass>(g, acc, mem, m0 + wm * (BM / WM), n0 + wn * (BN / WN), lane,
+                                  split);
 }
 
 template <int DT, int BM, int BN, int BK, int WM, int WN, int LA, int LB, int STAGES,
@@ -654,19 +945,28 @@ __global__ __launch_bounds__(256, 2) void linear_pair_kernel(PairArgs p) {
 // a whole 128-byte line; steps of 32 with a ring of four stages kept the
 // vector memory pipe busier than the products (8192^3, both operands with K
 // fastest: 922 us against 856).
-template <int DT, int LA, int LB, int BM, int BN, int STAGES>
-__global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
+template <int BM, int BN, int STAGES>
+struct Wide {
+  static constexpr int FM = BM / 32, FN = BN / 32;
+  static constexpr int kStage = (BM + BN) * 64 * 2;
+  static constexpr int kPass = FM < 8 ? 2 : 4;  // of the epilogue
+  static constexpr int kBytes = STAGES * kStage > 4 * kStoreBytes<FN, kPass>
+                                    ? STAGES * kStage
+                                    : 4 * kStoreBytes<FN, kPass>;
+};
+
+template <int DT, int LA, int LB, int BM, int BN, int STAGES, int MODE>
+__device__ __forceinline__ void wide_product(const args_t<MODE>& g, int block, int split,
+                                             char* smem) {
   constexpr int BK = 64, NW = 4, FM = BM / 32, FN = BN / 32;
+  constexpr int kCols = MODE == kGate ? BN / 2 : BN;  // of the output
   using TA = Tile<BM, BK, LA, NW>;
-  using TB = Tile<BN, BK, LB, NW>;
+  using TB = right_tile<MODE, BN, BK, LB, NW, FN>;
   using F = typename Mfma<DT>::frag;
   constexpr int kStage = TA::kBytes + TB::kBytes;
   constexpr int kLoads = TA::kPerWave + TB::kPerWave;  // of a wave and step
-  constexpr int kPass = FM < 8 ? 2 : 4;  // of the epilogue
-  constexpr int kBytes = STAGES * kStage > NW * kStoreBytes<FN, kPass>
-                             ? STAGES * kStage
-                             : NW * kStoreBytes<FN, kPass>;
-  __shared__ __attribute__((aligned(1024))) char smem[kBytes];
+  constexpr int kPass = Wide<BM, BN, STAGES>::kPass;
+  static_assert(kStage == Wide<BM, BN, STAGES>::kStage, "");
   lds_char* const lds = (lds_char*)smem;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
@@ -674,18 +974,22 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   int tm, tn;
-  tile_of(g.tiles_m, g.tiles_n, blockIdx.x, tm, tn);
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  tile_of(g.tiles_m, g.tiles_n, block, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * kCols;
   const int have_m = g.M - m0 < BM ? (int)(g.M - m0) : BM;
-  const int have_n = g.N - n0 < BN ? (int)(g.N - n0) : BN;
-  const int64_t steps = (g.K + BK - 1) / BK;
-  const int64_t per = (steps + g.splits - 1) / g.splits;
-  const int64_t s0 = blockIdx.y * per;
-  int64_t s1 = s0 + per < steps ? s0 + per : steps;
+  const int have_n = g.N - n0 < kCols ? (int)(g.N - n0) : kCols;
+  const int tail = g.K % BK ? (int)(g.K % BK) : g.guard ? BK : 0;
+  const Run run = split_run<BK, MODE>(g.K, tail, g.splits, split);
+  const int64_t steps = (g.K + BK - 1) / BK, s0 = run.s0;
+  int64_t s1 = run.s1;
   const int64_t a_step = (LA == 0 ? BK : BK * g.lda) * 2;
   const int64_t b_step = (LB == 0 ? BK : BK * g.ldb) * 2;
-  const char* a = (const char*)g.a + (LA == 0 ? m0 * g.lda : m0) * 2;
-  const char* b = (const char*)g.b + (LB == 0 ? n0 * g.ldb : n0) * 2;
+  const int64_t a_at = (LA == 0 ? m0 * g.lda : m0) * 2, b_at = (LB == 0 ? n0 * g.ldb : n0) * 2;
+  const char* a = (const char*)g.a + a_at;
+  const char* b = (const char*)g.b + b_at;
+  const char *a2 = nullptr, *b2 = nullptr;
+  if constexpr (MODE != kPlain) b2 = (const char*)g.b2 + b_at;
+  if constexpr (MODE == kLong) a2 = (const char*)g.a2 + a_at;
 
   f32x4 acc[FM][FN];
 #pragma unroll
@@ -695,13 +999,14 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
   const uint32_t base_a = TA::base(wm * (BM / 2), lane);
   const uint32_t base_b = TB::base(wn * (BN / 2), lane) + TA::kBytes;
 
-  const int tail = g.K % BK ? (int)(g.K % BK) : g.guard ? BK : 0;
-  if (s0 < s1 && s1 == steps && tail) {  // the part of a step, before the others
-    s1 -= 1;
+  auto part = [&](const char* pa, const char* pb, const char* pb2) {
     u32x4 va[TA::kPerWave], vb[TB::kPerWave];
-    TA::fetch(a + s1 * a_step, g.lda, have_m, tail, wave, lane, va);
+    TA::fetch(pa, g.lda, have_m, tail, wave, lane, va);
     TA::put(lds, wave, lane, va);
-    TB::fetch(b + s1 * b_step, g.ldb, have_n, tail, wave, lane, vb);
+    if constexpr (MODE == kGate)
+      TB::fetch(pb, pb2, g.ldb, have_n, tail, wave, lane, vb);
+    else
+      TB::fetch(pb, g.ldb, have_n, tail, wave, lane, vb);
     TB::put(lds + TA::kBytes, wave, lane, vb);
     __syncthreads();
 #pragma unroll
@@ -714,21 +1019,38 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
           acc[i][j] = Mfma<DT>::run(fb, TA::template frag<F>(lds, base_a, kk, i), acc[i][j]);
       }
     __syncthreads();
+  };
+  int until = 0;  // kLong: steps to the second part
+  if constexpr (MODE == kLong) {
+    const int64_t whole = steps - (tail ? 1 : 0);
+    if (tail && split == g.splits - 1) {
+      part(a + whole * a_step, b + whole * b_step, nullptr);
+      part(a2 + whole * a_step, b2 + whole * b_step, nullptr);
+    }
+    until = s0 < whole ? (int)(whole - s0) : INT32_MAX;
+    a = s0 < whole ? a + s0 * a_step : a2 + (s0 - whole) * a_step;
+    b = s0 < whole ? b + s0 * b_step : b2 + (s0 - whole) * b_step;
+  } else if (s0 < s1 && s1 == steps && tail) {  // the part of a step, before the others
+    s1 -= 1;
+    part(a + s1 * a_step, b + s1 * b_step, MODE == kGate ? b2 + s1 * b_step : nullptr);
   }
   const int n = (int)(s1 - s0);
   if (n > 0) {
-    a += s0 * a_step;
-    b += s0 * b_step;
+    if constexpr (MODE != kLong) {
+      a += s0 * a_step;
+      b += s0 * b_step;
+      if constexpr (MODE == kGate) b2 += s0 * b_step;
+    }
     uint32_t oa[TA::kPerWave], ob[TB::kPerWave];
     TA::offsets(g.lda, have_m, wave, lane, oa);
     TB::offsets(g.ldb, have_n, wave, lane, ob);
     // load i of a step, into the stage at `to`
     auto issue = [&](int i, uint32_t to) {
       if (i < TB::kPerWave)
-        load_to_lds(uniform(b), ob[i], to + TA::kBytes + (wave * TB::kPerWave + i) * 1024);
+        load_to_lds(uniform(MODE == kGate && i >= TB::kPerWave / 2 ? b2 : b), ob[i],
+                    to + TA::kBytes + TB::at(wave, i));
       else
-        load_to_lds(uniform(a), oa[i - TB::kPerWave],
-                    to + (wave * TA::kPerWave + i - TB::kPerWave) * 1024);
+        load_to_lds(uniform(a), oa[i - TB::kPerWave], to + TA::at(wave, i - TB::kPerWave));
     };
     // one step further; past the last one the same again (loaded, not used)
     int left = n;
@@ -736,6 +1058,12 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
       const bool more = --left > 0;
       a += more ? a_step : 0;
       b += more ? b_step : 0;
+      if constexpr (MODE == kGate) b2 += more ? b_step : 0;
+      if constexpr (MODE == kLong)
+        if (more && --until == 0) {
+          a = a2;
+          b = b2;
+        }
     };
     auto read = [&](F (&fa)[FM], F (&fb)[FN], int q, int kk, const lds_char* from) {
       if (q < FN)
@@ -804,8 +1132,19 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
     wait_loads<0>();
   }
   __syncthreads();
-  store_tile<DT, FM, FN, kPass>(g, acc, lds + wave * kStoreBytes<FN, kPass>,
-                                m0 + wm * (BM / 2), n0 + wn * (BN / 2), lane, blockIdx.y);
+  lds_char* const mem = lds + wave * kStoreBytes<FN, kPass>;
+  if constexpr (MODE == kGate)
+    gate_store_tile<DT, FM, FN, kPass>(g, acc, mem, m0 + wm * (BM / 2), n0 + wn * (kCols / 2),
+                                       lane, split);
+  else
+    store_tile<DT, FM, FN, kPass>(g, acc, mem, m0 + wm * (BM / 2), n0 + wn * (BN / 2), lane,
+                                  split);
+}
+
+template <int DT, int LA, int LB, int BM, int BN, int STAGES>
+__global__ __launch_bounds__(256, 1) void linear_wide_kernel(LinearArgs g) {
+  __shared__ __attribute__((aligned(1024))) char smem[Wide<BM, BN, STAGES>::kBytes];
+  wide_product<DT, LA, LB, BM, BN, STAGES, kPlain>(g, blockIdx.x, blockIdx.y, smem);
 }
 
 // The end of a product of up to ROWS rows: BN columns' [wave][row][column]

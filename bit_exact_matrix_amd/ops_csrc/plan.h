@@ -228,5 +228,111 @@ inline int64_t product_bytes(const Product& p, const Plan& q) {
          copy_bytes(q.copy_b, stored(p.lb, p.N, p.K));
 }
 
+// ------------------------------------------- products of a gated layer
+// kGated  C, C2 (M x N each) = A B, A B2, a tile with the same columns of both
+// kSummed C = A B + A2 B2
+// kApart  C = A B and C2 = A2 B2, in one launch
+// of inner size K each (linear.h and gated.h have the kernels).  Operands of a
+// pair have the same layout; where their leading dimensions differ both are
+// copied, as where their rows do not start on 16 bytes.
+enum { kGated = 0, kSummed = 1, kApart = 2 };
+struct Paired {
+  int kind;
+  Product p;
+  const void *a2, *b2;  // a2 NULL: a itself; b2 NULL: b itself
+  int64_t lda2, ldb2;
+};
+
+// The most columns of a tile's right operands, each (for few rows the gated
+// tile is twice as wide as a plain one).
+inline int paired_columns(int kind, int tile) {
+  return kind == kGated ? (tile == kTileFew ? 64 : kTileShape[tile].bn / 2) : kTileShape[tile].bn;
+}
+
+inline Plan paired_plan(const Paired& q, bool saves) {
+  const Product& p = q.p;
+  Plan r;
+  // a kernel has one leading dimension for both of a pair
+  const bool apart_a = q.a2 && q.lda2 != p.lda, apart_b = q.b2 && q.ldb2 != p.ldb;
+  const bool a16 = !apart_a && aligned(p.a, 16) && p.lda % 8 == 0 && aligned(q.a2, 16);
+  const bool b16 = !apart_b && aligned(p.b, 16) && p.ldb % 8 == 0 && aligned(q.b2, 16);
+  const Stored sa = stored(p.la, p.M, p.K), sb = stored(p.lb, p.N, p.K);
+  enum Load { kAsItIs, kCopied, kNot };
+  auto load_a = [&](int t) {
+    const TileShape& s = kTileShape[t];
+    return a16 && in_reach(p.la, s.bm, p.M, s.bk, p.lda) ? kAsItIs
+           : in_reach(p.la, s.bm, p.M, s.bk, sa.ld)      ? kCopied
+                                                         : kNot;
+  };
+  auto load_b = [&](int t) {
+    const int64_t most = paired_columns(q.kind, t), bk = kTileShape[t].bk;
+    return b16 && in_reach(p.lb, most, p.N, bk, p.ldb) ? kAsItIs
+           : in_reach(p.lb, most, p.N, bk, sb.ld)      ? kCopied
+                                                       : kNot;
+  };
+  // what one tile's product takes twice
+  const int64_t times = q.kind == kApart ? 2 : 1, parts = q.kind == kSummed ? 2 : 1;
+  const int64_t sums = q.kind == kSummed ? 1 : 2;  // FP32 sums of an output place
+  const int env_tile = env_int("MMAOPS_LINEAR_TILE", 0, kTiles - 1);
+  const int env_splits = env_int("MMAOPS_LINEAR_SPLITS", 1, 4096);
+  const bool few_as_is = load_a(kTileFew) == kAsItIs && load_b(kTileFew) == kAsItIs;
+  r.tile = kTileFew;
+  r.splits = 1;
+  r.direct = false;
+  r.copy_a = r.copy_b = false;
+  double best = 1e300;
+  for (int any = 0; any <= 1 && best == 1e300; ++any)
+    for (int v = kTileSmall; v <= kTileFew + 1; ++v) {  // the last: few rows through registers
+      const int t = v < kTileFew ? v : kTileFew;
+      const bool direct = v <= kTileFew;
+      if (any                ? t != kTileFew
+          : env_tile >= 0    ? t != (env_tile < kTileFew ? kTileSmall : kTileFew)
+          : t == kTileFew    ? p.M > 128
+                             : p.M <= 16)
+        continue;
+      const Load a = load_a(t), b = load_b(t);
+      if (direct ? a == kNot || b == kNot : !any && few_as_is) continue;
+      const bool copy_a = direct ? a == kCopied : apart_a;
+      const bool copy_b = direct ? b == kCopied : apart_b;
+      const double copies = (copy_a ? copy_time(p.M * p.K * (q.a2 ? 2 : 1)) : 0.0) +
+                            (copy_b ? copy_time(p.N * p.K * (q.b2 ? 2 : 1)) : 0.0);
+      const int64_t cols = paired_columns(q.kind, t), bk = kTileShape[t].bk;
+      const int64_t steps = (p.K + bk - 1) / bk * parts;
+      const int64_t n = (p.M + kTileShape[t].bm - 1) / kTileShape[t].bm * ((p.N + cols - 1) / cols);
+      for (int s = 1; s <= 32; s += s < 4 ? 1 : s / 2) {
+        const int k = env_splits >= 0 ? (int)(env_splits < steps ? env_splits : steps) : s;
+        if (env_splits < 0 && s > 1 && steps / s < (direct ? 4 : 1)) break;
+        const int64_t run = (steps + s - 1) / s;
+        const double time = (direct ? tile_time(t, n * s * times, run)
+                                    : few_through_registers_time(n * s * times, run)) +
+                            copies + (s > 1 ? join_time(p.M, p.N * sums, s) : 0.0);
+        if (time < best) {
+          best = time;
+          r.tile = t;
+          r.direct = direct;
+          r.copy_a = copy_a;
+          r.copy_b = copy_b;
+          r.splits = k < 1 ? 1 : k;
+        }
+        if (env_splits >= 0) break;
+      }
+    }
+  r.guard = r.direct && ((p.la == 1 && p.M % 8 && !r.copy_a) ||
+                         (p.lb == 1 && p.N % 8 && !r.copy_b));
+  // a wave of the gated 64 x 64 tile has 16 columns of each, half a block
+  r.partial = r.splits > 1 || (saves && (r.tile == kTileSmall || r.tile == kTileFew));
+  return r;
+}
+
+// What it takes of the workspace: the partial sums, then the copies.
+inline int64_t paired_partial_bytes(const Paired& q, const Plan& r) {
+  return r.partial ? up256(q.p.M * q.p.N * r.splits * 4 * (q.kind == kSummed ? 1 : 2)) : 0;
+}
+inline int64_t paired_bytes(const Paired& q, const Plan& r) {
+  return paired_partial_bytes(q, r) +
+         copy_bytes(r.copy_a, stored(q.p.la, q.p.M, q.p.K)) * (q.a2 ? 2 : 1) +
+         copy_bytes(r.copy_b, stored(q.p.lb, q.p.N, q.p.K)) * (q.b2 ? 2 : 1);
+}
+
 }  // namespace mmaops
 #endif

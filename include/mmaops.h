@@ -26,6 +26,10 @@
  *   mma_linear_backward       dz = dY act'(z), db = sum over rows of dz,
  *                             dX = dz W^T, dW = X^T dz
  *   mma_checkpoint, mma_restore   x to 8 bits and back
+ *   mma_gated_linear          g = X Wg + bg, u = X Wu + bu, Y = act(g) u
+ *   mma_gated_linear_backward dg = dY u act'(g), du = dY act(g), their sums
+ *                             over the rows, dX = dg Wg^T + du Wu^T,
+ *                             dWg = X^T dg, dWu = X^T du
  *   mma_dropout               y = m x / (1 - p) + residual, m 0 with
  *                             probability p, else 1; its backward pass is
  *                             the same of dY
@@ -211,6 +215,86 @@ typedef struct {
 int mma_linear_backward(const mma_linear_backward_args *args, void *workspace,
                         int64_t workspace_bytes, void *hip_stream);
 int64_t mma_linear_backward_workspace(const mma_linear_backward_args *args);
+
+/* Y = act(X Wg + bias_g) (X Wu + bias_u), the weights stored alike as in
+ * mma_linear, with leading dimensions of their own. */
+typedef struct {
+  int32_t dtype;        /* of X and the weights: FP16 or BF16 */
+  int32_t out_dtype;    /* of Y: dtype or FP32 */
+  int32_t bias_dtype;   /* dtype or FP32 */
+  int32_t activation;   /* MMAOPS_ACT_... */
+  int32_t w_transposed; /* 0 or 1 */
+  int32_t reserved;     /* 0 */
+  int64_t M, N, K;
+  const void *X;
+  int64_t ldx;
+  const void *Wg;
+  int64_t ldwg;
+  const void *Wu;
+  int64_t ldwu;
+  const void *bias_g;   /* N values, or NULL */
+  const void *bias_u;
+  void *Y;
+  int64_t ldy;
+  void *G;              /* both NULL, or M x N of dtype each: g and u */
+  int64_t ldg;
+  void *U;
+  int64_t ldu;
+  uint8_t *g_codes;     /* all four NULL, or the checkpoints of g and u */
+  uint8_t *g_scales;
+  uint8_t *u_codes;
+  uint8_t *u_scales;
+} mma_gated_linear_args;
+
+int mma_gated_linear(const mma_gated_linear_args *args, void *workspace, int64_t workspace_bytes,
+                     void *hip_stream);
+int64_t mma_gated_linear_workspace(const mma_gated_linear_args *args);
+
+/* Its backward pass.  X, and g and u together: matrices or checkpoints; both
+ * g and u are read whatever the activation.  dX, dWg and dWu, dbias_g, dbias_u:
+ * any of them NULL to leave it out (dWg and dWu both or neither).  dg and du
+ * enter the products rounded to dtype (in FP16 an infinity past its range);
+ * the biases' gradients sum them before that.  An infinity in G or U, past
+ * the range of its 16 bits, stands for a large number. */
+typedef struct {
+  int32_t dtype;        /* of dY, X, the weights, G, U and dX */
+  int32_t dw_dtype;     /* of dWg and dWu: dtype or FP32 */
+  int32_t bias_dtype;   /* of dbias_g and dbias_u: dtype or FP32 */
+  int32_t activation;
+  int32_t w_transposed; /* of the weights and their gradients */
+  int32_t reserved;     /* 0 */
+  int64_t M, N, K;
+  const void *dY;       /* M x N */
+  int64_t lddy;
+  const void *X;        /* M x K, or NULL with x_codes and x_scales */
+  int64_t ldx;
+  const uint8_t *x_codes;
+  const uint8_t *x_scales;
+  const void *Wg;
+  int64_t ldwg;
+  const void *Wu;
+  int64_t ldwu;
+  const void *G;        /* M x N each, or NULL with the four below */
+  int64_t ldg;
+  const void *U;
+  int64_t ldu;
+  const uint8_t *g_codes;
+  const uint8_t *g_scales;
+  const uint8_t *u_codes;
+  const uint8_t *u_scales;
+  void *dX;             /* M x K */
+  int64_t lddx;
+  void *dWg;            /* stored as the weights are */
+  int64_t lddwg;
+  void *dWu;
+  int64_t lddwu;
+  void *dbias_g;        /* N values each */
+  void *dbias_u;
+} mma_gated_linear_backward_args;
+
+int mma_gated_linear_backward(const mma_gated_linear_backward_args *args, void *workspace,
+                              int64_t workspace_bytes, void *hip_stream);
+int64_t mma_gated_linear_backward_workspace(const mma_gated_linear_backward_args *args);
 
 /* Y = drop(X) + residual (rows x cols of dtype; residual may be NULL); p in
  * [0, 1].  With dY as X and no residual, the gradient of X. */

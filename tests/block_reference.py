@@ -4,7 +4,8 @@ ops_reference: U = 2^-24, a row or column sum has a depth of at most DEPTH)."""
 import numpy as np
 import torch
 
-from ops_reference import DEPTH, ROUND, TINY, U  # noqa: F401
+import ops_reference
+from ops_reference import DEPTH, ROUND, TINY, U
 
 
 # ---------------------------------------------------------------- dropout
@@ -172,3 +173,38 @@ def residual_norm_backward(dr, dh, r, branch, p, stats, post, pre, scale, m):
         val["post_weight"], off["post_weight"] = g * s1, g.abs() * e1 + U * (g * s1).abs()
         val["post_bias"], off["post_bias"] = g * s0, g.abs() * e0 + U * (g * s0).abs()
     return val, off
+
+
+# ------------------------------------------------------------ gated layer
+def gated_linear(x, wg, wu, bg, bu, act):
+    """(y, g, u, and their bounds)."""
+    g, _, eg, _ = ops_reference.linear(x, wg, bg, "none", None)
+    u, _, eu, _ = ops_reference.linear(x, wu, bu, "none", None)
+    a = ops_reference.act(g, act)
+    ea = eg if act == "none" else (ops_reference.STEEP * eg
+                                   + ops_reference.EVAL * (g.abs() + 1))
+    return a * u, g, u, u.abs() * ea + a.abs() * eu + ea * eu + U * (a * u).abs(), eg, eu
+
+
+def gated_linear_backward(dy, x, wg, wu, g, u, act, dtype):
+    """dx, dw_gate, dw_up, dbias_gate, dbias_up and their bounds; x, g and u in
+    float64 already."""
+    dy, wg, wu = dy.double(), wg.double(), wu.double()
+    m, n = dy.shape
+    a, slope = ops_reference.act(g, act), ops_reference.act_slope(g, act)
+    ev = 0.0 if act == "none" else ops_reference.EVAL * (g.abs() + 1)
+    dg, du = dy * u * slope, dy * a
+    eg, eu = (dy * u).abs() * ev + 3 * U * dg.abs(), dy.abs() * ev + U * du.abs()
+    # the products take both rounded to the operands' type
+    rg = eg + ROUND[dtype] * (dg.abs() + eg) + TINY[dtype]
+    ru = eu + ROUND[dtype] * (du.abs() + eu) + TINY[dtype]
+    ag, au, xa = dg.abs() + rg, du.abs() + ru, x.abs()
+    dx = dg @ wg.t() + du @ wu.t()
+    ex = (rg @ wg.abs().t() + ru @ wu.abs().t()
+          + (2 * n + 64) * U * (ag @ wg.abs().t() + au @ wu.abs().t()))
+    values = dx, x.t() @ dg, x.t() @ du, dg.sum(0), du.sum(0)
+    bounds = (ex, xa.t() @ rg + (m + 64) * U * (xa.t() @ ag),
+              xa.t() @ ru + (m + 64) * U * (xa.t() @ au),
+              eg.sum(0) + DEPTH * U * (dg.abs() + eg).sum(0),
+              eu.sum(0) + DEPTH * U * (du.abs() + eu).sum(0))
+    return values, bounds

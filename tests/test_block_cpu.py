@@ -137,3 +137,96 @@ def test_structures_are_what_the_binding_packs(tmp_path):
                     os.path.join(ROOT, "include"), str(src), "-o", exe], check=True)
     out = subprocess.run([exe], capture_output=True, text=True).stdout.split()
     assert out == [str(s.size) for s in (block._JOIN, block._JOIN_BACKWARD)]
+
+
+# ------------------------------------------------------------ gated layer
+GATED = ("dtype out_dtype bias_dtype activation w_transposed reserved M N K X ldx Wg ldwg Wu ldwu "
+         "bias_g bias_u Y ldy G ldg U ldu g_codes g_scales u_codes u_scales").split()
+MORE = tuple(i << 36 for i in range(24, 32))
+GATED_OK = dict(zip(GATED, (1, 1, 1, 4, 0, 0, 100, 96, 64, X, 64, W, 96, B, 96, R, S, Y, 96, C, 96,
+                            P, 96, *MORE[:4])))
+
+
+def _gated(change, ws=MORE[4], ws_bytes=1 << 30):
+    v = dict(GATED_OK, **change)
+    return ops.mma_gated_linear(block._GATED.pack(*(v[k] for k in GATED)), ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(dtype=3), DTYPE), (dict(out_dtype=0), DTYPE), (dict(bias_dtype=0), DTYPE),
+    (dict(activation=5), UNSUPPORTED), (dict(w_transposed=2), UNSUPPORTED),
+    (dict(reserved=1), UNSUPPORTED), (dict(M=-1), SHAPE), (dict(N=1 << 31), SHAPE),
+    (dict(M=1 << 27, N=1 << 27), SHAPE), (dict(ldx=63), SHAPE), (dict(ldwg=95), SHAPE),
+    (dict(ldwu=95), SHAPE), (dict(w_transposed=1, ldwu=63), SHAPE), (dict(ldy=95), SHAPE),
+    (dict(ldg=95), SHAPE), (dict(ldu=95), SHAPE), (dict(X=0), NULL), (dict(Wg=0), NULL),
+    (dict(Wu=0), NULL), (dict(Y=0), NULL), (dict(U=0), NULL), (dict(g_codes=0), NULL),
+    (dict(u_scales=0), NULL), (dict(X=X + 1), ALIGN), (dict(Wu=B + 1), ALIGN),
+    (dict(bias_u=S + 1), ALIGN), (dict(G=C + 1), ALIGN), (dict(Y=X), ALIAS), (dict(G=B), ALIAS),
+    (dict(U=C + 2), ALIAS), (dict(u_codes=MORE[0] + 7), ALIAS), (dict(M=0), OK),
+    (dict(N=0, ldwg=0, ldwu=0, ldy=0, ldg=0, ldu=0), OK),
+])
+def test_gated_linear_argument_errors(change, code):
+    assert _gated(change) == code
+
+
+def test_gated_linear_workspace_is_checked():
+    few = dict(M=4, N=4096, K=16384, ldx=16384, ldwg=4096, ldwu=4096, ldy=4096, ldg=4096, ldu=4096)
+    v = dict(GATED_OK, **few)
+    need = ops.mma_gated_linear_workspace(block._GATED.pack(*(v[k] for k in GATED)))
+    assert need > 0 and need % 256 == 0
+    assert _gated(few, None, 0) == SCRATCH and _gated(few, MORE[4], need - 1) == SCRATCH
+    assert _gated(few, MORE[4] + 16, need) == ALIGN and _gated(few, Y, need) == ALIAS
+    assert ops.mma_gated_linear(None, None, 0, None) == NULL
+    assert ops.mma_gated_linear_workspace(None) == 0
+
+
+GATED_B = ("dtype dw_dtype bias_dtype activation w_transposed reserved M N K dY lddy X ldx x_codes "
+           "x_scales Wg ldwg Wu ldwu G ldg U ldu g_codes g_scales u_codes u_scales dX lddx dWg "
+           "lddwg dWu lddwu dbias_g dbias_u").split()
+GATED_B_OK = dict(zip(GATED_B, (1, 1, 1, 4, 0, 0, 100, 96, 64, Y, 96, X, 64, 0, 0, W, 96, B, 96, C,
+                                96, P, 96, 0, 0, 0, 0, R, 64, S, 96, Z, 96, *MORE[:2])))
+
+
+def _gated_b(change, ws=MORE[4], ws_bytes=1 << 30):
+    v = dict(GATED_B_OK, **change)
+    return ops.mma_gated_linear_backward(block._GATED_BACKWARD.pack(*(v[k] for k in GATED_B)), ws,
+                                         ws_bytes, None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(dtype=3), DTYPE), (dict(dw_dtype=0), DTYPE), (dict(bias_dtype=2), DTYPE),
+    (dict(activation=-1), UNSUPPORTED), (dict(reserved=3), UNSUPPORTED), (dict(K=-1), SHAPE),
+    (dict(lddy=95), SHAPE), (dict(ldx=63), SHAPE), (dict(ldwu=95), SHAPE), (dict(ldu=95), SHAPE),
+    (dict(lddx=63), SHAPE), (dict(lddwg=95), SHAPE), (dict(lddwu=95), SHAPE), (dict(dY=0), NULL),
+    (dict(X=0), NULL), (dict(Wg=0), NULL), (dict(Wu=0), NULL), (dict(G=0), NULL), (dict(U=0), NULL),
+    (dict(dWu=0), NULL), (dict(G=0, U=0), NULL), (dict(g_codes=MORE[5]), NULL),
+    (dict(x_codes=MORE[5], x_scales=MORE[6]), NULL),
+    (dict(G=0, U=0, g_codes=MORE[5], g_scales=MORE[6], u_codes=MORE[7]), NULL),
+    (dict(dY=Y + 1), ALIGN), (dict(dw_dtype=3, dWu=Z + 2), ALIGN), (dict(dbias_u=MORE[1] + 1), ALIGN),
+    (dict(dX=Y), ALIAS), (dict(dWg=B), ALIAS), (dict(dWu=S + 64), ALIAS),
+    (dict(dbias_u=MORE[0] + 2), ALIAS), (dict(dbias_g=P), ALIAS),
+    (dict(dX=0, dWg=0, dWu=0, dbias_g=0, dbias_u=0), OK),
+])
+def test_gated_linear_backward_argument_errors(change, code):
+    assert _gated_b(change) == code
+
+
+def test_gated_linear_backward_workspace_is_checked():
+    args = block._GATED_BACKWARD.pack(*(GATED_B_OK[k] for k in GATED_B))
+    need = ops.mma_gated_linear_backward_workspace(args)
+    assert need >= 2 * 100 * 96 * 2
+    assert _gated_b({}, None, 0) == SCRATCH and _gated_b({}, MORE[4], need - 1) == SCRATCH
+    assert _gated_b({}, MORE[4] + 8, need) == ALIGN and _gated_b({}, W, need) == ALIAS
+    assert ops.mma_gated_linear_backward(None, None, 0, None) == NULL
+    assert ops.mma_gated_linear_backward_workspace(None) == 0
+
+
+def test_gated_structures_are_what_the_binding_packs(tmp_path):
+    src, exe = tmp_path / "sizes.c", str(tmp_path / "sizes")
+    src.write_text('#include <stdio.h>\n#include "mmaops.h"\nint main(void) {\n'
+                   '  printf("%zu %zu\\n", sizeof(mma_gated_linear_args),\n'
+                   "         sizeof(mma_gated_linear_backward_args));\n  return 0;\n}\n")
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-pedantic", "-Werror", "-I",
+                    os.path.join(ROOT, "include"), str(src), "-o", exe], check=True)
+    out = subprocess.run([exe], capture_output=True, text=True).stdout.split()
+    assert out == [str(s.size) for s in (block._GATED, block._GATED_BACKWARD)]
