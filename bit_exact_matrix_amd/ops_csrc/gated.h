@@ -27,10 +27,28 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void joint_kernel(args_t<MODE> g) {
   small_product<DT, BM, BN, BK, WM, WN, 0, LB, STAGES, DIRECT, MODE>(g, block, blockIdx.y, smem);
 }
 
+template <int DT, int BM, int BN, int LB, int STAGES, int MODE>
+__global__ __launch_bounds__(256, 1) void joint_wide_kernel(args_t<MODE> g) {
+  __shared__ __attribute__((aligned(1024))) char smem[Wide<BM, BN, STAGES>::kBytes];
+  const int block = (int)(blockIdx.x + blockIdx.z * (uint32_t)g.grid_x);
+  if (block >= g.tiles_m * g.tiles_n) return;  // the whole workgroup
+  wide_product<DT, 0, LB, BM, BN, STAGES, MODE>(g, block, blockIdx.y, smem);
+}
+
 // Two products of the same sizes and layouts, one's tiles after the other's.
 struct TwoArgs {
   LinearArgs one, two;
 };
+
+template <int DT, int BM, int BN, int STAGES>
+__global__ __launch_bounds__(256, 1) void two_wide_kernel(TwoArgs p) {
+  __shared__ __attribute__((aligned(1024))) char smem[Wide<BM, BN, STAGES>::kBytes];
+  const int n = p.one.tiles_m * p.one.tiles_n;
+  const int64_t block = blockIdx.x + (int64_t)blockIdx.z * p.one.grid_x;
+  if (block >= 2 * (int64_t)n) return;  // the whole workgroup
+  wide_product<DT, 1, 1, BM, BN, STAGES, kPlain>(
+      block < n ? p.one : p.two, (int)(block < n ? block : block - n), blockIdx.y, smem);
+}
 
 template <int DT, int BM, int BN, int BK, int WM, int WN, int STAGES, bool DIRECT>
 __global__ __launch_bounds__(WM* WN * 64, 2) void two_kernel(TwoArgs p) {
@@ -187,13 +205,22 @@ constexpr uint32_t kMostBlocks = 1u << 23;
 
 inline dim3 joint_grid(int64_t blocks, int splits, int& grid_x) {
   grid_x = (int)(blocks < kMostBlocks ? blocks : kMostBlocks);
-  return dim3((uint32_t)grid_x, (uint32_t)splits, (uint32_t)((blocks + kMostBlocks - 1) / kMostBlocks));
+  return dim3((uint32_t)grid_x, (uint32_t)splits,
+              (uint32_t)((blocks + kMostBlocks - 1) / kMostBlocks));
 }
 
 template <int DT, int LB>
 hipError_t gate_launch_tile(int tile, bool direct, GateArgs g, hipStream_t s) {
   const dim3 grid = joint_grid((int64_t)g.tiles_m * g.tiles_n, g.splits, g.grid_x);
-  if (tile == kTileSmall)
+  // 128 x 128: three stages for one workgroup a CU, as in linear_launch_tile
+  const bool alone = (int64_t)grid.x * grid.y * grid.z <= kCUs;
+  if (tile == kTileBig)
+    joint_wide_kernel<DT, 256, 256, LB, 2, kGate><<<grid, 256, 0, s>>>(g);
+  else if (tile == kTileMid && alone)
+    joint_wide_kernel<DT, 128, 128, LB, 3, kGate><<<grid, 256, 0, s>>>(g);
+  else if (tile == kTileMid)
+    joint_wide_kernel<DT, 128, 128, LB, 2, kGate><<<grid, 256, 0, s>>>(g);
+  else if (tile == kTileSmall)
     joint_kernel<DT, 64, 64, 64, 2, 2, LB, 3, true, kGate><<<grid, 256, 0, s>>>(g);
   else if (direct)
     joint_kernel<DT, 16, 128, 128, 1, 4, LB, 3, true, kGate><<<grid, 256, 0, s>>>(g);
@@ -218,7 +245,15 @@ hipError_t finish_launch(const LinearArgs& g, hipStream_t s) {
 template <int DT, int LB>
 hipError_t long_launch_tile(int tile, bool direct, LongArgs g, hipStream_t s) {
   const dim3 grid = joint_grid((int64_t)g.tiles_m * g.tiles_n, g.splits, g.grid_x);
-  if (tile == kTileSmall)
+  // 128 x 128: three stages for one workgroup a CU, as in linear_launch_tile
+  const bool alone = (int64_t)grid.x * grid.y * grid.z <= kCUs;
+  if (tile == kTileBig)
+    joint_wide_kernel<DT, 256, 256, LB, 2, kLong><<<grid, 256, 0, s>>>(g);
+  else if (tile == kTileMid && alone)
+    joint_wide_kernel<DT, 128, 128, LB, 3, kLong><<<grid, 256, 0, s>>>(g);
+  else if (tile == kTileMid)
+    joint_wide_kernel<DT, 128, 128, LB, 2, kLong><<<grid, 256, 0, s>>>(g);
+  else if (tile == kTileSmall)
     joint_kernel<DT, 64, 64, 64, 2, 2, LB, 3, true, kLong><<<grid, 256, 0, s>>>(g);
   else if (direct)
     joint_kernel<DT, 16, 64, 128, 1, 4, LB, 3, true, kLong><<<grid, 256, 0, s>>>(g);
@@ -232,7 +267,14 @@ template <int DT>
 hipError_t two_launch(int tile, bool direct, TwoArgs p, hipStream_t s) {
   const dim3 grid =
       joint_grid(2 * (int64_t)p.one.tiles_m * p.one.tiles_n, p.one.splits, p.one.grid_x);
-  if (tile == kTileSmall)
+  const bool alone = (int64_t)grid.x * grid.y * grid.z <= kCUs;
+  if (tile == kTileBig)
+    two_wide_kernel<DT, 256, 256, 2><<<grid, 256, 0, s>>>(p);
+  else if (tile == kTileMid && alone)
+    two_wide_kernel<DT, 128, 128, 3><<<grid, 256, 0, s>>>(p);
+  else if (tile == kTileMid)
+    two_wide_kernel<DT, 128, 128, 2><<<grid, 256, 0, s>>>(p);
+  else if (tile == kTileSmall)
     two_kernel<DT, 64, 64, 64, 2, 2, 3, true><<<grid, 256, 0, s>>>(p);
   else if (direct)
     two_kernel<DT, 16, 64, 128, 1, 4, 3, true><<<grid, 256, 0, s>>>(p);

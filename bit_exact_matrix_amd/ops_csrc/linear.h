@@ -1059,11 +1059,11 @@ __device__ __forceinline__ void wide_product(const args_t<MODE>& g, int block, i
       a += more ? a_step : 0;
       b += more ? b_step : 0;
       if constexpr (MODE == kGate) b2 += more ? b_step : 0;
-      if constexpr (MODE == kLong)
-        if (more && --until == 0) {
-          a = a2;
-          b = b2;
-        }
+      if constexpr (MODE == kLong) {  // without a branch: it costs the loop's registers
+        until -= 1;
+        a = until == 0 ? a2 : a;
+        b = until == 0 ? b2 : b;
+      }
     };
     auto read = [&](F (&fa)[FM], F (&fb)[FN], int q, int kk, const lds_char* from) {
       if (q < FN)

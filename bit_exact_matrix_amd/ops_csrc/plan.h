@@ -282,11 +282,11 @@ inline Plan paired_plan(const Paired& q, bool saves) {
   r.copy_a = r.copy_b = false;
   double best = 1e300;
   for (int any = 0; any <= 1 && best == 1e300; ++any)
-    for (int v = kTileSmall; v <= kTileFew + 1; ++v) {  // the last: few rows through registers
+    for (int v = 0; v <= kTileFew + 1; ++v) {  // the last: few rows through registers
       const int t = v < kTileFew ? v : kTileFew;
       const bool direct = v <= kTileFew;
       if (any                ? t != kTileFew
-          : env_tile >= 0    ? t != (env_tile < kTileFew ? kTileSmall : kTileFew)
+          : env_tile >= 0    ? t != (env_tile < kTileFew ? env_tile : kTileFew)
           : t == kTileFew    ? p.M > 128
                              : p.M <= 16)
         continue;
