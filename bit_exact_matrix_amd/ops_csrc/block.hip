@@ -88,28 +88,75 @@ int check_join(const mma_residual_norm_args& r, DropArgs* d) {
   return v.clash() ? MMAEMU_ERR_ALIAS : MMAEMU_OK;
 }
 
+// How a row is held: lanes a row, vectors a lane; no lanes where it is too long.
+struct RowPlan {
+  int gt, nv;
+};
+
+// One vector a lane and as many waves as the row needs, up to 1024 lanes;
+// then `most`.
+RowPlan row_plan(int64_t cols, int V, int most) {
+  const int64_t vecs = (cols + V - 1) / V;
+  int gt = 64;
+  while (gt < 1024 && gt < vecs) gt *= 2;
+  if (vecs <= gt) return {gt, 1};
+  return vecs <= 1024 * most ? RowPlan{1024, most} : RowPlan{0, 0};
+}
+
+// Workgroups of a row's lanes (four rows of one wave), as many as the CUs
+// hold at once.
+template <int DT, int PDT, int GT, int NV>
+void join_run(const JoinArgs& a, hipStream_t s) {
+  constexpr int G = GT == 64 ? 4 : 1;
+  const int64_t groups = (a.rows + G - 1) / G;
+  constexpr int kPerCU = 1024 / (GT * G);
+  const uint32_t grid = (uint32_t)(groups < kCUs * kPerCU ? groups : kCUs * kPerCU);
+  join_kernel<DT, PDT, GT, NV, G><<<grid, GT * G, 0, s>>>(a);
+}
+
 template <int DT, int PDT>
 hipError_t join_launch(const JoinArgs& a, hipStream_t s) {
-  const uint32_t grid = (uint32_t)(a.rows < 2 * kCUs ? a.rows : 2 * kCUs);
-  join_long_kernel<DT, PDT><<<grid, 1024, 0, s>>>(a);
+  const RowPlan p = row_plan(a.cols, kVec<DT>, 2);
+  switch (p.gt * p.nv) {
+    case 64: join_run<DT, PDT, 64, 1>(a, s); break;
+    case 128: join_run<DT, PDT, 128, 1>(a, s); break;
+    case 256: join_run<DT, PDT, 256, 1>(a, s); break;
+    case 512: join_run<DT, PDT, 512, 1>(a, s); break;
+    case 1024: join_run<DT, PDT, 1024, 1>(a, s); break;
+    case 2048: join_run<DT, PDT, 1024, 2>(a, s); break;
+    default: {
+      const uint32_t grid = (uint32_t)(a.rows < 2 * kCUs ? a.rows : 2 * kCUs);
+      join_long_kernel<DT, PDT><<<grid, 1024, 0, s>>>(a);
+    }
+  }
   return hipGetLastError();
 }
 
-// The workspace: the groups' column sums, then the rows' means.
+// The launch and its workspace: the groups' column sums, then the rows' means
+// where a row is read in several passes, or what the kernel asks for spare rows.
 struct JoinPlan {
-  int groups;  // 0: no column sums
-  int64_t means_at, bytes;
+  int groups;        // workgroups, or runs of rows of the column pass
+  bool sums, shift;  // column sums, those of biases among them
+  int64_t means_at;  // the rows' means, or the spare rows
+  int64_t bytes;
 };
 
+// Workgroups of 512 lanes (1024 for the longest rows), as many as the CUs hold
+// at once, each with its own row of partial sums.
 JoinPlan join_plan(const mma_residual_norm_backward_args& r) {
-  JoinPlan p{0, 0, 0};
-  if (r.rows == 0 ||
-      !(r.dgate || r.dpost_weight || r.dpost_bias || r.dpre_weight || r.dpre_bias))
-    return p;
-  const int64_t runs = (r.rows + 31) / 32;
-  p.groups = (int)(runs < kCUs ? runs : kCUs);
-  p.means_at = up256(p.groups * 4 * r.cols * 4);
-  p.bytes = p.means_at + up256(r.rows * 8);
+  JoinPlan p{};
+  if (r.rows == 0) return p;
+  p.sums = r.dgate || r.dpost_weight || r.dpost_bias || r.dpre_weight || r.dpre_bias;
+  p.shift = r.dpre_bias || r.dpost_bias || (r.dgate && r.post != kNormNone && r.post_bias);
+  const int gt = row_plan(r.cols, r.dtype == kFP32 ? 4 : 8, 1).gt;
+  const int64_t per = gt ? (gt < 512 ? 512 / gt : 1) : 32, runs = (r.rows + per - 1) / per;
+  const int64_t most = gt && gt <= 512 ? 2 * kCUs : kCUs;
+  p.groups = (int)(runs < most ? runs : most);
+  if (!p.sums) return p;
+  p.means_at = up256((int64_t)p.groups * 4 * r.cols * 4);
+  const int64_t spare =
+      gt && !r.dX && !r.dbranch ? p.groups * per * r.cols * elem_bytes(r.dtype) : 0;
+  p.bytes = p.means_at + up256(gt ? spare : r.rows * 8);
   return p;
 }
 
@@ -171,12 +218,35 @@ int check_join_backward(const mma_residual_norm_backward_args& r, int64_t ws_byt
   return v.clash() ? MMAEMU_ERR_ALIAS : MMAEMU_OK;
 }
 
+template <int DT, int PDT, int GT, bool SHIFT>
+hipError_t join_backward_run(const JoinArgs& a, int groups, hipStream_t s) {
+  constexpr int G = GT < 512 ? 512 / GT : 1;
+  if (a.cols == GT * kVec<DT>)
+    join_backward_kernel<DT, PDT, GT, G, SHIFT, true><<<(uint32_t)groups, GT * G, 0, s>>>(a);
+  else
+    join_backward_kernel<DT, PDT, GT, G, SHIFT, false><<<(uint32_t)groups, GT * G, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int DT, int PDT, int GT>
+hipError_t join_backward_run(const JoinArgs& a, int groups, bool shift, hipStream_t s) {
+  return shift ? join_backward_run<DT, PDT, GT, true>(a, groups, s)
+               : join_backward_run<DT, PDT, GT, false>(a, groups, s);
+}
+
 template <int DT, int PDT>
-hipError_t join_backward_launch(const JoinArgs& a, int groups, hipStream_t s) {
+hipError_t join_backward_launch(const JoinArgs& a, int groups, bool shift, hipStream_t s) {
+  switch (row_plan(a.cols, kVec<DT>, 1).gt) {
+    case 64: return join_backward_run<DT, PDT, 64>(a, groups, shift, s);
+    case 128: return join_backward_run<DT, PDT, 128>(a, groups, shift, s);
+    case 256: return join_backward_run<DT, PDT, 256>(a, groups, shift, s);
+    case 512: return join_backward_run<DT, PDT, 512>(a, groups, shift, s);
+    case 1024: return join_backward_run<DT, PDT, 1024>(a, groups, shift, s);
+  }
   const uint32_t grid = (uint32_t)(a.rows < 2 * kCUs ? a.rows : 2 * kCUs);
   join_long_dx_kernel<DT, PDT><<<grid, 1024, 0, s>>>(a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !groups) return e;
+  if (e != hipSuccess || !a.partial) return e;
   constexpr int V = kVec<DT>;
   const dim3 sums((uint32_t)((a.cols + 64 * V - 1) / (64 * V)), (uint32_t)groups);
   join_long_sums_kernel<DT, PDT><<<sums, 256, 0, s>>>(a, (a.rows + groups - 1) / groups);
@@ -587,7 +657,7 @@ int mma_residual_norm_backward(const mma_residual_norm_backward_args* args, void
     return err == hipSuccess ? MMAEMU_OK : hip_fail(err, "mma_residual_norm_backward launch");
   }
   const JoinPlan plan = join_plan(r);
-  if (!plan.groups && !r.dX && !r.dbranch) return MMAEMU_OK;
+  if (!plan.sums && !r.dX && !r.dbranch) return MMAEMU_OK;
   a.branch = r.post != kNormNone || r.dgate ? r.branch : nullptr;
   a.ldb = r.ldb;
   a.gate = r.gate;
@@ -613,16 +683,22 @@ int mma_residual_norm_backward(const mma_residual_norm_backward_args* args, void
   a.lddx = r.lddx;
   a.db = r.dbranch;
   a.lddb = r.lddb;
-  if (plan.groups) {
+  if (plan.sums) {
     a.partial = (float*)workspace;
     a.means = (float*)((char*)workspace + plan.means_at);
+    a.spare = a.means;
   }
-  err = MMAOPS_BY_TYPES(r.dtype, r.param_dtype, join_backward_launch, a, plan.groups, s);
-  if (err == hipSuccess && plan.groups) {
+  err = MMAOPS_BY_TYPES(r.dtype, r.param_dtype, join_backward_launch, a, plan.groups, plan.shift,
+                        s);
+  if (err == hipSuccess && plan.sums) {
     const JoinSums j{a.partial, plan.groups, r.param_dtype, r.cols, r.gate, r.post_weight,
                      r.post_bias, r.post != kNormNone, r.dgate, r.dpost_weight, r.dpost_bias,
                      r.dpre_weight, r.dpre_bias};
-    join_sums_kernel<<<(uint32_t)((r.cols + 63) / 64), 1024, 0, s>>>(j);
+    const uint32_t grid = (uint32_t)((r.cols + 31) / 32);
+    if (plan.shift)
+      join_sums_kernel<true><<<grid, 1024, 0, s>>>(j);
+    else
+      join_sums_kernel<false><<<grid, 1024, 0, s>>>(j);
     err = hipGetLastError();
   }
   return err == hipSuccess ? MMAEMU_OK : hip_fail(err, "mma_residual_norm_backward launch");

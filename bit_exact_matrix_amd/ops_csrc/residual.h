@@ -40,6 +40,7 @@ struct JoinArgs {
   int64_t lddr, lddh, lddx, lddb;
   float* partial;  // [groups][4][cols]: p1, p0, s1, s0
   float* means;    // long rows: [rows][2], the means of pre'
+  void* spare;     // where neither dx nor db is wanted: a row for each at work
 };
 
 // V elements of a parameter at column c, `fill` where there is none
@@ -327,6 +328,353 @@ __global__ __launch_bounds__(256) void join_long_sums_kernel(JoinArgs a, int64_t
   }
 }
 
+// ------------------------------------------------------ rows in registers
+// A parameter's vectors as they are in memory, for all of a lane's columns.
+template <int PDT, int V, int NV, int GT>
+struct Vectors {
+  Pack<PDT, V> q[NV];
+  __device__ __forceinline__ void load(const void* p, int lane, int cols, float fill) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * GT + lane) * V;
+      float v[V];
+      param<PDT, V>(p, c, cols - c, fill, v);
+      q[j] = pack<PDT, V>(v);
+    }
+  }
+  __device__ __forceinline__ void values(int j, float (&v)[V]) const { unpack(q[j], v); }
+};
+
+// Mean and rstd of a row held by GT lanes, NV vectors each, which are centred
+// on the way (0 past the row's end).  As in norm_kernel.
+template <int GT, int NV, int V>
+__device__ __forceinline__ void held_stats(float (&v)[NV][V], int lane, int cols, bool layer,
+                                           float eps, float* lds, int& turn, float& mean,
+                                           float& rstd) {
+  const float n_f = (float)cols;
+  float s[1], mu = 0.0f;
+  if (layer) {
+    s[0] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) s[0] += pair_sum(v[j]);
+    row_sum<GT, 1>(s, lds, turn);
+    mu = s[0] / n_f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int n = cols - (j * GT + lane) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[j][i] = i < n ? v[j][i] - mu : 0.0f;
+    }
+  }
+  s[0] = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float t[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) t[i] = v[j][i] * v[j][i];
+    s[0] += pair_sum(t);
+  }
+  row_sum<GT, 1>(s, lds, turn);
+  float var = s[0] / n_f;
+  mean = mu;
+  // the same in all lanes that meet at its barriers
+  if (layer && row_far(mu, var, eps)) {
+    s[0] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) s[0] += pair_sum(v[j]);
+    row_sum<GT, 1>(s, lds, turn);
+    const float d = s[0] / n_f;
+    row_correct(d, mean, var);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[j][i] -= d;
+  }
+  rstd = 1.0f / sqrtf(var + eps);
+}
+
+// A row is held by GT lanes, NV vectors of 16 bytes of each matrix; a
+// workgroup works on G rows at a time (several only where a row is a wave) and
+// walks the matrices, the next rows' loads under way.
+template <int DT, int PDT, int GT, int NV, int G>
+__global__ __launch_bounds__(GT* G, 4) void join_kernel(JoinArgs a) {
+  constexpr int V = kVec<DT>;
+  using E = elem_t<DT>;
+  static_assert(G == 1 || GT == 64, "");
+  __shared__ float lds[2 * 16];
+  const int lane = threadIdx.x % GT;
+  const int g = __builtin_amdgcn_readfirstlane(threadIdx.x / GT);  // whole waves
+  int turn = 0;
+  const Drop drop(a.drop);
+  Vectors<PDT, V, NV, GT> gate, post_w, post_b, pre_w, pre_b;
+  gate.load(a.gate, lane, a.cols, 1.0f);
+  post_w.load(a.post_w, lane, a.cols, 1.0f);
+  post_b.load(a.post_b, lane, a.cols, 0.0f);
+  pre_w.load(a.pre_w, lane, a.cols, 1.0f);
+  pre_b.load(a.pre_b, lane, a.cols, 0.0f);
+  const int64_t step = (int64_t)gridDim.x * G;
+  Pack<DT, V> xr[NV], br[NV];
+  auto fetch = [&](int64_t row) {
+    const bool live = row < a.rows;
+    const E* const x = (const E*)a.x + (live ? row : 0) * a.ldx;
+    const E* const b = (const E*)a.branch + (live ? row : 0) * a.ldb;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * GT + lane) * V;
+      br[j] = load_pack<DT, V>(b + c, live ? a.cols - c : 0);
+      xr[j] = load_pack<DT, V>(x + c, live ? a.cols - c : 0);
+    }
+  };
+  int64_t r0 = (int64_t)blockIdx.x * G;
+  fetch(r0 + g);
+  for (; r0 < a.rows; r0 += step) {
+    const int64_t row = r0 + g;
+    const bool live = row < a.rows;
+    float v[NV][V];
+    Pack<DT, V> x[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      unpack(br[j], v[j]);
+      x[j] = xr[j];
+    }
+    if (r0 + step < a.rows) fetch(row + step);
+    float pm = 0.0f, pr = 1.0f, m = 0.0f, q = 1.0f;
+    if (a.post != kNormNone) {
+      held_stats<GT, NV, V>(v, lane, a.cols, a.post == kNormLayer, a.eps, lds, turn, pm, pr);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float w[V], b[V];
+        post_w.values(j, w);
+        post_b.values(j, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[j][i] = v[j][i] * pr * w[i] + b[i];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * GT + lane) * V;
+      if (drop.threshold) {
+        uint32_t w[V / 2];
+        drop.halves<V>(row, c, w);
+        drop.apply<V>(w, v[j]);
+      }
+      float k[V], t[V];
+      gate.values(j, k);
+      unpack(x[j], t);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[j][i] = t[i] * a.scale + k[i] * v[j][i];
+      if (live) store_pack<DT, V>((E*)a.r + row * a.ldr + c, pack<DT, V>(v[j]), a.cols - c);
+    }
+    if (a.pre != kNormNone) {
+      // past the row's end there may be a bias by now
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int n = a.cols - (j * GT + lane) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[j][i] = i < n ? v[j][i] : 0.0f;
+      }
+      held_stats<GT, NV, V>(v, lane, a.cols, a.pre == kNormLayer, a.eps, lds, turn, m, q);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * GT + lane) * V;
+        float w[V], b[V];
+        pre_w.values(j, w);
+        pre_b.values(j, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[j][i] = v[j][i] * q * w[i] + b[i];
+        if (live) store_pack<DT, V>((E*)a.h + row * a.ldh + c, pack<DT, V>(v[j]), a.cols - c);
+      }
+    }
+    if (live && lane == 0) {
+      if (a.post_mean) a.post_mean[row] = pm;
+      if (a.post_rstd) a.post_rstd[row] = pr;
+      if (a.mean) a.mean[row] = m;
+      if (a.rstd) a.rstd[row] = q;
+    }
+  }
+}
+
+// The gradients of x and of the branch, and the workgroup's part of the
+// column sums (SHIFT: p0 and s0 too, which only biases need): one vector a lane,
+// rows of GT lanes, G at a time.  What a row's sums need is made again from the
+// loaded elements after they have met.  Each matrix's next row is loaded as soon as
+// this one's has been used, with no registers of its own.  An element past a
+// row's end adds 0 to the row's sums, as its dh is 0 in the first ones and inner_w
+// in the second (unless the row's statistics are not finite, and then neither is
+// the row).
+template <int DT, int PDT, int GT, int G, bool SHIFT, bool WHOLE>
+__global__ __launch_bounds__(GT* G, 4) void join_backward_kernel(JoinArgs a) {
+  constexpr int V = kVec<DT>;
+  using E = elem_t<DT>;
+  __shared__ float lds[2 * 16 * 2];
+  const int lane = threadIdx.x % GT;
+  const int g = __builtin_amdgcn_readfirstlane(threadIdx.x / GT);  // whole waves
+  const int c = lane * V, n = WHOLE ? V : a.cols - c;
+  int turn = 0;
+  const Drop drop(a.drop);
+  float pre_w[V], inner_w[V];  // inner_w: gate post_w
+  param<PDT, V>(a.pre_w, c, n, 1.0f, pre_w);
+  {
+    float k[V];
+    param<PDT, V>(a.post != kNormNone ? a.post_w : nullptr, c, n, 1.0f, inner_w);
+    param<PDT, V>(a.gate, c, n, 1.0f, k);
+#pragma unroll
+    for (int i = 0; i < V; ++i) inner_w[i] = i < n ? inner_w[i] * k[i] : 0.0f;
+  }
+  float p1[V], p0[V], s1[V], s0[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) p1[i] = p0[i] = s1[i] = s0[i] = 0.0f;
+  const float n_f = (float)a.cols;
+  const int64_t step = (int64_t)gridDim.x * G;
+
+  // A row's loads, and the store of dx, are there whatever is asked for: a matrix
+  // that is not has another in its place, whose row is in the cache, and dx, if it
+  // is not wanted, goes where the branch's gradient will be written over it, or to
+  // spare rows.  Behind a branch they could not be counted, and the wait for a
+  // row's loads would be one for the stores behind them (8192 x 4096 bf16, both rms
+  // norms, gate, dropout: 95 us, so 81).
+  const void* const dr_p = a.dr ? a.dr : a.dh;
+  const int64_t dr_ld = a.dr ? a.lddr : a.lddh;
+  const void* const dh_p = a.pre != kNormNone ? a.dh : dr_p;
+  const int64_t dh_ld = a.pre != kNormNone ? a.lddh : dr_ld;
+  const void* const r_p = a.pre != kNormNone ? a.r : dr_p;
+  const int64_t r_ld = a.pre != kNormNone ? a.ldr : dr_ld;
+  const void* const b_p = a.branch ? a.branch : dr_p;
+  const int64_t b_ld = a.branch ? a.ldb : dr_ld;
+  E* const dx_p = a.dx   ? (E*)a.dx
+                  : a.db ? (E*)a.db
+                         : (E*)a.spare + ((int64_t)blockIdx.x * G + g) * a.cols;
+  const int64_t dx_ld = a.dx ? a.lddx : a.db ? a.lddb : 0;
+  Pack<DT, V> dh, rr, dr, br;
+  float pm, pr, m, rs;
+  auto load = [&](const void* p, int64_t ld, int64_t row, int k) {
+    const E* const at = (const E*)p + row * ld;
+    if constexpr (WHOLE) return load_pack<DT, V>(at + c);
+    return load_pack<DT, V>(at + c, k);
+  };
+  auto fetch = [&](int64_t row) {
+    const bool live = row < a.rows;
+    const int64_t at = live ? row : a.rows - 1;
+    const int k = live ? n : 0;
+    br = load(b_p, b_ld, at, k);
+    dr = load(dr_p, dr_ld, at, k);
+    dh = load(dh_p, dh_ld, at, k);
+    rr = load(r_p, r_ld, at, k);
+    m = a.pre == kNormLayer ? a.mean[at] : 0.0f;
+    rs = a.pre != kNormNone ? a.rstd[at] : 1.0f;
+    pm = a.post == kNormLayer ? a.post_mean[at] : 0.0f;
+    pr = a.post != kNormNone ? a.post_rstd[at] : 1.0f;
+  };
+  int64_t row = (int64_t)blockIdx.x * G + g;
+  fetch(row);
+  // every group of the workgroup takes as many turns (rows past the end
+  // are empty), for the barriers
+  for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < a.rows; r0 += step, row += step) {
+    const bool live = G == 1 || row < a.rows;
+    float s[2], t[V], b[V];
+    if (a.pre != kNormNone) {
+      float rh[V], h[V], d[V];
+      unpack(rr, rh);
+      unpack(dh, d);
+      if (WHOLE && G > 1 && !live) {  // another row's elements
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = 0.0f;
+      }
+      s[0] = s[1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        rh[i] = (rh[i] - m) * rs;
+        h[i] = d[i] * pre_w[i];
+        s[0] += h[i];
+        s[1] += h[i] * rh[i];
+        p1[i] += d[i] * rh[i];
+        if (SHIFT) p0[i] += d[i];
+      }
+      row_sum<GT, 2>(s, lds, turn);
+      const float m0 = a.pre == kNormLayer ? s[0] / n_f : 0.0f, m1 = s[1] / n_f;
+      unpack(dr, t);
+#pragma unroll
+      for (int i = 0; i < V; ++i) t[i] = (a.dr ? t[i] : 0.0f) + rs * (h[i] - m0 - rh[i] * m1);
+    } else {
+      unpack(dr, t);
+    }
+    if (WHOLE && G > 1 && !live) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) t[i] = 0.0f;
+    }
+    unpack(br, b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = (b[i] - pm) * pr;
+    const float pr_now = pr;
+    if (r0 + step < a.rows) fetch(row + step);
+    if (live) {
+      float o[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = t[i] * a.scale;
+      store_pack<DT, V>(dx_p + row * dx_ld + c, pack<DT, V>(o), n);
+    }
+    if (drop.threshold) {
+      uint32_t w[V / 2];
+      drop.halves<V>(row, c, w);
+      drop.apply<V>(w, t);
+      float k[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) k[i] = b[i];
+      drop.clear<V>(w, k);  // what was dropped has no part, whatever it was
+#pragma unroll
+      for (int i = 0; i < V; ++i) s1[i] += t[i] * k[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s1[i] += t[i] * b[i];
+    }
+    if (SHIFT) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s0[i] += t[i];
+    }
+    if (!a.db) continue;
+#pragma unroll
+    for (int i = 0; i < V; ++i) t[i] *= inner_w[i];
+    if (a.post != kNormNone) {
+      s[0] = s[1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        s[0] += t[i];
+        s[1] += t[i] * b[i];
+      }
+      row_sum<GT, 2>(s, lds, turn);
+      const float k0 = a.post == kNormLayer ? s[0] / n_f : 0.0f, k1 = s[1] / n_f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) t[i] = pr_now * (t[i] - k0 - b[i] * k1);
+    }
+    if (live) store_pack<DT, V>((E*)a.db + row * a.lddb + c, pack<DT, V>(t), n);
+  }
+  if (!a.partial) return;
+  float* const out = a.partial + (int64_t)blockIdx.x * 4 * a.cols;
+  float(*const sums[4])[V] = {&p1, &p0, &s1, &s0};
+  if constexpr (G == 1) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (SHIFT || k % 2 == 0)
+        store_pack<kFP32, V>(out + k * a.cols + c, pack<kFP32, V>(*sums[k]), n);
+  } else {  // the G rows' sums meet in LDS, in group order
+    __shared__ float meet[G][GT * V];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!SHIFT && k % 2) continue;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < V; ++i) meet[g][i * GT + lane] = (*sums[k])[i];
+      __syncthreads();
+      for (int t = threadIdx.x; t < GT * V; t += GT * G) {
+        float s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < G; ++q) s += meet[q][(t % V) * GT + t / V];
+        if (t < a.cols) out[(int64_t)k * a.cols + t] = s;
+      }
+    }
+  }
+}
+
 // -------------------------------------------------- the vectors' gradients
 struct JoinSums {
   const float* partial;  // [count][4][cols]
@@ -337,32 +685,37 @@ struct JoinSums {
   void *dgate, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
 };
 
-// The groups' sums in group order within each of 16 runs and then in run
-// order: 64 columns a workgroup, a run a wave.
-static __global__ __launch_bounds__(1024) void join_sums_kernel(JoinSums a) {
-  __shared__ float meet[4][16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  const int run = (a.count + 15) / 16;
-  const int p0 = wave * run, p1 = p0 + run < a.count ? p0 + run : a.count;
+// The groups' sums in group order within each of 32 runs and then in run
+// order: 32 columns a workgroup.
+template <bool SHIFT>
+__global__ __launch_bounds__(1024) void join_sums_kernel(JoinSums a) {
+  __shared__ float meet[4][32][32], total[4][32];
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  const int run = (a.count + 31) / 32;
+  const int p0 = part * run, p1 = p0 + run < a.count ? p0 + run : a.count;
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < a.cols) {
     const float* const p = a.partial + c;
 #pragma unroll 4
     for (int q = p0; q < p1; ++q)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[k] += p[((int64_t)q * 4 + k) * a.cols];
+      for (int k = 0; k < 4; ++k)
+        if (SHIFT || k % 2 == 0) s[k] += p[((int64_t)q * 4 + k) * a.cols];
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) meet[k][wave][lane] = s[k];
+  for (int k = 0; k < 4; ++k) meet[k][part][lane] = s[k];
   __syncthreads();
-  if (wave || c >= a.cols) return;
+  if (part < 4) {
+    float t = meet[part][0][lane];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    s[k] = meet[k][0][lane];
-#pragma unroll
-    for (int w = 1; w < 16; ++w) s[k] += meet[k][w][lane];
+    for (int w = 1; w < 32; ++w) t += meet[part][w][lane];
+    total[part][lane] = t;
   }
+  __syncthreads();
+  if (part || c >= a.cols) return;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) s[k] = total[k][lane];
   const float g = a.gate ? load_any(a.gate, c, a.dt) : 1.0f;
   if (a.dpre_w) store_any(a.dpre_w, c, s[0], a.dt);
   if (a.dpre_b) store_any(a.dpre_b, c, s[1], a.dt);
