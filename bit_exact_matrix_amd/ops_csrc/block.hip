@@ -256,6 +256,39 @@ hipError_t join_backward_launch(const JoinArgs& a, int groups, bool shift, hipSt
 // -------------------------------------------------------- gated layer
 GatedLaunches launches(int dt) { return dt == kFP16 ? gated_fp16() : gated_bf16(); }
 
+// Two matrices of 16-bit elements copied to rows that start on 16 bytes, in
+// one launch (as align_kernel).
+__global__ __launch_bounds__(256) void align_two_kernel(const uint16_t* x, int64_t ldx,
+                                                        uint16_t* y, const uint16_t* x2,
+                                                        int64_t ldx2, uint16_t* y2, int64_t ldy,
+                                                        int64_t rows, int64_t cols) {
+  constexpr int V = 8, kLanes = 64;
+  const bool two = blockIdx.z != 0;
+  const uint16_t* const from = two ? x2 : x;
+  const int64_t ld = two ? ldx2 : ldx;
+  uint16_t* const to = two ? y2 : y;
+  const int lane = threadIdx.x % kLanes, g = threadIdx.x / kLanes;
+  const int64_t step = (int64_t)gridDim.x * (256 / kLanes);
+  const int64_t cstep = (int64_t)gridDim.y * kLanes * V;
+  for (int64_t row = (int64_t)blockIdx.x * (256 / kLanes) + g; row < rows; row += step)
+    for (int64_t c = ((int64_t)blockIdx.y * kLanes + lane) * V; c < cols; c += cstep) {
+      const int n = cols - c < V ? (int)(cols - c) : V;
+      store_pack<kBF16, V>((__bf16*)(to + row * ldy + c),
+                           load_pack<kBF16, V>((const __bf16*)(from + row * ld + c), n), V);
+    }
+}
+
+hipError_t align_two(const void* x, int64_t ldx, void* y, const void* x2, int64_t ldx2, void* y2,
+                     const Stored& t, hipStream_t s) {
+  if (t.rows == 0 || t.cols == 0) return hipSuccess;
+  const int64_t gx = (t.rows + 3) / 4, gy = (t.cols + 511) / 512;
+  const dim3 grid((uint32_t)(gx < (1 << 22) ? gx : (1 << 22)), (uint32_t)(gy < 256 ? gy : 256), 2);
+  align_two_kernel<<<grid, 256, 0, s>>>((const uint16_t*)x, ldx, (uint16_t*)y,
+                                        (const uint16_t*)x2, ldx2, (uint16_t*)y2, t.ld, t.rows,
+                                        t.cols);
+  return hipGetLastError();
+}
+
 // A pair's arguments, with its operands copied where the plan says so.
 hipError_t paired_fill(const Paired& q, const Plan& r, LinearArgs& g, const void*& a2,
                        const void*& b2, void* ws, hipStream_t s) {
@@ -271,16 +304,13 @@ hipError_t paired_fill(const Paired& q, const Plan& r, LinearArgs& g, const void
   char* at = (char*)ws + paired_partial_bytes(q, r);
   auto copy = [&](const void*& one, const void*& two, bool second, int64_t ld2, int64_t& ld,
                   const Stored& st) {
-    hipError_t e = align_rows(one, ld, at, st, s);
-    one = at;
-    at += copy_bytes(true, st);
-    if (second && e == hipSuccess) {
-      e = align_rows(two, ld2, at, st, s);
-      two = at;
-      at += copy_bytes(true, st);
-    } else {
-      two = one;
-    }
+    char* const to = at;
+    at += copy_bytes(true, st) * (second ? 2 : 1);
+    char* const to2 = second ? to + copy_bytes(true, st) : to;
+    const hipError_t e = second ? align_two(one, ld, to, two, ld2, to2, st, s)
+                                : align_rows(one, ld, to, st, s);
+    one = to;
+    two = to2;
     ld = st.ld;
     return e;
   };
@@ -382,7 +412,8 @@ struct GatedBackward {
   bool has_dz;     // dg and du are written
   int db_runs;     // rows of column sums, 0: no bias gradient
   int64_t db_run;  // rows of one of them
-  int64_t dg_at, du_at, ldd, x_at, db_at, part_at, bytes;
+  int64_t dg_at, du_at, ldd, x_at, db_at, part_at, part2_at, bytes;
+  bool small;      // the products and the column sums in one launch
 };
 
 GatedBackward gated_backward(const mma_gated_linear_backward_args& r, void* ws) {
@@ -405,7 +436,7 @@ GatedBackward gated_backward(const mma_gated_linear_backward_args& r, void* ws) 
   if (r.dbias_g || r.dbias_u) {
     const int64_t cols = (r.N + 511) / 512;
     int64_t runs = (8 * kCUs + cols - 1) / cols;
-    if (runs > (r.M + 7) / 8) runs = (r.M + 7) / 8;
+    if (runs > (r.M + 3) / 4) runs = (r.M + 3) / 4;  // a row for each wave
     b.db_run = (r.M + runs - 1) / runs;
     b.db_runs = (int)((r.M + b.db_run - 1) / b.db_run);
     b.db_at = at;
@@ -433,7 +464,13 @@ GatedBackward gated_backward(const mma_gated_linear_backward_args& r, void* ws) 
     const int64_t w = paired_bytes(b.dw, b.pdw);
     part = part > w ? part : w;
   }
-  b.bytes = at + part;
+  // All on small tiles, whole, and few enough that one grid holds them: one
+  // launch.  Their copies, if any, then stand in the workspace side by side.
+  auto tiles = [](const Product& p) { return ((p.M + 63) / 64) * ((p.N + 63) / 64); };
+  b.small = r.dX && r.dWg && r.K && b.pdx.tile == kTileSmall && b.pdw.tile == kTileSmall &&
+            !b.pdx.partial && !b.pdw.partial && tiles(b.dx.p) + 2 * tiles(b.dw.p) <= (1 << 20);
+  b.part2_at = b.small ? at + paired_bytes(b.dx, b.pdx) : at;
+  b.bytes = b.small ? b.part2_at + paired_bytes(b.dw, b.pdw) : at + part;
   return b;
 }
 
@@ -528,38 +565,47 @@ hipError_t gated_backward_run(const mma_gated_linear_backward_args& r, void* ws,
   d.run = b.db_run;
   int64_t runs = b.db_runs;
   if (!runs) {
-    runs = (r.M + 7) / 8 < 4096 ? (r.M + 7) / 8 : 4096;
+    runs = (r.M + 3) / 4 < 4096 ? (r.M + 3) / 4 : 4096;
     d.run = (r.M + runs - 1) / runs;
   }
   e = run.dz(d, runs, s);
-  if (e == hipSuccess && b.db_runs)
+  if (e == hipSuccess && b.db_runs && !b.small)
     e = column_sums(d.partial, b.db_runs, r.N, r.dbias_g, r.dbias_u, 1, r.bias_dtype, s);
   if (e == hipSuccess && r.dWg && r.K && r.x_codes)
     e = restore_to(r.dtype, r.x_codes, r.x_scales, base + b.x_at, (r.K + 7) / 8 * 8, r.M, r.K, s);
+  SmallArgs all;
+  memset(&all, 0, sizeof all);
   if (e == hipSuccess && r.dX && r.K) {
-    LongArgs g;
-    memset(&g, 0, sizeof g);
+    LongArgs& g = all.dx;
     g.y = r.dX;
     g.ldy = r.lddx;
     g.out_dt = r.dtype;
     e = paired_fill(b.dx, b.pdx, g, g.a2, g.b2, base + b.part_at, s);
-    if (e == hipSuccess) e = run.both(b.pdx.tile, b.pdx.direct, b.dx.p.lb, g, s);
+    if (e == hipSuccess && !b.small) e = run.both(b.pdx.tile, b.pdx.direct, b.dx.p.lb, g, s);
   }
   if (e == hipSuccess && r.dWg && r.K) {
-    TwoArgs p;
-    memset(&p, 0, sizeof p);
+    TwoArgs& p = all.dw;
     const void *a2, *b2;
     p.one.y = r.dWg;
     p.one.ldy = r.lddwg;
     p.one.out_dt = r.dw_dtype;
-    e = paired_fill(b.dw, b.pdw, p.one, a2, b2, base + b.part_at, s);
+    e = paired_fill(b.dw, b.pdw, p.one, a2, b2, base + b.part2_at, s);
     p.two = p.one;
     p.two.a = a2;
     p.two.b = b2;
     p.two.y = r.dWu;
     p.two.ldy = r.lddwu;
     if (p.one.partial) p.two.partial += b.dw.p.M * b.dw.p.N * b.pdw.splits;
-    if (e == hipSuccess) e = run.two(b.pdw.tile, b.pdw.direct, p, s);
+    if (e == hipSuccess && !b.small) e = run.two(b.pdw.tile, b.pdw.direct, p, s);
+  }
+  if (e == hipSuccess && b.small) {
+    all.partial = d.partial;
+    all.dbias_g = r.dbias_g;
+    all.dbias_u = r.dbias_u;
+    all.cols = r.N;
+    all.count = b.db_runs;
+    all.dbias_dt = r.bias_dtype;
+    e = run.small(b.dx.p.lb, all, s);
   }
   return e;
 }

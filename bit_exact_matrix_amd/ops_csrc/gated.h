@@ -35,6 +35,13 @@ __global__ __launch_bounds__(256, 1) void joint_wide_kernel(args_t<MODE> g) {
   wide_product<DT, 0, LB, BM, BN, STAGES, MODE>(g, block, blockIdx.y, smem);
 }
 
+// Up to 16 rows in one launch, BN / 2 output columns a workgroup.
+template <int DT, int LB, int BN>
+__global__ __launch_bounds__(512, 2) void gate_rows_kernel(GateArgs g) {
+  __shared__ __attribute__((aligned(1024))) char smem[kRowsBytes];
+  rows_product<DT, LB, BN, kGate>(g, smem);
+}
+
 // Two products of the same sizes and layouts, one's tiles after the other's.
 struct TwoArgs {
   LinearArgs one, two;
@@ -58,6 +65,62 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void two_kernel(TwoArgs p) {
   if (block >= 2 * (int64_t)n) return;  // the whole workgroup
   small_product<DT, BM, BN, BK, WM, WN, 1, 1, STAGES, DIRECT>(
       block < n ? p.one : p.two, (int)(block < n ? block : block - n), blockIdx.y, smem);
+}
+
+// A small backward pass's second launch: the tiles of dg Wg^T + du Wu^T, those of
+// both weight gradients, then the column sums of both biases, 64 columns a
+// workgroup; all need only the first launch's results.
+struct SmallArgs {
+  LongArgs dx;
+  TwoArgs dw;
+  const float* partial;  // [count][2][cols]
+  void *dbias_g, *dbias_u;
+  int64_t cols;
+  int count, dbias_dt;  // count 0: no sums
+};
+
+template <int DT, int LB>
+__global__ __launch_bounds__(256, 2) void gated_small_kernel(SmallArgs p) {
+  __shared__ __attribute__((aligned(1024))) char smem[kRingBytes<64, 64, 64, 3>];
+  const int n1 = p.dx.tiles_m * p.dx.tiles_n, n2 = p.dw.one.tiles_m * p.dw.one.tiles_n;
+  const int b = blockIdx.x;
+  if (b < n1) {
+    small_product<DT, 64, 64, 64, 2, 2, 0, LB, 3, true, kLong>(p.dx, b, 0, smem);
+  } else if (b < n1 + 2 * n2) {
+    const int t = b - n1;
+    small_product<DT, 64, 64, 64, 2, 2, 1, 1, 3, true>(t < n2 ? p.dw.one : p.dw.two,
+                                                       t < n2 ? t : t - n2, 0, smem);
+  } else {
+    // in the runs and the order of column_sum_kernel, for the same bits
+    float(&meet)[16][64] = *(float(*)[16][64])smem;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int blocks = (int)((p.cols + 63) / 64), t = b - n1 - 2 * n2;
+    const int which = t < blocks ? 0 : 1;
+    void* const out = which ? p.dbias_u : p.dbias_g;
+    const int64_t c = (int64_t)(t - which * blocks) * 64 + lane;
+    const int run = (p.count + 15) / 16;
+    // four of the sixteen runs a wave, side by side; past a run's end + 0
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < p.cols) {
+#pragma unroll 4
+      for (int q = 0; q < run; ++q) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = (wave * 4 + i) * run + q;
+          s[i] += row < p.count ? p.partial[((int64_t)row * 2 + which) * p.cols + c] : 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) meet[wave * 4 + i][lane] = s[i];
+    __syncthreads();
+    if (wave == 0 && c < p.cols && out) {
+      float sum = meet[0][lane];
+#pragma unroll
+      for (int r = 1; r < 16; ++r) sum += meet[r][lane];
+      store_any(out, c, sum, p.dbias_dt);
+    }
+  }
 }
 
 // The runs' sums of both halves added in run order, then the epilogue: four
@@ -135,10 +198,60 @@ __device__ __forceinline__ void as_numbers(float (&v)[8]) {
   for (int i = 0; i < 8; ++i) v[i] = v[i] > kFar ? kFar : v[i] < -kFar ? -kFar : v[i];
 }
 
+// act(z) and its slope of V values, as act_apply and act_slope have them, what
+// both need made once (gelu's tail, a logistic).
+template <int V>
+__device__ __forceinline__ void act_both(const float (&z)[V], const int act, float (&f)[V],
+                                         float (&s)[V]) {
+  switch (act) {
+    case kActRelu:
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        f[i] = z[i] < 0.0f ? 0.0f : z[i];
+        s[i] = z[i] > 0.0f ? 1.0f : 0.0f;
+      }
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float b = bounded(z[i], kTailEnd), a = __builtin_fabsf(b), q = normal_tail(a);
+        const float e = fast_exp2(z[i] * z[i] * (-0.5f * kLog2e));
+        f[i] = __builtin_fmaf(-a, q, z[i] < 0.0f ? 0.0f : z[i]);
+        s[i] = __builtin_fmaf(b * e, kInvSqrt2Pi, z[i] > 0.0f ? 1.0f - q : q);
+      }
+      break;
+    case kActGeluTanh:
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float b = z[i] > 12.0f ? 12.0f : z[i] < -12.0f ? -12.0f : z[i], b2 = b * b;
+        const float l = logistic(2.0f * kSqrt2OverPi * b * __builtin_fmaf(0.044715f, b2, 1.0f));
+        f[i] = z[i] * l;
+        s[i] = l + b * l * (1.0f - l) * 2.0f * kSqrt2OverPi * (1.0f + 3.0f * 0.044715f * b2);
+      }
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float l = logistic(z[i]);
+        f[i] = z[i] * l;
+        s[i] = l * (1.0f + bounded(z[i], 100.0f) * (1.0f - l));
+      }
+      break;
+    default:
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        f[i] = z[i];
+        s[i] = 1.0f;
+      }
+  }
+}
+
 // dg, du and their column sums over the workgroup's run of rows: 64 lanes of
-// 8 columns, four waves over the rows, the waves' sums added in wave order.
-template <int DT>
-__global__ __launch_bounds__(256) void gate_dz_kernel(GateDzArgs a) {
+// 8 columns, four waves over the rows, the waves' sums added in wave order.  The
+// activation is the kernel's own: with a switch in it, it held the registers
+// of the largest.
+template <int DT, int ACT, bool SAVED>
+__global__ __launch_bounds__(256, 4) void gate_dz_kernel(GateDzArgs a) {
   constexpr int V = 8;
   using E = elem_t<DT>;
   __shared__ float meet[4][64 * V];
@@ -153,22 +266,25 @@ __global__ __launch_bounds__(256) void gate_dz_kernel(GateDzArgs a) {
   if (n > 0) {
     for (int64_t m = r0 + wave; m < r1; m += 4) {
       float d[V], g[V], u[V];
-      unpack(load_pack<DT, V>((const E*)a.dy + m * a.lddy + c, n), d);
-      if (a.g_codes) {
+      const Pack<DT, V> py = load_pack<DT, V>((const E*)a.dy + m * a.lddy + c, n);
+      if constexpr (SAVED) {
         const int64_t at = m * nb + c / kBlock;
-        decode<V>(load_codes<V>(a.g_codes + m * a.N + c, n), a.g_scales[at], g);
-        decode<V>(load_codes<V>(a.u_codes + m * a.N + c, n), a.u_scales[at], u);
+        const Codes<V> qg = load_codes<V>(a.g_codes + m * a.N + c, n);
+        const Codes<V> qu = load_codes<V>(a.u_codes + m * a.N + c, n);
+        const int eg = a.g_scales[at], eu = a.u_scales[at];
+        decode<V>(qg, eg, g);
+        decode<V>(qu, eu, u);
       } else {
-        unpack(load_pack<DT, V>((const E*)a.g + m * a.ldg + c, n), g);
-        unpack(load_pack<DT, V>((const E*)a.u + m * a.ldu + c, n), u);
+        const Pack<DT, V> pg = load_pack<DT, V>((const E*)a.g + m * a.ldg + c, n);
+        const Pack<DT, V> pu = load_pack<DT, V>((const E*)a.u + m * a.ldu + c, n);
+        unpack(pg, g);
+        unpack(pu, u);
         as_numbers<DT>(g);
         as_numbers<DT>(u);
       }
+      unpack(py, d);
       float f[V], s[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = s[i] = g[i];
-      act_all(f, a.act, act_apply);
-      act_all(s, a.act, act_slope);
+      act_both<V>(g, ACT, f, s);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float dg = d[i] * (u[i] * s[i]), du = d[i] * f[i];
@@ -211,6 +327,13 @@ inline dim3 joint_grid(int64_t blocks, int splits, int& grid_x) {
 
 template <int DT, int LB>
 hipError_t gate_launch_tile(int tile, bool direct, GateArgs g, hipStream_t s) {
+  if (tile == kTileRows) {
+    if (g.codes)
+      gate_rows_kernel<DT, LB, 64><<<dim3((uint32_t)((g.N + 31) / 32)), 512, 0, s>>>(g);
+    else
+      gate_rows_kernel<DT, LB, 32><<<dim3((uint32_t)((g.N + 15) / 16)), 512, 0, s>>>(g);
+    return hipGetLastError();
+  }
   const dim3 grid = joint_grid((int64_t)g.tiles_m * g.tiles_n, g.splits, g.grid_x);
   // 128 x 128: three stages for one workgroup a CU, as in linear_launch_tile
   const bool alone = (int64_t)grid.x * grid.y * grid.z <= kCUs;
@@ -289,7 +412,20 @@ hipError_t two_launch(int tile, bool direct, TwoArgs p, hipStream_t s) {
 template <int DT>
 hipError_t gate_dz_launch(const GateDzArgs& d, int64_t runs, hipStream_t s) {
   const dim3 grid((uint32_t)((d.N + 511) / 512), (uint32_t)runs);
-  gate_dz_kernel<DT><<<grid, 256, 0, s>>>(d);
+  const auto go = [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    if (d.g_codes)
+      gate_dz_kernel<DT, ACT, true><<<grid, 256, 0, s>>>(d);
+    else
+      gate_dz_kernel<DT, ACT, false><<<grid, 256, 0, s>>>(d);
+  };
+  switch (d.act) {
+    case kActRelu: go(std::integral_constant<int, kActRelu>{}); break;
+    case kActGelu: go(std::integral_constant<int, kActGelu>{}); break;
+    case kActGeluTanh: go(std::integral_constant<int, kActGeluTanh>{}); break;
+    case kActSilu: go(std::integral_constant<int, kActSilu>{}); break;
+    default: go(std::integral_constant<int, kActNone>{});
+  }
   return hipGetLastError();
 }
 
@@ -299,6 +435,7 @@ struct GatedLaunches {
   hipError_t (*both)(int tile, bool direct, int lb, const LongArgs& g, hipStream_t s);
   hipError_t (*two)(int tile, bool direct, const TwoArgs& p, hipStream_t s);
   hipError_t (*dz)(const GateDzArgs& d, int64_t runs, hipStream_t s);
+  hipError_t (*small)(int lb, const SmallArgs& p, hipStream_t s);
 };
 
 template <int DT>
@@ -316,6 +453,17 @@ GatedLaunches gated_launches() {
           },
           [](const GateDzArgs& d, int64_t runs, hipStream_t s) {
             return gate_dz_launch<DT>(d, runs, s);
+          },
+          [](int lb, const SmallArgs& p, hipStream_t s) {
+            const int64_t sums = p.count ? 2 * ((p.cols + 63) / 64) : 0;
+            const uint32_t grid =
+                (uint32_t)((int64_t)p.dx.tiles_m * p.dx.tiles_n +
+                           2 * (int64_t)p.dw.one.tiles_m * p.dw.one.tiles_n + sums);
+            if (lb)
+              gated_small_kernel<DT, 1><<<grid, 256, 0, s>>>(p);
+            else
+              gated_small_kernel<DT, 0><<<grid, 256, 0, s>>>(p);
+            return hipGetLastError();
           }};
 }
 

@@ -1185,6 +1185,39 @@ __device__ __forceinline__ void finish_rows(const LinearArgs& g, const lds_char*
   finish<DT, 4, 1, false>(g, m, 0, c, have, v, res);
 }
 
+// The same of a gated product: of a wave's BN columns the first half are the
+// gate's sums.
+template <int DT, int ROWS, int BN, int NW>
+__device__ __forceinline__ void gate_finish_rows(const GateArgs& g, const lds_char* meet,
+                                                 int64_t n0) {
+  using lds_f4 = __attribute__((address_space(3))) f32x4;
+  constexpr int kMeet = ROWS * BN * 4, kLanes = BN / 8;
+  if (threadIdx.x >= ROWS * kLanes) return;
+  const int64_t m = threadIdx.x / kLanes, c = n0 + threadIdx.x % kLanes * 4;
+  const int have = g.N - c < 4 ? (int)(g.N - c) : 4;
+  float v[4], w[4], bias[4], bias2[4];
+#pragma unroll
+  for (int k = 0; k < NW; ++k) {
+    const lds_char* const at = meet + k * kMeet + m * BN * 4 + threadIdx.x % kLanes * 16;
+    const f32x4 a = *(const lds_f4*)at, b = *(const lds_f4*)(at + BN * 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = k ? v[i] + a[i] : a[i];
+      w[i] = k ? w[i] + b[i] : b[i];
+    }
+  }
+  gate_bias<4>(g, c, have, bias, bias2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] += bias[i];
+    w[i] += bias2[i];
+  }
+  if constexpr (kLanes >= 8) {
+    if (g.codes) gate_save<DT, 4>(g, m, c, have, v, w);
+  }
+  gate_finish<DT, 4, 1>(g, m, 0, c, have, false, v, w);
+}
+
 // Up to 16 rows (a decoding step): what bounds it is reading the weight
 // once, from as many CUs and with as much under way as there can be.  A
 // workgroup takes BN = 16 columns (32 where z is saved, as a checkpoint
@@ -1196,25 +1229,32 @@ __device__ __forceinline__ void finish_rows(const LinearArgs& g, const lds_char*
 // bytes (32 columns 13.6, 64 columns 14.9: fewer workgroups); K split over
 // workgroups and joined by a second kernel takes 8.7 + 3.8 us and a second
 // launch.
-template <int DT, int LB, int BN>
-__global__ __launch_bounds__(512, 2) void linear_rows_kernel(LinearArgs g) {
+// A gated one has half its columns of either weight.
+constexpr int kRowsBytes = 8 * 8 * 16 * 64 * 2;  // waves, and 16 KB each
+
+template <int DT, int LB, int BN, int MODE>
+__device__ __forceinline__ void rows_product(const args_t<MODE>& g, char* smem) {
   constexpr int BK = 64, NW = 8, FN = BN / 16, kSteps = 8 / FN;  // steps at once
-  using TB = Tile<BN, BK, LB, 1>;
+  constexpr int kCols = MODE == kGate ? BN / 2 : BN;  // of the output
+  using TB = right_tile<MODE, BN, BK, LB, 1, FN>;
   using F = typename Mfma<DT>::frag;
   using lds_f4 = __attribute__((address_space(3))) f32x4;
   constexpr int kPer = TB::kPerWave;
-  __shared__ __attribute__((aligned(1024))) char smem[NW * kSteps * TB::kBytes];
+  static_assert(NW * kSteps * TB::kBytes == kRowsBytes, "");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   lds_char* const lds = (lds_char*)smem + wave * kSteps * TB::kBytes;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
   int tm, tn;
   tile_of(1, (int)gridDim.x, blockIdx.x, tm, tn);
-  const int64_t n0 = (int64_t)tn * BN;
-  const int have_n = g.N - n0 < BN ? (int)(g.N - n0) : BN;
+  const int64_t n0 = (int64_t)tn * kCols;
+  const int have_n = g.N - n0 < kCols ? (int)(g.N - n0) : kCols;
   const int64_t steps = g.K / BK, s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
   const int64_t b_step = (LB == 0 ? BK : BK * g.ldb) * 2;
-  const char* b = (const char*)g.b + (LB == 0 ? n0 * g.ldb : n0) * 2 + s0 * b_step;
+  const int64_t b_at = (LB == 0 ? n0 * g.ldb : n0) * 2 + s0 * b_step;
+  const char* b = (const char*)g.b + b_at;
+  const char* b2 = nullptr;
+  if constexpr (MODE == kGate) b2 = (const char*)g.b2 + b_at;
   // rows past M repeat the last one: what they give is not stored
   const int64_t row = (lane & 15) < g.M ? (lane & 15) : g.M - 1;
   const char* x = (const char*)g.a + (row * g.lda + s0 * BK + (lane >> 4) * 8) * 2;
@@ -1237,8 +1277,12 @@ __global__ __launch_bounds__(512, 2) void linear_rows_kernel(LinearArgs g) {
 #pragma unroll
     for (int t = 0; t < kSteps; ++t) {
       if (t >= n) continue;
-      TB::load(b, ob, lds0 + t * TB::kBytes, 0);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        load_to_lds(uniform(MODE == kGate && i >= kPer / 2 ? b2 : b), ob[i],
+                    lds0 + t * TB::kBytes + TB::at(0, i));
       b += b_step;
+      if constexpr (MODE == kGate) b2 += b_step;
     }
     x += kSteps * BK * 2;
     static_for<kSteps>([&](auto step) {
@@ -1264,7 +1308,16 @@ __global__ __launch_bounds__(512, 2) void linear_rows_kernel(LinearArgs g) {
     *(lds_f4*)(meet + wave * (16 * BN * 4) + (lane & 15) * BN * 4 + j * 64 + (lane >> 4) * 16) =
         acc[j];
   __syncthreads();
-  finish_rows<DT, 16, BN, NW>(g, meet, n0);
+  if constexpr (MODE == kGate)
+    gate_finish_rows<DT, 16, BN, NW>(g, meet, n0);
+  else
+    finish_rows<DT, 16, BN, NW>(g, meet, n0);
+}
+
+template <int DT, int LB, int BN>
+__global__ __launch_bounds__(512, 2) void linear_rows_kernel(LinearArgs g) {
+  __shared__ __attribute__((aligned(1024))) char smem[kRowsBytes];
+  rows_product<DT, LB, BN, kPlain>(g, smem);
 }
 
 // One or two rows against a weight stored K x N whose rows direct loads

@@ -243,10 +243,24 @@ struct Paired {
   int64_t lda2, ldb2;
 };
 
+// The gated tile of few rows, 37 KB a step, one workgroup a CU at a time.  Up to
+// 128 workgroups wait for their loads, from there on they share the memory's rate
+// (K = 4096, weights from memory, K whole, split in two, four, eight: 1 x 4096 K x N 36
+// us, 25, 21 and 22; 16 x 8192 K x N 40, 35, 34 and 36, N x K 39, 35, 32 and 44; 1 x
+// 11008 N x K 44, 46, 40 and 48).
+inline double gated_few_time(int layout, int64_t n, int64_t steps) {
+  const double even = (double)n / kCUs, full = (double)((n + kCUs - 1) / kCUs);
+  const double step = n <= 128    ? 1.05
+                      : n <= kCUs ? 1.05 + (n - 128) / 128.0 * 0.45
+                                  : (even + full) / 2 * (layout == 0 ? 1.35 : 1.5);
+  return 4.5 + steps * step;
+}
+
 // The most columns of a tile's right operands, each (for few rows the gated
 // tile is twice as wide as a plain one).
 inline int paired_columns(int kind, int tile) {
-  return kind == kGated ? (tile == kTileFew ? 64 : kTileShape[tile].bn / 2) : kTileShape[tile].bn;
+  if (kind != kGated || tile == kTileRows) return kTileShape[tile].bn;
+  return tile == kTileFew ? 64 : kTileShape[tile].bn / 2;
 }
 
 inline Plan paired_plan(const Paired& q, bool saves) {
@@ -281,6 +295,18 @@ inline Plan paired_plan(const Paired& q, bool saves) {
   r.direct = false;
   r.copy_a = r.copy_b = false;
   double best = 1e300;
+  // All of K in one workgroup of 16 columns of both, by the rule of a plain
+  // product (weights from memory, rows against few: 1 x 4096 x 4096 N x K 16.2 us
+  // and 17.4, K x N 31.5 and 21.3; 16 x 4096 x 1024 6.1 and 7.3, 8.1 and 8.7; 16 x
+  // 8192 x 4096 N x K 33.2 and 31.6).
+  const bool rows_fit = q.kind == kGated && p.M <= 16 && a16 && load_b(kTileRows) == kAsItIs &&
+                        p.K > 0 && p.K % 64 == 0 && (p.lb == 0 || p.N % 8 == 0);
+  const bool rows_win = p.N <= 16 * kCUs && p.K <= (p.lb == 0 ? 4096 : 1024);
+  if (rows_fit && (env_tile < 0 ? rows_win : env_tile == kTileRows)) {
+    r.tile = kTileRows;
+    r.direct = true;
+    best = 0.0;
+  }
   for (int any = 0; any <= 1 && best == 1e300; ++any)
     for (int v = 0; v <= kTileFew + 1; ++v) {  // the last: few rows through registers
       const int t = v < kTileFew ? v : kTileFew;
@@ -303,8 +329,10 @@ inline Plan paired_plan(const Paired& q, bool saves) {
         const int k = env_splits >= 0 ? (int)(env_splits < steps ? env_splits : steps) : s;
         if (env_splits < 0 && s > 1 && steps / s < (direct ? 4 : 1)) break;
         const int64_t run = (steps + s - 1) / s;
-        const double time = (direct ? tile_time(t, n * s * times, run)
-                                    : few_through_registers_time(n * s * times, run)) +
+        const double time = (!direct ? few_through_registers_time(n * s * times, run)
+                             : q.kind == kGated && t == kTileFew
+                                 ? gated_few_time(p.lb, n * s, run)
+                                 : tile_time(t, n * s * times, run)) +
                             copies + (s > 1 ? join_time(p.M, p.N * sums, s) : 0.0);
         if (time < best) {
           best = time;
