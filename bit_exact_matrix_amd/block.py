@@ -76,7 +76,7 @@ def dropout(x, p, seed=0, offset=0, residual=None, stream=None):
                                                          dev)
     p, seed, offset, state = _seeds(p, seed, offset, dev)
     with call:
-        y = call.empty((rows, cols), dt)
+        y = ops._torch.empty_like(x)  # rows of cols elements, whatever x's stride
         rc = _load()["mma_dropout"](t, px, ldx, pr, ldr, y.data_ptr(), cols, rows, cols, p, seed,
                                     offset, state, call.raw)
     _done(rc, "mma_dropout")
@@ -119,17 +119,17 @@ def _params(params, post, pre, dt, cols, dev):
     """(the five pointers, the vectors' type)."""
     if not isinstance(params, ResidualParams):
         raise TypeError("params is a ResidualParams")
-    pointers, kind = [], None
-    for name, t in zip(ResidualParams._fields, params):
-        if t is not None and not (post if name.startswith("post") else
-                                  pre if name.startswith("pre") else True):
+    pointers, kind = [0] * 5, None
+    for i, t in enumerate(params):
+        if t is None:
+            continue
+        name = ResidualParams._fields[i]
+        if i and not (post if i < 3 else pre):
             raise ValueError(f"{name} without that norm")
-        p, k = _vector(t, name, cols, dev, (dt, ops._torch.float32))
-        if k is not None:
-            if kind is not None and t.dtype != kind:
-                raise TypeError("the vectors must be of one type")
-            kind = t.dtype
-        pointers.append(p or 0)
+        pointers[i] = _vector(t, name, cols, dev, (dt, ops._torch.float32))[0] or 0
+        if kind is not None and t.dtype != kind:
+            raise TypeError("the vectors must be of one type")
+        kind = t.dtype
     return pointers, dt if kind is None else kind
 
 
@@ -157,8 +157,8 @@ def residual_norm(x, branch, params=ResidualParams(), post=None, pre=None, scale
     p, seed, offset, state = _seeds(dropout, seed, offset, dev)
     f32 = ops._torch.float32
     with call:
-        r = call.empty((rows, cols), dt)
-        h = call.empty((rows, cols), dt) if kr else None
+        r = ops._torch.empty_like(x)  # rows of cols elements, whatever x's stride
+        h = ops._torch.empty_like(x) if kr else None
         stats = ResidualStats(*(call.empty((rows,), f32) if there else None
                                 for there in (kp == 1, kp, kr == 1, kr)))
         args = _JOIN.pack(t, ops._dt[vt], kp, kr, scale, eps, p, seed, offset, state or 0, rows,
