@@ -25,6 +25,16 @@ _JOIN = struct.Struct("4i2fd3Q2q17Q")
 _JOIN_BACKWARD = struct.Struct("4ifid3Q2q25Q")
 
 
+def _several(call, wanted, n, dtype):
+    """Vectors of n elements, one for each true value of wanted and None for the
+    others, in one allocation (an allocation takes 1.9 us, a view 0.4)."""
+    count = sum(map(bool, wanted))
+    if count < 2:
+        return [call.empty((n,), dtype) if w else None for w in wanted]
+    rows = iter(call.empty((count, n), dtype).unbind(0))
+    return [next(rows) if w else None for w in wanted]
+
+
 def _known(dt, what):
     if dt not in ops._dt:
         raise TypeError(f"{what}: expected float16, bfloat16 or float32, got {dt}")
@@ -159,8 +169,7 @@ def residual_norm(x, branch, params=ResidualParams(), post=None, pre=None, scale
     with call:
         r = ops._torch.empty_like(x)  # rows of cols elements, whatever x's stride
         h = ops._torch.empty_like(x) if kr else None
-        stats = ResidualStats(*(call.empty((rows,), f32) if there else None
-                                for there in (kp == 1, kp, kr == 1, kr)))
+        stats = ResidualStats(*_several(call, (kp == 1, kp, kr == 1, kr), rows, f32))
         args = _JOIN.pack(t, ops._dt[vt], kp, kr, scale, eps, p, seed, offset, state or 0, rows,
                           cols, px, ldx, pb, ldb, *vectors, r.data_ptr(), cols,
                           h.data_ptr() if kr else 0, cols,
@@ -206,10 +215,11 @@ def residual_norm_backward(dr, dh, r, branch, params, stats, post=None, pre=None
     p, seed, offset, state = _seeds(dropout, seed, offset, dev)
     fns = _load()
     with call:
-        dx = call.empty(shape, dt) if need_dx else None
-        db = call.empty(shape, dt) if need_dbranch else None
-        grads = ResidualParams(*(call.empty((cols,), vt) if need_dparams and v is not None
-                                 else None for v in params))
+        # rows of cols elements, whatever the stride of the gradient given
+        dx = ops._torch.empty_like(lead) if need_dx else None
+        db = ops._torch.empty_like(lead) if need_dbranch else None
+        grads = ResidualParams(*_several(
+            call, [need_dparams and v is not None for v in params], cols, vt))
         args = _JOIN_BACKWARD.pack(
             t, ops._dt[vt], kp, kr, scale, 0, p, seed, offset, state or 0, rows, cols, *matrices,
             *vectors[:4], *pointers, dx.data_ptr() if need_dx else 0, cols,
@@ -226,6 +236,9 @@ def residual_norm_backward(dr, dh, r, branch, params, stats, post=None, pre=None
 def _weights(w_gate, w_up, dt, dev):
     """(pointer and ld of both, transposed)."""
     pg, ldg, tg = _weight(w_gate, "w_gate", dt, dev)
+    if (isinstance(w_up, ops._torch.Tensor) and w_up.dtype == dt and w_up.device == dev
+            and w_up.shape == w_gate.shape and w_up.stride() == w_gate.stride()):
+        return pg, ldg, w_up.data_ptr(), ldg, tg
     pu, ldu, tu = _weight(w_up, "w_up", dt, dev)
     if w_up.shape != w_gate.shape:
         raise ValueError(f"w_up must have shape {tuple(w_gate.shape)}, got {tuple(w_up.shape)}")
@@ -346,7 +359,7 @@ def gated_linear_backward(dy, x, w_gate, w_up, kept, activation="silu", need_dx=
         dw = [None, None]
         if need_dw:
             dw = [call.empty((n, k), wd).t() if wt else call.empty((k, n), wd) for _ in range(2)]
-        db = [call.empty((n,), bd) if need_dbias else None for _ in range(2)]
+        db = _several(call, (need_dbias, need_dbias), n, bd)
         ldw = k if wt else n
         args = _GATED_BACKWARD.pack(
             t, ops._dt[wd], ops._dt[bd], act, wt, 0, m, n, k, pd, ldd, px, ldx, xc, xs, pg, ldg,

@@ -740,7 +740,10 @@ int mma_residual_norm_backward(const mma_residual_norm_backward_args* args, void
     const JoinSums j{a.partial, plan.groups, r.param_dtype, r.cols, r.gate, r.post_weight,
                      r.post_bias, r.post != kNormNone, r.dgate, r.dpost_weight, r.dpost_bias,
                      r.dpre_weight, r.dpre_bias};
-    const uint32_t grid = (uint32_t)((r.cols + 31) / 32);
+    const int64_t blocks = (r.cols + 31) / 32;
+    constexpr int64_t kMost = 1 << 20;
+    const dim3 grid((uint32_t)(blocks < kMost ? blocks : kMost),
+                    (uint32_t)((blocks + kMost - 1) / kMost));
     if (plan.shift)
       join_sums_kernel<true><<<grid, 1024, 0, s>>>(j);
     else

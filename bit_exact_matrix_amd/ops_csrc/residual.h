@@ -686,18 +686,19 @@ struct JoinSums {
 };
 
 // The groups' sums in group order within each of 32 runs and then in run
-// order: 32 columns a workgroup.
+// order: 32 columns a workgroup.  SHIFT: p0 and s0 are there.
 template <bool SHIFT>
 __global__ __launch_bounds__(1024) void join_sums_kernel(JoinSums a) {
   __shared__ float meet[4][32][32], total[4][32];
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  // a grid has fewer than 2^32 lanes in x: the longest rows take several of it
+  const int64_t c = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 32 + lane;
   const int run = (a.count + 31) / 32;
   const int p0 = part * run, p1 = p0 + run < a.count ? p0 + run : a.count;
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < a.cols) {
     const float* const p = a.partial + c;
-#pragma unroll 4
+#pragma unroll 8
     for (int q = p0; q < p1; ++q)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
