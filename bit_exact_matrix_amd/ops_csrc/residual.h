@@ -342,7 +342,13 @@ struct Vectors {
       q[j] = pack<PDT, V>(v);
     }
   }
-  __device__ __forceinline__ void values(int j, float (&v)[V]) const { unpack(q[j], v); }
+  // Two vectors a lane: unpacked where they are used, in every row; taken out of
+  // the loop they would hold twice the registers.  One: unpacked once (the forward
+  // pass of 8192 x 4096 bf16 54 us, in every row 59).
+  __device__ __forceinline__ void values(int j, float (&v)[V]) {
+    if constexpr (NV > 1) hide(q[j]);
+    unpack(q[j], v);
+  }
 };
 
 // Mean and rstd of a row held by GT lanes, NV vectors each, which are centred
