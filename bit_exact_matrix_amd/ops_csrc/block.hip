@@ -88,48 +88,68 @@ int check_join(const mma_residual_norm_args& r, DropArgs* d) {
   return v.clash() ? MMAEMU_ERR_ALIAS : MMAEMU_OK;
 }
 
-// How a row is held: lanes a row, vectors a lane; no lanes where it is too long.
+// How a row is held: waves a row and vectors a lane; no waves where it is too
+// long for registers.
 struct RowPlan {
-  int gt, nv;
+  int waves, nv;
 };
 
-// One vector a lane and as many waves as the row needs, up to 1024 lanes;
-// then `most`.
-RowPlan row_plan(int64_t cols, int V, int most) {
+// One vector a lane and as many waves as the row needs, up to 16; then two.
+RowPlan row_plan(int64_t cols, int V) {
   const int64_t vecs = (cols + V - 1) / V;
-  int gt = 64;
-  while (gt < 1024 && gt < vecs) gt *= 2;
-  if (vecs <= gt) return {gt, 1};
-  return vecs <= 1024 * most ? RowPlan{1024, most} : RowPlan{0, 0};
+  if (vecs <= 1024) return {(int)((vecs + 63) / 64), 1};
+  if (vecs > 2048) return {0, 0};
+  return {(int)((vecs + 127) / 128), 2};
 }
 
-// Workgroups of a row's lanes (four rows of one wave), as many as the CUs
-// hold at once.
-template <int DT, int PDT, int GT, int NV>
-void join_run(const JoinArgs& a, hipStream_t s) {
-  constexpr int G = GT == 64 ? 4 : 1;
-  const int64_t groups = (a.rows + G - 1) / G;
-  constexpr int kPerCU = 1024 / (GT * G);
-  const uint32_t grid = (uint32_t)(groups < kCUs * kPerCU ? groups : kCUs * kPerCU);
-  join_kernel<DT, PDT, GT, NV, G><<<grid, GT * G, 0, s>>>(a);
+// Workgroups of a row's waves (four rows of one wave), as many as the CUs
+// hold at once: 20 waves with one vector a lane, 16 with two.
+template <int DT, int PDT, int W, int NV>
+void join_run(const JoinArgs& a, int waves, hipStream_t s) {
+  constexpr int G = W == 1 ? 4 : 1;
+  const int64_t groups = (a.rows + G - 1) / G, per = (NV == 1 ? 20 : 16) / (waves * G);
+  const int64_t most = kCUs * (per > 1 ? per : 1);
+  join_kernel<DT, PDT, W, NV, G>
+      <<<(uint32_t)(groups < most ? groups : most), waves * 64 * G, 0, s>>>(a);
 }
 
 template <int DT, int PDT>
 hipError_t join_launch(const JoinArgs& a, hipStream_t s) {
-  const RowPlan p = row_plan(a.cols, kVec<DT>, 2);
-  switch (p.gt * p.nv) {
-    case 64: join_run<DT, PDT, 64, 1>(a, s); break;
-    case 128: join_run<DT, PDT, 128, 1>(a, s); break;
-    case 256: join_run<DT, PDT, 256, 1>(a, s); break;
-    case 512: join_run<DT, PDT, 512, 1>(a, s); break;
-    case 1024: join_run<DT, PDT, 1024, 1>(a, s); break;
-    case 2048: join_run<DT, PDT, 1024, 2>(a, s); break;
-    default: {
-      const uint32_t grid = (uint32_t)(a.rows < 2 * kCUs ? a.rows : 2 * kCUs);
-      join_long_kernel<DT, PDT><<<grid, 1024, 0, s>>>(a);
-    }
+  const RowPlan p = row_plan(a.cols, kVec<DT>);
+  if (p.waves == 0) {
+    const uint32_t grid = (uint32_t)(a.rows < 2 * kCUs ? a.rows : 2 * kCUs);
+    join_long_kernel<DT, PDT><<<grid, 1024, 0, s>>>(a);
+  } else if (p.nv == 2) {
+    join_run<DT, PDT, 16, 2>(a, p.waves, s);
+  } else if (p.waves == 1) {
+    join_run<DT, PDT, 1, 1>(a, 1, s);
+  } else if (p.waves <= 4) {
+    join_run<DT, PDT, 4, 1>(a, p.waves, s);
+  } else if (p.waves <= 8) {
+    join_run<DT, PDT, 8, 1>(a, p.waves, s);
+  } else {
+    join_run<DT, PDT, 16, 1>(a, p.waves, s);
   }
   return hipGetLastError();
+}
+
+// The backward pass: elements a lane and waves a row (8 elements of FP32, two
+// vectors, take the registers that one vector of the 16-bit types does: 3276 x 5120
+// 212 us in several passes over the rows, so 128), and the rows that a workgroup
+// works on at a time.
+struct BackPlan {
+  int v, waves, rows;  // waves 0: in several passes
+};
+BackPlan back_plan(int64_t cols, int dt) {
+  const int one = dt == kFP32 ? 4 : 8;
+  for (int v = one; v <= 8; v *= 2) {
+    const int64_t waves = (cols + 64 * v - 1) / (64 * v);
+    if (waves <= 16) {
+      const int w = (int)waves;
+      return {v, w, w <= 2 ? 8 / w : w <= 4 ? 2 : 1};
+    }
+  }
+  return {one, 0, 32};
 }
 
 // The launch and its workspace: the groups' column sums, then the rows' means
@@ -141,22 +161,23 @@ struct JoinPlan {
   int64_t bytes;
 };
 
-// Workgroups of 512 lanes (1024 for the longest rows), as many as the CUs hold
-// at once, each with its own row of partial sums.
+// Workgroups as many as the CUs hold at once, 16 waves each, with a row of
+// partial sums for each.
 JoinPlan join_plan(const mma_residual_norm_backward_args& r) {
   JoinPlan p{};
   if (r.rows == 0) return p;
   p.sums = r.dgate || r.dpost_weight || r.dpost_bias || r.dpre_weight || r.dpre_bias;
   p.shift = r.dpre_bias || r.dpost_bias || (r.dgate && r.post != kNormNone && r.post_bias);
-  const int gt = row_plan(r.cols, r.dtype == kFP32 ? 4 : 8, 1).gt;
-  const int64_t per = gt ? (gt < 512 ? 512 / gt : 1) : 32, runs = (r.rows + per - 1) / per;
-  const int64_t most = gt && gt <= 512 ? 2 * kCUs : kCUs;
+  const BackPlan b = back_plan(r.cols, r.dtype);
+  const int waves = b.waves;
+  const int64_t per = b.rows, runs = (r.rows + per - 1) / per;
+  const int64_t most = kCUs * (waves && waves <= 8 ? 16 / (waves * per) : 1);
   p.groups = (int)(runs < most ? runs : most);
   if (!p.sums) return p;
   p.means_at = up256((int64_t)p.groups * 4 * r.cols * 4);
   const int64_t spare =
-      gt && !r.dX && !r.dbranch ? p.groups * per * r.cols * elem_bytes(r.dtype) : 0;
-  p.bytes = p.means_at + up256(gt ? spare : r.rows * 8);
+      waves && !r.dX && !r.dbranch ? p.groups * per * r.cols * elem_bytes(r.dtype) : 0;
+  p.bytes = p.means_at + up256(waves ? spare : r.rows * 8);
   return p;
 }
 
@@ -218,36 +239,44 @@ int check_join_backward(const mma_residual_norm_backward_args& r, int64_t ws_byt
   return v.clash() ? MMAEMU_ERR_ALIAS : MMAEMU_OK;
 }
 
-template <int DT, int PDT, int GT, bool SHIFT>
-hipError_t join_backward_run(const JoinArgs& a, int groups, hipStream_t s) {
-  constexpr int G = GT < 512 ? 512 / GT : 1;
-  if (a.cols == GT * kVec<DT>)
-    join_backward_kernel<DT, PDT, GT, G, SHIFT, true><<<(uint32_t)groups, GT * G, 0, s>>>(a);
+template <int DT, int PDT, int V, int W, int G, bool SHIFT>
+hipError_t join_backward_run(const JoinArgs& a, int waves, int groups, hipStream_t s) {
+  if (a.cols == waves * 64 * V)
+    join_backward_kernel<DT, PDT, V, W, G, SHIFT, true>
+        <<<(uint32_t)groups, waves * 64 * G, 0, s>>>(a);
   else
-    join_backward_kernel<DT, PDT, GT, G, SHIFT, false><<<(uint32_t)groups, GT * G, 0, s>>>(a);
+    join_backward_kernel<DT, PDT, V, W, G, SHIFT, false>
+        <<<(uint32_t)groups, waves * 64 * G, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <int DT, int PDT, int GT>
-hipError_t join_backward_run(const JoinArgs& a, int groups, bool shift, hipStream_t s) {
-  return shift ? join_backward_run<DT, PDT, GT, true>(a, groups, s)
-               : join_backward_run<DT, PDT, GT, false>(a, groups, s);
+template <int DT, int PDT, int V, int W, int G>
+hipError_t join_backward_run(const JoinArgs& a, int waves, int groups, bool shift, hipStream_t s) {
+  return shift ? join_backward_run<DT, PDT, V, W, G, true>(a, waves, groups, s)
+               : join_backward_run<DT, PDT, V, W, G, false>(a, waves, groups, s);
 }
 
 template <int DT, int PDT>
 hipError_t join_backward_launch(const JoinArgs& a, int groups, bool shift, hipStream_t s) {
-  switch (row_plan(a.cols, kVec<DT>, 1).gt) {
-    case 64: return join_backward_run<DT, PDT, 64>(a, groups, shift, s);
-    case 128: return join_backward_run<DT, PDT, 128>(a, groups, shift, s);
-    case 256: return join_backward_run<DT, PDT, 256>(a, groups, shift, s);
-    case 512: return join_backward_run<DT, PDT, 512>(a, groups, shift, s);
-    case 1024: return join_backward_run<DT, PDT, 1024>(a, groups, shift, s);
+  constexpr int V = kVec<DT>;
+  const BackPlan b = back_plan(a.cols, DT);
+  if constexpr (DT == kFP32) {
+    if (b.v == 8) return join_backward_run<DT, PDT, 8, 16, 1>(a, b.waves, groups, shift, s);
+  }
+  switch (b.waves) {  // the rows at a time: back_plan
+    case 0: break;
+    case 1: return join_backward_run<DT, PDT, V, 1, 8>(a, 1, groups, shift, s);
+    case 2: return join_backward_run<DT, PDT, V, 2, 4>(a, 2, groups, shift, s);
+    case 3: return join_backward_run<DT, PDT, V, 3, 2>(a, 3, groups, shift, s);
+    case 4: return join_backward_run<DT, PDT, V, 4, 2>(a, 4, groups, shift, s);
+    default:
+      return b.waves <= 8 ? join_backward_run<DT, PDT, V, 8, 1>(a, b.waves, groups, shift, s)
+                          : join_backward_run<DT, PDT, V, 16, 1>(a, b.waves, groups, shift, s);
   }
   const uint32_t grid = (uint32_t)(a.rows < 2 * kCUs ? a.rows : 2 * kCUs);
   join_long_dx_kernel<DT, PDT><<<grid, 1024, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.partial) return e;
-  constexpr int V = kVec<DT>;
   const dim3 sums((uint32_t)((a.cols + 64 * V - 1) / (64 * V)), (uint32_t)groups);
   join_long_sums_kernel<DT, PDT><<<sums, 256, 0, s>>>(a, (a.rows + groups - 1) / groups);
   return hipGetLastError();

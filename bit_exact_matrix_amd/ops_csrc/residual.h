@@ -329,14 +329,55 @@ __global__ __launch_bounds__(256) void join_long_sums_kernel(JoinArgs a, int64_t
 }
 
 // ------------------------------------------------------ rows in registers
+// A row is held by whole waves, no more than it needs: W of them where a
+// workgroup has G > 1 rows (or W = 1), up to W where it has one, as many as the
+// workgroup has.  (Powers of two of waves left lanes idle, and bytes in flight with
+// them: 13107 x 2560 bf16 forward 78 us, so 58; 6553 x 5120 backward 136 and 91.)
+template <int W, int G>
+__device__ __forceinline__ int row_lanes() {
+  return G > 1 || W == 1 ? W * 64 : (int)blockDim.x;
+}
+
+// Sums of N values over a row's waves, the same in each of its lanes, as row_sum
+// has them.  `lds` has 2 * 16 * N floats, zeros at first: those of waves that
+// are not there stay zero.
+template <int N>
+__device__ __forceinline__ void join_sum_start(float* lds) {
+  if (threadIdx.x < 2 * 16 * N) lds[threadIdx.x] = 0.0f;
+  __syncthreads();
+}
+template <int W, int G, int N>
+__device__ __forceinline__ void join_sum(float (&v)[N], float* lds, int& turn) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (W > 1) {
+    float* const buf = lds + turn * 16 * N;
+    turn ^= 1;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) buf[wave * N + i] = v[i];
+    }
+    __syncthreads();
+    const int first = G > 1 ? wave / W * W : 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) s += buf[(first + w) * N + i];
+      v[i] = s;
+    }
+  }
+}
+
 // A parameter's vectors as they are in memory, for all of a lane's columns.
-template <int PDT, int V, int NV, int GT>
+template <int PDT, int V, int NV>
 struct Vectors {
   Pack<PDT, V> q[NV];
-  __device__ __forceinline__ void load(const void* p, int lane, int cols, float fill) {
+  __device__ __forceinline__ void load(const void* p, int lane, int lanes, int cols, float fill) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * GT + lane) * V;
+      const int c = (j * lanes + lane) * V;
       float v[V];
       param<PDT, V>(p, c, cols - c, fill, v);
       q[j] = pack<PDT, V>(v);
@@ -351,11 +392,11 @@ struct Vectors {
   }
 };
 
-// Mean and rstd of a row held by GT lanes, NV vectors each, which are centred
+// Mean and rstd of a row held by its lanes, NV vectors each, which are centred
 // on the way (0 past the row's end).  As in norm_kernel.
-template <int GT, int NV, int V>
-__device__ __forceinline__ void held_stats(float (&v)[NV][V], int lane, int cols, bool layer,
-                                           float eps, float* lds, int& turn, float& mean,
+template <int W, int G, int NV, int V>
+__device__ __forceinline__ void held_stats(float (&v)[NV][V], int lane, int lanes, int cols,
+                                           bool layer, float eps, float* lds, int& turn, float& mean,
                                            float& rstd) {
   const float n_f = (float)cols;
   float s[1], mu = 0.0f;
@@ -363,11 +404,11 @@ __device__ __forceinline__ void held_stats(float (&v)[NV][V], int lane, int cols
     s[0] = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) s[0] += pair_sum(v[j]);
-    row_sum<GT, 1>(s, lds, turn);
+    join_sum<W, G, 1>(s, lds, turn);
     mu = s[0] / n_f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int n = cols - (j * GT + lane) * V;
+      const int n = cols - (j * lanes + lane) * V;
 #pragma unroll
       for (int i = 0; i < V; ++i) v[j][i] = i < n ? v[j][i] - mu : 0.0f;
     }
@@ -380,7 +421,7 @@ __device__ __forceinline__ void held_stats(float (&v)[NV][V], int lane, int cols
     for (int i = 0; i < V; ++i) t[i] = v[j][i] * v[j][i];
     s[0] += pair_sum(t);
   }
-  row_sum<GT, 1>(s, lds, turn);
+  join_sum<W, G, 1>(s, lds, turn);
   float var = s[0] / n_f;
   mean = mu;
   // the same in all lanes that meet at its barriers
@@ -388,7 +429,7 @@ __device__ __forceinline__ void held_stats(float (&v)[NV][V], int lane, int cols
     s[0] = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) s[0] += pair_sum(v[j]);
-    row_sum<GT, 1>(s, lds, turn);
+    join_sum<W, G, 1>(s, lds, turn);
     const float d = s[0] / n_f;
     row_correct(d, mean, var);
 #pragma unroll
@@ -399,25 +440,27 @@ __device__ __forceinline__ void held_stats(float (&v)[NV][V], int lane, int cols
   rstd = 1.0f / sqrtf(var + eps);
 }
 
-// A row is held by GT lanes, NV vectors of 16 bytes of each matrix; a
-// workgroup works on G rows at a time (several only where a row is a wave) and
-// walks the matrices, the next rows' loads under way.
-template <int DT, int PDT, int GT, int NV, int G>
-__global__ __launch_bounds__(GT* G, 4) void join_kernel(JoinArgs a) {
+// A lane has NV vectors of 16 bytes of each matrix's row; a workgroup works on
+// G rows at a time (several only where a row is a wave) and walks the matrices,
+// the next rows' loads under way.
+template <int DT, int PDT, int W, int NV, int G>
+__global__ __launch_bounds__(W * 64 * G, NV == 1 ? 5 : 4) void join_kernel(JoinArgs a) {
   constexpr int V = kVec<DT>;
   using E = elem_t<DT>;
-  static_assert(G == 1 || GT == 64, "");
+  static_assert(G == 1 || W == 1, "");
   __shared__ float lds[2 * 16];
-  const int lane = threadIdx.x % GT;
-  const int g = __builtin_amdgcn_readfirstlane(threadIdx.x / GT);  // whole waves
+  const int lanes = row_lanes<W, G>();
+  const int lane = G > 1 ? threadIdx.x % (W * 64) : threadIdx.x;
+  const int g = G > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / (W * 64)) : 0;
+  join_sum_start<1>(lds);
   int turn = 0;
   const Drop drop(a.drop);
-  Vectors<PDT, V, NV, GT> gate, post_w, post_b, pre_w, pre_b;
-  gate.load(a.gate, lane, a.cols, 1.0f);
-  post_w.load(a.post_w, lane, a.cols, 1.0f);
-  post_b.load(a.post_b, lane, a.cols, 0.0f);
-  pre_w.load(a.pre_w, lane, a.cols, 1.0f);
-  pre_b.load(a.pre_b, lane, a.cols, 0.0f);
+  Vectors<PDT, V, NV> gate, post_w, post_b, pre_w, pre_b;
+  gate.load(a.gate, lane, lanes, a.cols, 1.0f);
+  post_w.load(a.post_w, lane, lanes, a.cols, 1.0f);
+  post_b.load(a.post_b, lane, lanes, a.cols, 0.0f);
+  pre_w.load(a.pre_w, lane, lanes, a.cols, 1.0f);
+  pre_b.load(a.pre_b, lane, lanes, a.cols, 0.0f);
   const int64_t step = (int64_t)gridDim.x * G;
   Pack<DT, V> xr[NV], br[NV];
   auto fetch = [&](int64_t row) {
@@ -426,7 +469,7 @@ __global__ __launch_bounds__(GT* G, 4) void join_kernel(JoinArgs a) {
     const E* const b = (const E*)a.branch + (live ? row : 0) * a.ldb;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * GT + lane) * V;
+      const int c = (j * lanes + lane) * V;
       br[j] = load_pack<DT, V>(b + c, live ? a.cols - c : 0);
       xr[j] = load_pack<DT, V>(x + c, live ? a.cols - c : 0);
     }
@@ -446,7 +489,7 @@ __global__ __launch_bounds__(GT* G, 4) void join_kernel(JoinArgs a) {
     if (r0 + step < a.rows) fetch(row + step);
     float pm = 0.0f, pr = 1.0f, m = 0.0f, q = 1.0f;
     if (a.post != kNormNone) {
-      held_stats<GT, NV, V>(v, lane, a.cols, a.post == kNormLayer, a.eps, lds, turn, pm, pr);
+      held_stats<W, G, NV, V>(v, lane, lanes, a.cols, a.post == kNormLayer, a.eps, lds, turn, pm, pr);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float w[V], b[V];
@@ -458,7 +501,7 @@ __global__ __launch_bounds__(GT* G, 4) void join_kernel(JoinArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * GT + lane) * V;
+      const int c = (j * lanes + lane) * V;
       if (drop.threshold) {
         uint32_t w[V / 2];
         drop.halves<V>(row, c, w);
@@ -475,14 +518,14 @@ __global__ __launch_bounds__(GT* G, 4) void join_kernel(JoinArgs a) {
       // past the row's end there may be a bias by now
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int n = a.cols - (j * GT + lane) * V;
+        const int n = a.cols - (j * lanes + lane) * V;
 #pragma unroll
         for (int i = 0; i < V; ++i) v[j][i] = i < n ? v[j][i] : 0.0f;
       }
-      held_stats<GT, NV, V>(v, lane, a.cols, a.pre == kNormLayer, a.eps, lds, turn, m, q);
+      held_stats<W, G, NV, V>(v, lane, lanes, a.cols, a.pre == kNormLayer, a.eps, lds, turn, m, q);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (j * GT + lane) * V;
+        const int c = (j * lanes + lane) * V;
         float w[V], b[V];
         pre_w.values(j, w);
         pre_b.values(j, b);
@@ -501,20 +544,20 @@ __global__ __launch_bounds__(GT* G, 4) void join_kernel(JoinArgs a) {
 }
 
 // The gradients of x and of the branch, and the workgroup's part of the
-// column sums (SHIFT: p0 and s0 too, which only biases need): one vector a lane,
-// rows of GT lanes, G at a time.  What a row's sums need is made again from the
+// column sums (SHIFT: p0 and s0 too, which only biases need): V elements a lane,
+// G rows at a time (WHOLE: all of a row's lanes have them).  What a row's sums need is made again from the
 // loaded elements after they have met.  Each matrix's next row is loaded as soon as
 // this one's has been used, with no registers of its own.  An element past a
 // row's end adds 0 to the row's sums, as its dh is 0 in the first ones and inner_w
 // in the second (unless the row's statistics are not finite, and then neither is
 // the row).
-template <int DT, int PDT, int GT, int G, bool SHIFT, bool WHOLE>
-__global__ __launch_bounds__(GT* G, 4) void join_backward_kernel(JoinArgs a) {
-  constexpr int V = kVec<DT>;
+template <int DT, int PDT, int V, int W, int G, bool SHIFT, bool WHOLE>
+__global__ __launch_bounds__(W * 64 * G, 4) void join_backward_kernel(JoinArgs a) {
   using E = elem_t<DT>;
   __shared__ float lds[2 * 16 * 2];
-  const int lane = threadIdx.x % GT;
-  const int g = __builtin_amdgcn_readfirstlane(threadIdx.x / GT);  // whole waves
+  const int lane = G > 1 ? threadIdx.x % (W * 64) : threadIdx.x;
+  const int g = G > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / (W * 64)) : 0;
+  join_sum_start<2>(lds);
   const int c = lane * V, n = WHOLE ? V : a.cols - c;
   int turn = 0;
   const Drop drop(a.drop);
@@ -596,7 +639,7 @@ __global__ __launch_bounds__(GT* G, 4) void join_backward_kernel(JoinArgs a) {
         p1[i] += d[i] * rh[i];
         if (SHIFT) p0[i] += d[i];
       }
-      row_sum<GT, 2>(s, lds, turn);
+      join_sum<W, G, 2>(s, lds, turn);
       const float m0 = a.pre == kNormLayer ? s[0] / n_f : 0.0f, m1 = s[1] / n_f;
       unpack(dr, t);
 #pragma unroll
@@ -647,7 +690,7 @@ __global__ __launch_bounds__(GT* G, 4) void join_backward_kernel(JoinArgs a) {
         s[0] += t[i];
         s[1] += t[i] * b[i];
       }
-      row_sum<GT, 2>(s, lds, turn);
+      join_sum<W, G, 2>(s, lds, turn);
       const float k0 = a.post == kNormLayer ? s[0] / n_f : 0.0f, k1 = s[1] / n_f;
 #pragma unroll
       for (int i = 0; i < V; ++i) t[i] = pr_now * (t[i] - k0 - b[i] * k1);
@@ -663,6 +706,7 @@ __global__ __launch_bounds__(GT* G, 4) void join_backward_kernel(JoinArgs a) {
       if (SHIFT || k % 2 == 0)
         store_pack<kFP32, V>(out + k * a.cols + c, pack<kFP32, V>(*sums[k]), n);
   } else {  // the G rows' sums meet in LDS, in group order
+    constexpr int GT = W * 64;
     __shared__ float meet[G][GT * V];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {

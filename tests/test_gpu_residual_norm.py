@@ -62,7 +62,8 @@ def check(torch, dev, rows, cols, dtype, vt, post, pre, gate, bias, p, scale, pa
 
 
 SHAPES = [(1, 1), (3, 7), (2, 64), (70, 33), (5, 513), (37, 1000), (9, 4096), (4, 4104), (3, 8200),
-          (2, 16384), (2, 20001), (300, 96), (1100, 260)]
+          (2, 16384), (2, 20001), (300, 96), (1100, 260), (1030, 640), (6, 1536), (5, 2560),
+          (3, 5120), (3, 8192), (2, 10240)]
 
 
 @pytest.mark.parametrize("dt", DT)
