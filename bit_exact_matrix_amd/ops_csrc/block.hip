@@ -31,12 +31,20 @@ hipError_t dropout_launch(const void* x, int64_t ldx, const void* residual, int6
                           int64_t ldy, int64_t rows, int64_t cols, const DropArgs& d,
                           hipStream_t s) {
   const int64_t vecs = (cols + 7) / 8;
-  int shift = 4;
-  while (shift < 8 && (int64_t(1) << shift) < vecs) ++shift;
-  const int64_t per = 256 >> shift, gx = (rows + per - 1) / per;
-  const int64_t gy = (vecs + (int64_t(1) << shift) - 1) >> shift;
+  DropGrid cut{4, 0, 0};
+  while (cut.shift < 8 && (int64_t(1) << cut.shift) < vecs) ++cut.shift;
+  const bool exact = vecs <= 128 && vecs != (int64_t(1) << cut.shift);
+  cut.lanes = exact ? (int)vecs : 1 << cut.shift;
+  cut.inverse = 65536 / cut.lanes + 1;
+  const int64_t per = 256 / cut.lanes, gx = (rows + per - 1) / per;
+  const int64_t gy = (vecs + cut.lanes - 1) / cut.lanes;
   const dim3 grid((uint32_t)(gx < (1 << 22) ? gx : (1 << 22)), (uint32_t)(gy < 256 ? gy : 256));
-  dropout_kernel<DT><<<grid, 256, 0, s>>>(x, ldx, residual, ldr, y, ldy, rows, cols, d, shift);
+  if (exact)
+    dropout_kernel<DT, true><<<grid, 256, 0, s>>>(x, ldx, residual, ldr, y, ldy, rows, cols, d,
+                                                  cut);
+  else
+    dropout_kernel<DT, false><<<grid, 256, 0, s>>>(x, ldx, residual, ldr, y, ldy, rows, cols, d,
+                                                   cut);
   return hipGetLastError();
 }
 

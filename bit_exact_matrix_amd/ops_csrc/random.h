@@ -8,8 +8,10 @@
 // so a mask goes by an element's place alone: not by the kernel, the tile or
 // the number of rows, and whoever needs it again makes it again.
 //
-// 16 bits an element: keeping is decided to within 2^-16 of p, and what is
-// kept is divided by the share that truly is, (65536 - T) / 65536.
+// 16 bits an element: keeping is decided to within 2^-17 of p, and what is
+// kept is divided by the share that truly is, (65536 - T) / 65536.  32 bits take two
+// calls for eight elements: 8192 x 4096 bf16 33 us, so 24.5 (134 MB, 5.5 TB/s, a
+// copy's rate); in the forward residual sum 60 and 54.
 #ifndef MMAOPS_RANDOM_H
 #define MMAOPS_RANDOM_H
 
@@ -97,21 +99,32 @@ struct Drop {
   }
 };
 
-// y = drop(x) + residual, each element read and written once.  A workgroup
-// of 256 lanes is cut into rows of 2^shift lanes, as many as a row has groups
-// of 8 elements (16 at least).
-template <int DT>
+// y = drop(x) + residual, each element read and written once, 8 a lane.  A
+// workgroup of 256 lanes is cut into rows of 2^shift lanes, as many as a row has
+// groups of 8 elements (16 at least), or, with EXACT, for short rows, into rows of
+// `lanes` lanes, as many as there are groups: fewer stand idle (bf16, 104857 x 320
+// 39 us and 30, 52428 x 640 35 and 31), but the address takes more (8192 x 4096 24.5
+// and 28).  inverse: 65536 / lanes + 1, with which a lane's row is found in one
+// product, exact below 256.
+struct DropGrid {
+  int shift, lanes, inverse;
+};
+template <int DT, bool EXACT>
 __global__ __launch_bounds__(256) void dropout_kernel(const void* x, int64_t ldx,
                                                       const void* residual, int64_t ldr, void* y,
                                                       int64_t ldy, int64_t rows, int64_t cols,
-                                                      DropArgs args, int shift) {
+                                                      DropArgs args, DropGrid cut) {
   constexpr int V = 8;
   using E = elem_t<DT>;
   const Drop drop(args);
-  const int lane = threadIdx.x & ((1 << shift) - 1), g = threadIdx.x >> shift;
-  const int64_t step = (int64_t)gridDim.x * (256 >> shift);
-  const int64_t c0 = ((int64_t)blockIdx.y << shift) * V, cstep = ((int64_t)gridDim.y << shift) * V;
-  for (int64_t row = (int64_t)blockIdx.x * (256 >> shift) + g; row < rows; row += step)
+  const int lanes = EXACT ? cut.lanes : 1 << cut.shift;
+  const int per = EXACT ? 256 / lanes : 256 >> cut.shift;
+  const int g = EXACT ? (int)threadIdx.x * cut.inverse >> 16 : (int)threadIdx.x >> cut.shift;
+  const int lane = EXACT ? (int)threadIdx.x - g * lanes : (int)threadIdx.x & (lanes - 1);
+  if (EXACT && g >= per) return;
+  const int64_t step = (int64_t)gridDim.x * per;
+  const int64_t c0 = (int64_t)blockIdx.y * lanes * V, cstep = (int64_t)gridDim.y * lanes * V;
+  for (int64_t row = (int64_t)blockIdx.x * per + g; row < rows; row += step)
     for (int64_t c = c0 + lane * V; c < cols; c += cstep) {
       const int n = cols - c < V ? (int)(cols - c) : V;
       float v[V], r[V];
