@@ -11,6 +11,11 @@
 // rounded to the operands' type, and their column sums before that.  Then
 //   dX = dg Wg^T + du Wu^T   one product with an inner size of 2 N
 //   dWg = X^T dg, dWu = X^T du   the tiles of both in one launch
+//
+// Measured (one MI355X).  4096 x 4096 x 4096 bf16, gelu, both biases: 207 us for
+// 275 GFLOP (1.33 PFLOP/s, the plain product's rate; 569 on small tiles).  Its
+// backward pass from checkpoints: dg and du 29, dX 210, both dW 240.  1 x 4096 x
+// 4096 bf16, both W N x K: 13 (67 MB, again and again; 16 from memory, 4.2 TB/s).
 #ifndef MMAOPS_GATED_H
 #define MMAOPS_GATED_H
 
@@ -35,7 +40,8 @@ __global__ __launch_bounds__(256, 1) void joint_wide_kernel(args_t<MODE> g) {
   wide_product<DT, 0, LB, BM, BN, STAGES, MODE>(g, block, blockIdx.y, smem);
 }
 
-// Up to 16 rows in one launch, BN / 2 output columns a workgroup.
+// Up to 16 rows in one launch, BN / 2 output columns a workgroup: bound by the
+// weights' bytes.
 template <int DT, int LB, int BN>
 __global__ __launch_bounds__(512, 2) void gate_rows_kernel(GateArgs g) {
   __shared__ __attribute__((aligned(1024))) char smem[kRowsBytes];
@@ -69,7 +75,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void two_kernel(TwoArgs p) {
 
 // A small backward pass's second launch: the tiles of dg Wg^T + du Wu^T, those of
 // both weight gradients, then the column sums of both biases, 64 columns a
-// workgroup; all need only the first launch's results.
+// workgroup; all need only the first launch's results.  Launches bound such a
+// pass (fp16, silu, 299 x 260 x 640, on the GPU: four launches 27 us, two 14.5).
 struct SmallArgs {
   LongArgs dx;
   TwoArgs dw;
@@ -124,7 +131,8 @@ __global__ __launch_bounds__(256, 2) void gated_small_kernel(SmallArgs p) {
 }
 
 // The runs' sums of both halves added in run order, then the epilogue: four
-// columns a lane, eight neighbouring lanes for a checkpoint block.
+// columns a lane, eight neighbouring lanes for a checkpoint block.  A launch's
+// fixed cost, mostly (16 x 8192: 4.2 to 4.7 us for two runs or four).
 template <int DT>
 __global__ __launch_bounds__(64) void gate_finish_kernel(GateArgs g) {
   const int64_t quads = (g.N + kBlock - 1) / kBlock * (kBlock / 4);  // of a row
@@ -249,7 +257,8 @@ __device__ __forceinline__ void act_both(const float (&z)[V], const int act, flo
 // dg, du and their column sums over the workgroup's run of rows: 64 lanes of
 // 8 columns, four waves over the rows, the waves' sums added in wave order.  The
 // activation is the kernel's own: with a switch in it, it held the registers
-// of the largest.
+// of the largest.  Bound by memory (4096 x 4096 bf16 from both checkpoints: 26.3
+// to 28.6 us for 135 MB, 5 TB/s), so dg and du leave in one pass.
 template <int DT, int ACT, bool SAVED>
 __global__ __launch_bounds__(256, 4) void gate_dz_kernel(GateDzArgs a) {
   constexpr int V = 8;

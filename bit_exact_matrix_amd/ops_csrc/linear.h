@@ -20,7 +20,8 @@
 // and for few rows (16 x 64, also through registers where an operand allows
 // no direct load); linear_rows_kernel for up to 16 rows in one launch.
 // Where there are few tiles, K is split over workgroups and
-// linear_finish_kernel adds the runs in order.
+// linear_finish_kernel adds the runs in order.  Their bodies take products of
+// more operands too (kGate, kLong below), for the kernels of gated.h.
 //
 // LDS banks.  A layout-0 tile row is BK elements; 16-byte chunk c of row r
 // is kept at chunk c ^ (r & 7), so that the rows of a fragment read spread

@@ -10,7 +10,7 @@
 //
 // 16 bits an element: keeping is decided to within 2^-17 of p, and what is
 // kept is divided by the share that truly is, (65536 - T) / 65536.  32 bits take two
-// calls for eight elements: 8192 x 4096 bf16 33 us, so 24.5 (134 MB, 5.5 TB/s, a
+// calls for eight elements: 8192 x 4096 bf16 33 us, one call 25 (134 MB, 5.4 TB/s, a
 // copy's rate); in the forward residual sum 60 and 54.
 #ifndef MMAOPS_RANDOM_H
 #define MMAOPS_RANDOM_H

@@ -12,6 +12,13 @@
 //   dgate = post_w s1 + post_b s0
 // (bh = b where there is no post norm).  All in FP32; h is made from r as it
 // is before r's rounding.
+//
+// One pass over the data: a row stays in its lanes' registers from the loads to
+// the stores, and the next row's loads are under way meanwhile.  Bound by memory
+// (one MI355X, 8192 x 4096 bf16, both rms norms, gate, dropout): forward 53 us for
+// 268 MB, 5.0 TB/s (197 where a row is read for each of its sums), backward 81 for
+// 403 MB, 5.0 TB/s, and 6.4 for the sums of the workgroups' partial rows (239 and 71).
+// Layer norms: 57, and 87 and 9.
 #ifndef MMAOPS_RESIDUAL_H
 #define MMAOPS_RESIDUAL_H
 
@@ -55,7 +62,9 @@ __device__ __forceinline__ void param(const void* p, int c, int n, float fill, f
 }
 
 // --------------------------------------------------- rows of any length
-// One workgroup a row, the row read again for each of its sums.
+// One workgroup a row, the row read again for each of its sums (backward of 2048 x
+// 16384 bf16: 161 us for both inputs' gradients, 66 for the vectors', 1.9 TB/s of
+// what has to be read and written once).
 
 // Mean and rstd of a row whose elements fn(c, n, v) gives, 0 past its end.
 template <int GT, int V, typename FN>
@@ -332,7 +341,7 @@ __global__ __launch_bounds__(256) void join_long_sums_kernel(JoinArgs a, int64_t
 // A row is held by whole waves, no more than it needs: W of them where a
 // workgroup has G > 1 rows (or W = 1), up to W where it has one, as many as the
 // workgroup has.  (Powers of two of waves left lanes idle, and bytes in flight with
-// them: 13107 x 2560 bf16 forward 78 us, so 58; 6553 x 5120 backward 136 and 91.)
+// them: 13107 x 2560 bf16 forward 78 us, this way 58; 6553 x 5120 backward 136 and 91.)
 template <int W, int G>
 __device__ __forceinline__ int row_lanes() {
   return G > 1 || W == 1 ? W * 64 : (int)blockDim.x;
@@ -581,7 +590,7 @@ __global__ __launch_bounds__(W * 64 * G, 4) void join_backward_kernel(JoinArgs a
   // is not wanted, goes where the branch's gradient will be written over it, or to
   // spare rows.  Behind a branch they could not be counted, and the wait for a
   // row's loads would be one for the stores behind them (8192 x 4096 bf16, both rms
-  // norms, gate, dropout: 95 us, so 81).
+  // norms, gate, dropout: that way 95 us, this way 81).
   const void* const dr_p = a.dr ? a.dr : a.dh;
   const int64_t dr_ld = a.dr ? a.lddr : a.lddh;
   const void* const dh_p = a.pre != kNormNone ? a.dh : dr_p;
