@@ -230,3 +230,29 @@ def test_gated_structures_are_what_the_binding_packs(tmp_path):
                     os.path.join(ROOT, "include"), str(src), "-o", exe], check=True)
     out = subprocess.run([exe], capture_output=True, text=True).stdout.split()
     assert out == [str(s.size) for s in (block._GATED, block._GATED_BACKWARD)]
+
+
+@pytest.mark.parametrize("wanted", [(True, True, False, True), (False, True), (False, False)])
+@pytest.mark.parametrize("grad", [True, False])
+def test_vectors_of_one_allocation_are_tensors_like_any_other(wanted, grad):
+    """Each may be added to in place, under autograd too, and has a version of its own."""
+    torch = pytest.importorskip("torch")
+
+    class Call:
+        @staticmethod
+        def empty(shape, dtype):
+            return torch.empty(shape, dtype=dtype)
+
+    with torch.set_grad_enabled(grad):
+        got = block._several(Call, wanted, 3, torch.float32)
+    assert [v is not None for v in got] == list(wanted)
+    got = [v for v in got if v is not None]
+    for i, v in enumerate(got):
+        assert tuple(v.shape) == (3,) and v.is_contiguous() and not v.requires_grad
+        v.fill_(i)
+    versions = [v._version for v in got]
+    for v in got[:1]:
+        v.add_(torch.ones(3, requires_grad=True))
+        assert v.requires_grad
+    assert [v._version for v in got[1:]] == versions[1:]
+    assert [v.tolist() for v in got[1:]] == [[i] * 3 for i in range(1, len(got))]
