@@ -12,7 +12,7 @@
 //   dX = dg Wg^T + du Wu^T   one product with an inner size of 2 N
 //   dWg = X^T dg, dWu = X^T du   the tiles of both in one launch
 //
-// Measured (one MI355X).  4096 x 4096 x 4096 bf16, gelu, both biases: 207 us for
+// Measured (one MI355X).  4096 x 4096 x 4096 bf16, gelu, both biases: 207 us and more for
 // 275 GFLOP (1.33 PFLOP/s, the plain product's rate; 569 on small tiles).  Its
 // backward pass from checkpoints: dg and du 29, dX 210, both dW 240.  1 x 4096 x
 // 4096 bf16, both W N x K: 13 (67 MB, again and again; 16 from memory, 4.2 TB/s).
