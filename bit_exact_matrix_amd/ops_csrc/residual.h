@@ -623,6 +623,12 @@ __global__ __launch_bounds__(W * 64 * G, 4) void join_backward_kernel(JoinArgs a
     pm = a.post == kNormLayer ? a.post_mean[at] : 0.0f;
     pr = a.post != kNormNone ? a.post_rstd[at] : 1.0f;
   };
+  // a row past the end has another's elements and statistics, which may be no
+  // numbers: they are cleared, and not multiplied with 0
+  auto none = [](float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.0f;
+  };
   int64_t row = (int64_t)blockIdx.x * G + g;
   fetch(row);
   // every group of the workgroup takes as many turns (rows past the end
@@ -634,14 +640,12 @@ __global__ __launch_bounds__(W * 64 * G, 4) void join_backward_kernel(JoinArgs a
       float rh[V], h[V], d[V];
       unpack(rr, rh);
       unpack(dh, d);
-      if (WHOLE && G > 1 && !live) {  // another row's elements
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = 0.0f;
-      }
+      for (int i = 0; i < V; ++i) rh[i] = (rh[i] - m) * rs;
+      if (G > 1 && !live) none(d), none(rh);
       s[0] = s[1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        rh[i] = (rh[i] - m) * rs;
         h[i] = d[i] * pre_w[i];
         s[0] += h[i];
         s[1] += h[i] * rh[i];
@@ -656,13 +660,10 @@ __global__ __launch_bounds__(W * 64 * G, 4) void join_backward_kernel(JoinArgs a
     } else {
       unpack(dr, t);
     }
-    if (WHOLE && G > 1 && !live) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) t[i] = 0.0f;
-    }
     unpack(br, b);
 #pragma unroll
     for (int i = 0; i < V; ++i) b[i] = (b[i] - pm) * pr;
+    if (G > 1 && !live) none(t), none(b);
     const float pr_now = pr;
     if (r0 + step < a.rows) fetch(row + step);
     if (live) {

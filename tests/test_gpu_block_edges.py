@@ -188,3 +188,30 @@ def test_more_columns_than_a_grid_has(torch_dev):
     y = mm.dropout(dr, 0.5, 3, 4)
     m = ref.mask([1], 64, 0.5, 3, 4, dev)
     assert torch.equal(y[1:, :64].double(), 2 * m)
+
+
+@pytest.mark.parametrize("cols", [512, 500, 1024, 1536, 2048])
+@pytest.mark.parametrize("post", [None, "rms"])
+def test_last_rows_that_are_not_finite_where_they_are_dropped(torch_dev, cols, post):
+    """A workgroup works on several of these rows, and where the matrix has fewer, the
+    places of the others take no part: not with what the last row holds."""
+    torch, dev = torch_dev
+    for rows in (1, 3, 5, 2049):
+        say("dropped infinities in the last row", cols, post, rows)
+        how = dict(post=post, dropout=0.5, seed=3, offset=rows)
+        branch = matrix(torch, dev, rows, cols, torch.bfloat16, 1)
+        dr = matrix(torch, dev, rows, cols, torch.bfloat16, 2)
+        v = torch.rand(cols, device=dev).bfloat16()
+        params = mm.ResidualParams(gate=v, post_weight=v if post else None)
+        kept = ref.mask(rows, cols, 0.5, 3, rows, dev)[-1] != 0
+        x = torch.zeros_like(branch)
+        _, _, stats = mm.residual_norm(x, branch, params, **how)
+        _, _, want = mm.residual_norm_backward(dr, None, None, branch, params, stats, **how)
+        branch[-1, ~kept] = float("inf")
+        if post:
+            stats.post_rstd[-1] = float("nan")
+        _, _, got = mm.residual_norm_backward(dr, None, None, branch, params, stats, **how)
+        for a, b in zip(got, want):
+            if a is not None:
+                assert torch.equal(a[~kept], b[~kept])
+                assert bool(torch.isfinite(a[~kept]).all())
