@@ -557,9 +557,8 @@ __global__ __launch_bounds__(W * 64 * G, NV == 1 ? 5 : 4) void join_kernel(JoinA
 // G rows at a time (WHOLE: all of a row's lanes have them).  What a row's sums need is made again from the
 // loaded elements after they have met.  Each matrix's next row is loaded as soon as
 // this one's has been used, with no registers of its own.  An element past a
-// row's end adds 0 to the row's sums, as its dh is 0 in the first ones and inner_w
-// in the second (unless the row's statistics are not finite, and then neither is
-// the row).
+// row's end adds 0 to the row's sums: its dh is 0 in the first ones and inner_w
+// in the second.
 template <int DT, int PDT, int V, int W, int G, bool SHIFT, bool WHOLE>
 __global__ __launch_bounds__(W * 64 * G, 4) void join_backward_kernel(JoinArgs a) {
   using E = elem_t<DT>;
@@ -623,11 +622,18 @@ __global__ __launch_bounds__(W * 64 * G, 4) void join_backward_kernel(JoinArgs a
     pm = a.post == kNormLayer ? a.post_mean[at] : 0.0f;
     pr = a.post != kNormNone ? a.post_rstd[at] : 1.0f;
   };
-  // a row past the end has another's elements and statistics, which may be no
-  // numbers: they are cleared, and not multiplied with 0
+  // A row past the end has another's elements and statistics, which may be no
+  // numbers, and an element past a row's end is the row's mean below 0, which its
+  // rstd may take past a float: they are cleared, and not multiplied with 0.
   auto none = [](float (&v)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = 0.0f;
+  };
+  auto only = [&](float (&v)[V], bool live) {
+    if (G > 1 && !live) none(v);
+    if (WHOLE) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = i < n ? v[i] : 0.0f;
   };
   int64_t row = (int64_t)blockIdx.x * G + g;
   fetch(row);
@@ -642,7 +648,8 @@ __global__ __launch_bounds__(W * 64 * G, 4) void join_backward_kernel(JoinArgs a
       unpack(dh, d);
 #pragma unroll
       for (int i = 0; i < V; ++i) rh[i] = (rh[i] - m) * rs;
-      if (G > 1 && !live) none(d), none(rh);
+      if (G > 1 && !live) none(d);
+      only(rh, live);
       s[0] = s[1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -663,7 +670,8 @@ __global__ __launch_bounds__(W * 64 * G, 4) void join_backward_kernel(JoinArgs a
     unpack(br, b);
 #pragma unroll
     for (int i = 0; i < V; ++i) b[i] = (b[i] - pm) * pr;
-    if (G > 1 && !live) none(t), none(b);
+    if (G > 1 && !live) none(t);
+    only(b, live);
     const float pr_now = pr;
     if (r0 + step < a.rows) fetch(row + step);
     if (live) {

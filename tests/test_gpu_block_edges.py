@@ -215,3 +215,35 @@ def test_last_rows_that_are_not_finite_where_they_are_dropped(torch_dev, cols, p
             if a is not None:
                 assert torch.equal(a[~kept], b[~kept])
                 assert bool(torch.isfinite(a[~kept]).all())
+
+
+@pytest.mark.parametrize("cols", [1, 8, 60, 100])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_equal_rows_of_large_values(torch_dev, cols, dtype):
+    """A row of equal values has an rstd of 1 / sqrt(eps): with a mean of 2^120 their
+    product is past a float, and no element of the row is that far from its mean.
+    (The row's sum has to be a float: 100 2^120 < 2^127.)"""
+    torch, dev = torch_dev
+    dt = getattr(torch, dtype)
+    for rows in (1, 5):
+        say("equal rows", cols, dtype, rows)
+        big = torch.full((rows, cols), 2.0 ** 120, device=dev, dtype=dt)
+        none = torch.zeros_like(big)
+        how = dict(post="layer", pre="layer")
+        # the norm of equal values is 0, in both places
+        r, h, stats = mm.residual_norm(big, big, mm.ResidualParams(), **how)
+        assert torch.equal(r, big) and not bool(h.any())
+        dr, dh = (matrix(torch, dev, rows, cols, dt, s) for s in (1, 2))
+        v = torch.ones(cols, device=dev, dtype=dt)
+        p = mm.ResidualParams(None, v, v, v, v)
+        dx, db, grads = mm.residual_norm_backward(dr, dh, r, big, p, stats, **how)
+        centred = dh.double() - dh.double().mean(dim=1, keepdim=True)
+        want = dr.double() + stats.rstd.double()[:, None] * centred
+        for t in (dx, db, *grads[1:]):
+            assert bool(torch.isfinite(t).all())
+        assert not bool(grads.pre_weight.any()) and not bool(grads.post_weight.any())
+        # the mean's sum and the rounding of dx: half a step, and 2^-20 of what is added
+        far = dr.double().abs() + stats.rstd.double()[:, None] * dh.double().abs().amax(
+            dim=1, keepdim=True)
+        bound = want.abs() * torch.finfo(dt).eps + far * 2.0 ** -18
+        assert bool(((dx.double() - want).abs() <= bound).all())
