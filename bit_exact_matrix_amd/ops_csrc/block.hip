@@ -64,6 +64,37 @@ int join_head(const ARGS& r, DropArgs* d) {
   return MMAEMU_OK;
 }
 
+// The arguments without those that the call does not read: the vectors of a norm
+// that is not there, whose pointers may be anything, and what goes with them.  The
+// checks and the kernels see only what is left.
+mma_residual_norm_args in_use(mma_residual_norm_args r) {
+  if (r.post == kNormNone) {
+    r.post_weight = r.post_bias = nullptr;
+    r.post_mean = r.post_rstd = nullptr;
+  }
+  if (r.pre == kNormNone) {
+    r.pre_weight = r.pre_bias = nullptr;
+    r.mean = r.rstd = nullptr;
+    r.H = nullptr;
+  }
+  return r;
+}
+
+mma_residual_norm_backward_args in_use(mma_residual_norm_backward_args r) {
+  if (r.post == kNormNone) {
+    r.post_weight = r.post_bias = nullptr;
+    r.post_rstd = nullptr;
+    if (!r.dgate) r.branch = nullptr;
+  }
+  if (r.pre == kNormNone) {
+    r.dH = r.R = r.pre_weight = nullptr;
+    r.rstd = nullptr;
+  }
+  if (r.post != kNormLayer) r.post_mean = nullptr;
+  if (r.pre != kNormLayer) r.mean = nullptr;
+  return r;
+}
+
 int check_join(const mma_residual_norm_args& r, DropArgs* d) {
   const int rc = join_head(r, d);
   if (rc) return rc;
@@ -195,10 +226,9 @@ int check_join_backward(const mma_residual_norm_backward_args& r, int64_t ws_byt
   if (rc) return rc;
   if (r.reserved) return MMAEMU_ERR_UNSUPPORTED;
   const bool post = r.post != kNormNone, pre = r.pre != kNormNone;
-  const bool branch = r.branch && (post || r.dgate);
   if (r.cols < 1 || (r.dR && !shape_ok(r.rows, r.cols, r.lddr)) ||
       (pre && (!shape_ok(r.rows, r.cols, r.lddh) || !shape_ok(r.rows, r.cols, r.ldr))) ||
-      (branch && !shape_ok(r.rows, r.cols, r.ldb)) ||
+      (r.branch && !shape_ok(r.rows, r.cols, r.ldb)) ||
       (r.dX && !shape_ok(r.rows, r.cols, r.lddx)) ||
       (r.dbranch && !shape_ok(r.rows, r.cols, r.lddb)) || !shape_ok(r.rows, r.cols, r.cols))
     return MMAEMU_ERR_SHAPE;
@@ -225,11 +255,9 @@ int check_join_backward(const mma_residual_norm_backward_args& r, int64_t ws_byt
   const int64_t need = join_plan(r).bytes;
   if (need && (!ws || ws_bytes < need)) return MMAEMU_ERR_SCRATCH;
   v.reads(view(r.dR, r.rows, r.cols, r.lddr, e));
-  if (pre) {
-    v.reads(view(r.dH, r.rows, r.cols, r.lddh, e));
-    v.reads(view(r.R, r.rows, r.cols, r.ldr, e));
-  }
-  if (branch) v.reads(view(r.branch, r.rows, r.cols, r.ldb, e));
+  v.reads(view(r.dH, r.rows, r.cols, r.lddh, e));
+  v.reads(view(r.R, r.rows, r.cols, r.ldr, e));
+  v.reads(view(r.branch, r.rows, r.cols, r.ldb, e));
   v.reads(view(r.state, 1, 2, 0, 8));
   const void* const vectors[4] = {r.gate, r.post_weight, r.post_bias, r.pre_weight};
   const float* const stats[4] = {r.post_mean, r.post_rstd, r.mean, r.rstd};
@@ -682,7 +710,7 @@ int mma_dropout(int dtype, const void* X, int64_t ldx, const void* residual, int
 
 int mma_residual_norm(const mma_residual_norm_args* args, void* hip_stream) {
   if (!args) return MMAEMU_ERR_NULL;
-  const mma_residual_norm_args& r = *args;
+  const mma_residual_norm_args r = in_use(*args);
   JoinArgs a;
   memset(&a, 0, sizeof a);
   const int rc = check_join(r, &a.drop);
@@ -701,9 +729,9 @@ int mma_residual_norm(const mma_residual_norm_args* args, void* hip_stream) {
   a.h = r.H;
   a.ldh = r.ldh;
   a.post_mean = r.post == kNormLayer ? r.post_mean : nullptr;
-  a.post_rstd = r.post != kNormNone ? r.post_rstd : nullptr;
+  a.post_rstd = r.post_rstd;
   a.mean = r.pre == kNormLayer ? r.mean : nullptr;
-  a.rstd = r.pre != kNormNone ? r.rstd : nullptr;
+  a.rstd = r.rstd;
   a.rows = r.rows;
   a.cols = (int)r.cols;
   a.post = r.post;
@@ -718,14 +746,15 @@ int mma_residual_norm(const mma_residual_norm_args* args, void* hip_stream) {
 
 int64_t mma_residual_norm_backward_workspace(const mma_residual_norm_backward_args* args) {
   DropArgs d;
-  if (!args || check_join_backward(*args, 0, nullptr, true, &d) != MMAEMU_OK) return 0;
-  return join_plan(*args).bytes;
+  if (!args) return 0;
+  const mma_residual_norm_backward_args r = in_use(*args);
+  return check_join_backward(r, 0, nullptr, true, &d) == MMAEMU_OK ? join_plan(r).bytes : 0;
 }
 
 int mma_residual_norm_backward(const mma_residual_norm_backward_args* args, void* workspace,
                                int64_t workspace_bytes, void* hip_stream) {
   if (!args) return MMAEMU_ERR_NULL;
-  const mma_residual_norm_backward_args& r = *args;
+  const mma_residual_norm_backward_args r = in_use(*args);
   JoinArgs a;
   memset(&a, 0, sizeof a);
   const int rc = check_join_backward(r, workspace_bytes, workspace, false, &a.drop);
@@ -741,7 +770,7 @@ int mma_residual_norm_backward(const mma_residual_norm_backward_args* args, void
   }
   const JoinPlan plan = join_plan(r);
   if (!plan.sums && !r.dX && !r.dbranch) return MMAEMU_OK;
-  a.branch = r.post != kNormNone || r.dgate ? r.branch : nullptr;
+  a.branch = r.branch;
   a.ldb = r.ldb;
   a.gate = r.gate;
   a.post_w = r.post_weight;

@@ -305,7 +305,8 @@ int mma_dropout(int dtype, const void *X, int64_t ldx, const void *residual, int
 enum { MMAOPS_NORM_NONE = 0, MMAOPS_NORM_LAYER = 1, MMAOPS_NORM_RMS = 2 };
 
 /* R = scale X + gate drop(post(branch)), H = pre(R), for matrices rows x cols
- * of dtype, cols at least 1. */
+ * of dtype, cols at least 1.  The weight, bias, statistics and output of a norm
+ * that is not there may be any pointers: they are neither used nor checked. */
 typedef struct {
   int32_t dtype;
   int32_t param_dtype;     /* of the five vectors: dtype or FP32 */
@@ -321,7 +322,7 @@ typedef struct {
   const void *branch;
   int64_t ldb;
   const void *gate;        /* cols values, or NULL (1) */
-  const void *post_weight; /* or NULL (1); not read without that norm */
+  const void *post_weight; /* or NULL (1) */
   const void *post_bias;   /* or NULL (0) */
   const void *pre_weight;
   const void *pre_bias;
@@ -339,8 +340,9 @@ int mma_residual_norm(const mma_residual_norm_args *args, void *hip_stream);
 
 /* Its backward pass, with the forward pass's settings and statistics (a
  * mean for a layer norm only).  dR may be NULL (0) where there is a pre norm; dH and R
- * are read with one only.  branch is read with a post norm or for dgate.  dX, dbranch and
- * the vectors' gradients (of param_dtype): any of them NULL to leave it out. */
+ * are read with one only.  branch is read with a post norm or for dgate.  What is not
+ * read may be any pointer.  dX, dbranch and the vectors' gradients (of param_dtype): any
+ * of them NULL to leave it out. */
 typedef struct {
   int32_t dtype, param_dtype, post, pre;
   float scale;

@@ -256,3 +256,30 @@ def test_vectors_of_one_allocation_are_tensors_like_any_other(wanted, grad):
         assert v.requires_grad
     assert [v._version for v in got[1:]] == versions[1:]
     assert [v.tolist() for v in got[1:]] == [[i] * 3 for i in range(1, len(got))]
+
+
+@pytest.mark.parametrize("change", [
+    dict(post=0, post_weight=VECTORS[1] + 1), dict(post=0, post_bias=VECTORS[2] + 1),
+    dict(post=0, post_mean=STATS[0] + 1), dict(post=0, post_rstd=STATS[1] + 1),
+    dict(pre=0, pre_weight=VECTORS[3] + 1), dict(pre=0, pre_bias=VECTORS[4] + 1),
+    dict(pre=0, mean=STATS[2] + 1), dict(pre=0, rstd=STATS[3] + 1), dict(pre=0, H=Y + 1, ldh=1),
+])
+def test_residual_norm_does_not_look_at_an_absent_norm(change):
+    """Pointers of a norm that is not there may be anything: the call is refused for
+    what comes after its checks of alignment."""
+    assert _join(dict(change, R=X)) == ALIAS
+
+
+NO_POST, NO_PRE = dict(post=0, dpost_weight=0, dpost_bias=0), dict(pre=0, dpre_weight=0, dpre_bias=0)
+
+
+@pytest.mark.parametrize("change", [
+    dict(NO_POST, post_weight=VECTORS[1] + 1), dict(NO_POST, post_bias=VECTORS[2] + 1),
+    dict(NO_POST, post_mean=STATS[0] + 1), dict(NO_POST, post_rstd=STATS[1] + 1),
+    dict(NO_POST, dgate=0, branch=B + 1, ldb=1), dict(NO_PRE, pre_weight=VECTORS[3] + 1),
+    dict(NO_PRE, dH=W + 1, lddh=1), dict(NO_PRE, R=R + 1, ldr=1), dict(NO_PRE, mean=STATS[2] + 1),
+    dict(NO_PRE, rstd=STATS[3] + 1), dict(post=2, post_mean=STATS[0] + 1),
+    dict(pre=2, mean=STATS[2] + 1),
+])
+def test_residual_norm_backward_does_not_look_at_an_absent_norm(change):
+    assert _join_b(dict(change, dX=X)) == ALIAS

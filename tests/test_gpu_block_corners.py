@@ -1,0 +1,70 @@
+"""Corners of the gated block's operators: what a call leaves out."""
+import itertools
+import math
+
+import pytest
+
+import bit_exact_matrix_amd as mm
+from bit_exact_matrix_amd import block, ops
+from test_gpu_ops_linear import matrix
+from test_gpu_parity import say, torch_dev  # noqa: F401
+from test_gpu_residual_norm import vectors
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------- what a call leaves out (C entry points)
+JOIN = ("dtype param_dtype post pre scale eps p seed offset state rows cols X ldx branch ldb gate "
+        "post_weight post_bias pre_weight pre_bias R ldr H ldh post_mean post_rstd mean rstd").split()
+JOIN_BACKWARD = (
+    "dtype param_dtype post pre scale reserved p seed offset state rows cols dR lddr dH lddh R ldr "
+    "branch ldb gate post_weight post_bias pre_weight post_mean post_rstd mean rstd dX lddx dbranch "
+    "lddb dgate dpost_weight dpost_bias dpre_weight dpre_bias").split()
+
+
+def raw(torch, names, packed, call, values, *more):
+    """A call of the C entry point; tensors are given as their pointers, the rest is 0."""
+    v = [values.get(n, 0) for n in names]
+    args = packed.pack(*(t.data_ptr() if isinstance(t, torch.Tensor) else t for t in v))
+    return call(args, *more, torch.cuda.current_stream().cuda_stream)
+
+
+@pytest.mark.parametrize("cols", [72, 640, 4096, 8256, 16392])
+def test_vectors_of_a_norm_that_is_not_there_are_not_read(torch_dev, cols):
+    """They hold NaN, or are the memory of an output."""
+    torch, dev = torch_dev
+    rows, dt = 5, torch.bfloat16
+    x, b, dr, dh = (matrix(torch, dev, rows, cols, dt, i) for i in range(4))
+    nan = torch.full((cols,), math.nan, dtype=dt, device=dev)
+    v = vectors(torch, dev, cols, dt, "rms", "rms", True, True)
+    base = dict(dtype=ops.BF16, param_dtype=ops.BF16, scale=1.0, eps=1e-5, rows=rows, cols=cols,
+                gate=v.gate)
+    ld = {k: cols for k in ("ldx", "ldb", "ldr", "ldh", "lddr", "lddh", "lddx", "lddb")}
+    for post, pre in itertools.product((None, "rms"), repeat=2):
+        say("vectors without their norm", cols, post, pre)
+        p = mm.ResidualParams(v.gate, v.post_weight if post else None, None,
+                              v.pre_weight if pre else None, None)
+        r, h, stats = mm.residual_norm(x, b, p, post=post, pre=pre)
+        dx, db, grads = mm.residual_norm_backward(dr, dh if pre else None, r, b, p, stats,
+                                                  post=post, pre=pre)
+        R, H, dX, dB = (torch.empty_like(x) for _ in range(4))
+        dgate = torch.empty_like(nan)
+        kinds = dict(post=block.NORMS[post], pre=block.NORMS[pre])
+        # the vectors: of a norm that is there its own, else NaN, and (for the biases) R's memory
+        own = dict(post_weight=v.post_weight if post else nan, post_bias=0 if post else R,
+                   pre_weight=v.pre_weight if pre else nan, pre_bias=0 if pre else R)
+        rc = raw(torch, JOIN, block._JOIN, ops.mma_residual_norm,
+                 {**base, **ld, **kinds, **own, "X": x, "branch": b, "R": R, "H": H})
+        assert rc == 0 and torch.equal(R, r) and (h is None or torch.equal(H, h))
+        # statistics of a norm that is not there, and an rms norm's mean: an output's memory
+        s = {n: t if t is not None else dX for n, t in stats._asdict().items()}
+        own.update(post_bias=0 if post else dB, **s)
+        args = {**base, **ld, **kinds, **own, "dR": dr, "dH": dh if pre else dX,
+                "R": r if pre else dB, "branch": b, "dX": dX, "dbranch": dB, "dgate": dgate}
+        need = raw(torch, JOIN_BACKWARD, block._JOIN_BACKWARD,
+                   lambda a, _: ops.mma_residual_norm_backward_workspace(a), args)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        rc = raw(torch, JOIN_BACKWARD, block._JOIN_BACKWARD, ops.mma_residual_norm_backward, args,
+                 ws.data_ptr(), need)
+        assert rc == 0 and torch.equal(dX, dx) and torch.equal(dB, db)
+        assert torch.equal(dgate, grads.gate)
