@@ -557,8 +557,8 @@ __global__ __launch_bounds__(W * 64 * G, NV == 1 ? 5 : 4) void join_kernel(JoinA
 // G rows at a time (WHOLE: all of a row's lanes have them).  What a row's sums need is made again from the
 // loaded elements after they have met.  Each matrix's next row is loaded as soon as
 // this one's has been used, with no registers of its own.  An element past a
-// row's end adds 0 to the row's sums: its dh is 0 in the first ones and inner_w
-// in the second.
+// row's end adds 0 to the row's sums: its dh and rh are 0 in the first ones, its t
+// and b in the second.
 template <int DT, int PDT, int V, int W, int G, bool SHIFT, bool WHOLE>
 __global__ __launch_bounds__(W * 64 * G, 4) void join_backward_kernel(JoinArgs a) {
   using E = elem_t<DT>;
@@ -623,8 +623,9 @@ __global__ __launch_bounds__(W * 64 * G, 4) void join_backward_kernel(JoinArgs a
     pr = a.post != kNormNone ? a.post_rstd[at] : 1.0f;
   };
   // A row past the end has another's elements and statistics, which may be no
-  // numbers, and an element past a row's end is the row's mean below 0, which its
-  // rstd may take past a float: they are cleared, and not multiplied with 0.
+  // numbers, and an element past a row's end is the row's mean below 0, in t that of
+  // dh w, which its rstd may take past a float: they are cleared, and not multiplied
+  // with 0.
   auto none = [](float (&v)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = 0.0f;
@@ -670,7 +671,7 @@ __global__ __launch_bounds__(W * 64 * G, 4) void join_backward_kernel(JoinArgs a
     unpack(br, b);
 #pragma unroll
     for (int i = 0; i < V; ++i) b[i] = (b[i] - pm) * pr;
-    if (G > 1 && !live) none(t);
+    only(t, live);
     only(b, live);
     const float pr_now = pr;
     if (r0 + step < a.rows) fetch(row + step);

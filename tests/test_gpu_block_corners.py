@@ -1,10 +1,12 @@
-"""Corners of the gated block's operators: what a call leaves out."""
+"""Corners of the gated block's operators: what a call leaves out, elements past
+a row's end beside large gradients."""
 import itertools
 import math
 
 import pytest
 
 import bit_exact_matrix_amd as mm
+import ops_reference
 from bit_exact_matrix_amd import block, ops
 from test_gpu_ops_linear import matrix
 from test_gpu_parity import say, torch_dev  # noqa: F401
@@ -68,3 +70,42 @@ def test_vectors_of_a_norm_that_is_not_there_are_not_read(torch_dev, cols):
                  ws.data_ptr(), need)
         assert rc == 0 and torch.equal(dX, dx) and torch.equal(dB, db)
         assert torch.equal(dgate, grads.gate)
+
+
+# --------------------------------------------------------- past a row's end
+@pytest.mark.parametrize("cols", [60, 100, 200])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("post", ["layer", "rms"])
+def test_large_equal_gradients_of_equal_rows(torch_dev, cols, dtype, post):
+    """dh is 2^120 and r is 1 throughout: the layer norm before the next block gives
+    no gradient, exactly (cols 2^120 < 2^128 is a float, and so is their mean), but an
+    element that is not there would be 2^120 below the mean, times an rstd of 316 no
+    float.  What is left is the gradient of the norm behind the block, of dr alone:
+    its sums have at most 200 terms in no more than 16 additions each, so with some ten
+    roundings of the products the error is below 32 2^-24 of the largest term."""
+    torch, dev = torch_dev
+    dt = getattr(torch, dtype)
+    for rows in (1, 5):
+        say("large equal gradients", cols, dtype, post, rows)
+        one = torch.ones((rows, cols), device=dev, dtype=dt)
+        dr, dh = matrix(torch, dev, rows, cols, dt, 1), one * 2.0 ** 120
+        v = one[0].clone()
+        bias = v if post == "layer" else None
+        p = mm.ResidualParams(None, v, bias, v, v)
+        how = dict(post=post, pre="layer")
+        # each norm's statistics of rows of ones
+        zero = torch.zeros_like(one)
+        stats = mm.ResidualStats(*mm.residual_norm(zero, one, p, **how)[2][:2],
+                                 *mm.residual_norm(one, zero, mm.ResidualParams(),
+                                                   pre="layer")[2][2:])
+        dx, db, grads = mm.residual_norm_backward(dr, dh, one, one, p, stats, **how)
+        assert torch.equal(dx, dr)
+        d, k = dr.double(), stats.post_rstd.double()[:, None]
+        bh = (one.double() - (1.0 if post == "layer" else 0.0)) * k
+        want = k * (d - (d.mean(1, keepdim=True) if post == "layer" else 0.0)
+                    - bh * (d * bh).mean(1, keepdim=True))
+        ops_reference.close(db, want, 2.0 ** -19 * k * d.abs().amax(1, keepdim=True) * 2, "dbranch")
+        assert not bool(grads.pre_weight.any())
+        assert torch.equal(grads.pre_bias, rows * dh[0])
+        s = (d * bh).sum(0)
+        ops_reference.close(grads.post_weight, s, 2.0 ** -20 * (d * bh).abs().sum(0), "post_weight")
