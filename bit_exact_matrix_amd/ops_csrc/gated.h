@@ -294,9 +294,12 @@ __global__ __launch_bounds__(256, 4) void gate_dz_kernel(GateDzArgs a) {
       unpack(py, d);
       float f[V], s[V];
       act_both<V>(g, ACT, f, s);
+      // u may be as large as a float can be, and the slope 1.13: half of their
+      // product is a number, which a dy of 0 makes 0.  Powers of two move no other
+      // bits (above the subnormal numbers).
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float dg = d[i] * (u[i] * s[i]), du = d[i] * f[i];
+        const float dg = d[i] * (u[i] * (0.5f * s[i])) * 2.0f, du = d[i] * f[i];
         g[i] = i < n ? dg : 0.0f;
         u[i] = i < n ? du : 0.0f;
         sg[i] += g[i];

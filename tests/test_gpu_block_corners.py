@@ -1,13 +1,15 @@
 """Corners of the gated block's operators: what a call leaves out, elements past
-a row's end beside large gradients."""
+a row's end beside large gradients, kept values near the largest float."""
 import itertools
 import math
 
 import pytest
 
 import bit_exact_matrix_amd as mm
+import block_reference as ref
 import ops_reference
 from bit_exact_matrix_amd import block, ops
+from test_gpu_gated_linear import NAMES
 from test_gpu_ops_linear import matrix
 from test_gpu_parity import say, torch_dev  # noqa: F401
 from test_gpu_residual_norm import vectors
@@ -109,3 +111,49 @@ def test_large_equal_gradients_of_equal_rows(torch_dev, cols, dtype, post):
         assert torch.equal(grads.pre_bias, rows * dh[0])
         s = (d * bh).sum(0)
         ops_reference.close(grads.post_weight, s, 2.0 ** -20 * (d * bh).abs().sum(0), "post_weight")
+
+
+# ------------------------------------------- kept values near the largest float
+def one_sided(torch, dev, value, gate, dy, dtype):
+    """dy, g and u of 6 x 40: u is `value` in the first columns, g is `gate`."""
+    g = torch.full((6, 40), gate, dtype=dtype, device=dev)
+    u = torch.randn((6, 40), generator=torch.Generator(dev).manual_seed(3), device=dev).to(dtype)
+    u[:, :5] = value
+    return torch.full_like(g, dy), g, u
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_a_kept_infinity_beside_no_gradient(torch_dev, act):
+    """Slopes above 1 (gates of about 2) times the largest float are no float; times a
+    dy of 0 they are 0."""
+    torch, dev = torch_dev
+    x = matrix(torch, dev, 6, 16, torch.bfloat16, 1)
+    w = matrix(torch, dev, 16, 40, torch.bfloat16, 2)
+    for value, gate in itertools.product((math.inf, -math.inf), (1.4, 2.4)):
+        dy, g, u = one_sided(torch, dev, value, gate, 0.0, torch.bfloat16)
+        say("kept infinity, no gradient", act, value, gate)
+        got = mm.gated_linear_backward(dy, x, w, w, (g, u), activation=act)
+        assert not any(bool(t.any()) for t in got)
+        # a large number, and a small gradient: still a number
+        got = mm.gated_linear_backward(dy + 2.0 ** -100, x, w, w, (g, u), activation=act)
+        assert all(bool(torch.isfinite(t).all()) for t in got)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_a_checkpoint_at_its_bound(torch_dev, act):
+    """u is 1.875 * 2^127, the largest value that a bf16 checkpoint keeps."""
+    torch, dev = torch_dev
+    dt = torch.bfloat16
+    x = matrix(torch, dev, 6, 16, dt, 1)
+    w = matrix(torch, dev, 16, 40, dt, 2)
+    for dy, gate in itertools.product((0.0, 2.0 ** -100), (1.4, 2.4)):
+        dy, g, u = one_sided(torch, dev, 1.875 * 2.0 ** 127, gate, dy, dt)
+        say("saturated checkpoint", act)
+        kept = mm.checkpoint(g), mm.checkpoint(u)
+        gr, ur = (mm.restore(c).double() for c in kept)
+        assert float(ur.max()) == 1.875 * 2.0 ** 127
+        got = mm.gated_linear_backward(dy, x, w, w, kept, activation=act,
+                                       bias_dtype=torch.float32)
+        values, bounds = ref.gated_linear_backward(dy, x.double(), w, w, gr, ur, act, dt)
+        for name, t, v, e in zip(NAMES, got, values, bounds):
+            ops_reference.close(t, v, e, name)
