@@ -198,10 +198,11 @@ struct GateDzArgs {
 
 // What was kept whole may be an infinity where the forward pass had a number,
 // past its 16 bits: taken as a number, a gate far below 0 gives 0 (and not 0
-// times infinity).  NaN stays.
+// times infinity).  That number is the largest of BF16, for FP16 one past its own:
+// finite values stay, and so does NaN.
 template <int DT>
 __device__ __forceinline__ void as_numbers(float (&v)[8]) {
-  constexpr float kFar = DT == kFP16 ? 1e30f : 3.3e38f;
+  constexpr float kFar = DT == kFP16 ? 1e30f : 0x1.FEp127f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = v[i] > kFar ? kFar : v[i] < -kFar ? -kFar : v[i];
 }

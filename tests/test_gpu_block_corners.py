@@ -157,3 +157,22 @@ def test_a_checkpoint_at_its_bound(torch_dev, act):
         values, bounds = ref.gated_linear_backward(dy, x.double(), w, w, gr, ur, act, dt)
         for name, t, v, e in zip(NAMES, got, values, bounds):
             ops_reference.close(t, v, e, name)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu"])
+def test_the_largest_numbers_kept_whole(torch_dev, act):
+    """Finite values of g and u are taken as they are, up to bf16's largest."""
+    torch, dev = torch_dev
+    dt = torch.bfloat16
+    x = matrix(torch, dev, 6, 16, dt, 1)
+    w = matrix(torch, dev, 16, 40, dt, 2)
+    for top in (torch.finfo(dt).max, -torch.finfo(dt).max):
+        dy, g, u = one_sided(torch, dev, top, 1.0, 2.0 ** -100, dt)
+        g[:, 20:25] = abs(top)
+        say("largest numbers", act, top)
+        got = mm.gated_linear_backward(dy, x, w, w, (g, u), activation=act,
+                                       bias_dtype=torch.float32)
+        values, bounds = ref.gated_linear_backward(dy, x.double(), w, w, g.double(), u.double(),
+                                                   act, dt)
+        for name, t, v, e in zip(NAMES, got, values, bounds):
+            ops_reference.close(t, v, e, name)
