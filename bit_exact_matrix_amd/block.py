@@ -245,11 +245,13 @@ def _weights(w_gate, w_up, dt, dev):
     if w_up.shape != w_gate.shape:
         raise ValueError(f"w_up must have shape {tuple(w_gate.shape)}, got {tuple(w_up.shape)}")
     if tg != tu:
-        # of one row or column both ways of reading a weight are right
-        if 1 in w_up.shape:
-            pu, ldu, tu = (*_matrix(w_up.t() if tg else w_up, "w_up", dt, None, dev), tg)
-        else:
+        if 1 not in w_up.shape:
             raise ValueError("w_gate and w_up must be stored alike")
+        # a matrix of one column is row-major however far apart its elements are,
+        # one of one row the view of such a column
+        tg = 0 if w_up.shape[1] == 1 else 1
+        (pg, ldg), (pu, ldu) = (_matrix(w.t() if tg else w, what, dt, None, dev)
+                                for w, what in ((w_gate, "w_gate"), (w_up, "w_up")))
     return pg, ldg, pu, ldu, tg
 
 

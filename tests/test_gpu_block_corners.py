@@ -1,5 +1,6 @@
 """Corners of the gated block's operators: what a call leaves out, elements past
-a row's end beside large gradients, kept values near the largest float."""
+a row's end beside large gradients, kept values near the largest float,
+weights of one row or column."""
 import itertools
 import math
 
@@ -175,4 +176,32 @@ def test_the_largest_numbers_kept_whole(torch_dev, act):
         values, bounds = ref.gated_linear_backward(dy, x.double(), w, w, g.double(), u.double(),
                                                    act, dt)
         for name, t, v, e in zip(NAMES, got, values, bounds):
+            ops_reference.close(t, v, e, name)
+
+
+# ------------------------------------------------- weights of one row or column
+@pytest.mark.parametrize("k,n", [(1, 24), (40, 1), (1, 1)])
+def test_weights_of_one_row_or_column(torch_dev, k, n):
+    """They are rows and columns at once: any two are stored alike."""
+    torch, dev = torch_dev
+    dt = torch.bfloat16
+    x, dy = matrix(torch, dev, 9, k, dt, 1), matrix(torch, dev, 9, n, dt, 2)
+
+    def ways(seed):
+        w = matrix(torch, dev, k, n, dt, seed)
+        wide = torch.full((k, n + 7), math.nan, dtype=dt, device=dev)
+        wide[:, :n] = w
+        tall = torch.full((n, k + 7), math.nan, dtype=dt, device=dev)
+        tall[:, :k] = w.t()
+        return [w, wide[:, :n], w.t().contiguous().t(), tall[:, :k].t()]
+
+    for a, b in itertools.product(ways(3), ways(4)):
+        say("one row or column", k, n, a.stride(), b.stride())
+        y, kept = mm.gated_linear(x, a, b, keep="full")
+        want, _, _, ey, _, _ = ref.gated_linear(x, a, b, None, None, "silu")
+        ops_reference.close(y, want, ey, "y")
+        values, bounds = ref.gated_linear_backward(dy, x.double(), a, b, kept[0].double(),
+                                                   kept[1].double(), "silu", dt)
+        for name, t, v, e in zip(NAMES, mm.gated_linear_backward(dy, x, a, b, kept), values,
+                                 bounds):
             ops_reference.close(t, v, e, name)
