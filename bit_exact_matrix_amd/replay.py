@@ -231,10 +231,11 @@ def replay_gated(rows=4096, dim=1024, hidden=4096, dtype="bf16", model="hopper",
     import torch
     dt = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
     p, x, branch, dr, dh = make_gated(rows, dim, hidden, dt, seed)
+    mask = seed % 2 ** 64  # torch's generators take negative seeds, dropout does not
     runs = []
     for _ in range(2):
-        r2, h2, saved = gated_forward(x, branch, p, dropout, seed)
-        back = gated_backward(dr, dh, saved, p, dropout, seed)
+        r2, h2, saved = gated_forward(x, branch, p, dropout, mask)
+        back = gated_backward(dr, dh, saved, p, dropout, mask)
         runs.append(gated_outputs(r2, h2, saved, *back))
     same = all(same_bits(a, b) for a, b in zip(*runs))
     sample = torch.linspace(0, rows - 1, min(rows, 16), device=x.device).long()

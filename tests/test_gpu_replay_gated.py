@@ -131,3 +131,10 @@ def test_the_step_in_a_captured_graph(torch_dev):
         torch.cuda.synchronize()
         got = [t.clone() for t in out]
         assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+def test_a_negative_seed(torch_dev):
+    """As the plain block's replay takes it."""
+    say("replay of the gated block, negative seed")
+    found = [replay.replay(64, 128, 256, seed=-1), replay.replay_gated(64, 128, 256, seed=-1)]
+    assert all(f["repeats"] for f in found)
