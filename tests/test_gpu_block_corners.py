@@ -1,6 +1,6 @@
 """Corners of the gated block's operators: what a call leaves out, elements past
 a row's end beside large gradients, kept values near the largest float,
-weights of one row or column."""
+weights of one row or column, inputs and outputs on their own."""
 import itertools
 import math
 
@@ -10,7 +10,7 @@ import bit_exact_matrix_amd as mm
 import block_reference as ref
 import ops_reference
 from bit_exact_matrix_amd import block, ops
-from test_gpu_gated_linear import NAMES
+from test_gpu_gated_linear import NAMES, operands
 from test_gpu_ops_linear import matrix
 from test_gpu_parity import say, torch_dev  # noqa: F401
 from test_gpu_residual_norm import vectors
@@ -205,3 +205,66 @@ def test_weights_of_one_row_or_column(torch_dev, k, n):
         for name, t, v, e in zip(NAMES, mm.gated_linear_backward(dy, x, a, b, kept), values,
                                  bounds):
             ops_reference.close(t, v, e, name)
+
+
+# ------------------------------------------------ outputs and inputs on their own
+@pytest.mark.parametrize("dtype,cols", [("bfloat16", 640), ("bfloat16", 1024), ("bfloat16", 4096),
+                                        ("float32", 1000), ("float32", 1024), ("float32", 5120),
+                                        ("bfloat16", 8256)])
+@pytest.mark.parametrize("post,pre", [("rms", "layer"), (None, "rms")])
+def test_without_the_gradient_of_the_sum(torch_dev, dtype, cols, post, pre):
+    """dr=None, behind the last block: what dr=0 gives, and the formula."""
+    torch, dev = torch_dev
+    dt = getattr(torch, dtype)
+    rows = 37
+    x, b, dh = (matrix(torch, dev, rows, cols, dt, i) for i in range(3))
+    v = vectors(torch, dev, cols, dt, post, pre, True, pre == "layer")
+    how = dict(post=post, pre=pre, scale=0.7, dropout=0.25, seed=11, offset=12)
+    say("no gradient of the sum", dtype, cols, post, pre)
+    r, _, stats = mm.residual_norm(x, b, v, **how)
+    got = mm.residual_norm_backward(None, dh, r, b, v, stats, **how)
+    zero = mm.residual_norm_backward(torch.zeros_like(dh), dh, r, b, v, stats, **how)
+    for s, t in zip((*got[:2], *got[2]), (*zero[:2], *zero[2])):
+        assert (s is None) == (t is None) and (s is None or torch.equal(s, t))
+    m = ref.mask(rows, cols, 0.25, 11, 12, dev)
+    val, off = ref.residual_norm_backward(None, dh, r, b, v, stats, post, pre, 0.7, m)
+    for k, t in {"dx": got[0], "dbranch": got[1], **got[2]._asdict()}.items():
+        if t is not None:
+            ops_reference.close(t, val[k], off[k], k)
+
+
+@pytest.mark.parametrize("dtype,cols", [("bfloat16", 5120), ("bfloat16", 8192), ("float32", 1000),
+                                        ("float32", 5120), ("float32", 8200)])
+def test_gradients_without_those_of_the_vectors(torch_dev, dtype, cols):
+    """dx and dbranch have the same bits on their own, rows of 9 to 16 waves and the
+    gradients of biases among what is left out."""
+    torch, dev = torch_dev
+    dt = getattr(torch, dtype)
+    x, b, dr, dh = (matrix(torch, dev, 600, cols, dt, i) for i in range(4))
+    v = vectors(torch, dev, cols, dt, "layer", "layer", True, True)
+    how = dict(post="layer", pre="layer")
+    say("gradients without the vectors'", dtype, cols)
+    r, _, stats = mm.residual_norm(x, b, v, **how)
+    dx, db, _ = mm.residual_norm_backward(dr, dh, r, b, v, stats, **how)
+    for need in itertools.product((False, True), repeat=2):
+        got = mm.residual_norm_backward(dr, dh, r, b, v, stats, need_dx=need[0],
+                                        need_dbranch=need[1], need_dparams=False, **how)
+        assert got[0] is None or torch.equal(got[0], dx)
+        assert got[1] is None or torch.equal(got[1], db)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1024, 1024), (64, 48, 40), (299, 260, 640), (520, 1040, 96),
+                                   (1100, 1300, 65), (2048, 512, 512)])
+@pytest.mark.parametrize("saved", [False, True])
+def test_bias_gradients_on_their_own(torch_dev, m, n, k, saved):
+    """The same bits from the small pass's second launch and from a kernel of their own."""
+    torch, dev = torch_dev
+    x, wg, wu = operands(torch, dev, m, n, k, torch.bfloat16, "kn", 1, 0)
+    dy, g, u = (matrix(torch, dev, m, n, torch.bfloat16, i) for i in (3, 4, 5))
+    kept = (mm.checkpoint(g), mm.checkpoint(u)) if saved else (g, u)
+    say("bias gradients on their own", m, n, k, saved)
+    want = mm.gated_linear_backward(dy, x, wg, wu, kept, bias_dtype=torch.float32)[3:]
+    for need in itertools.product((False, True), repeat=2):
+        got = mm.gated_linear_backward(dy, x, wg, wu, kept, need_dx=need[0], need_dw=need[1],
+                                       bias_dtype=torch.float32)[3:]
+        assert all(torch.equal(s, t) for s, t in zip(got, want)), need
