@@ -174,8 +174,8 @@ hipError_t join_launch(const JoinArgs& a, hipStream_t s) {
 
 // The backward pass: elements a lane and waves a row (8 elements of FP32, two
 // vectors, take the registers that one vector of the 16-bit types does: 3276 x 5120
-// 212 us in several passes over the rows, in one 128), and the rows that a workgroup
-// works on at a time.
+// 212 us in several passes over the rows, in one 127, with biases 186), and the rows
+// that a workgroup works on at a time.
 struct BackPlan {
   int v, waves, rows;  // waves 0: in several passes
 };

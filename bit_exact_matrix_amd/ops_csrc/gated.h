@@ -8,14 +8,17 @@
 //
 // Backward.  One pass over dY and what was kept gives
 //   dg = dY u act'(g),  du = dY act(g)
-// rounded to the operands' type, and their column sums before that.  Then
+// rounded to the operands' type, which is what the matrix cores multiply at their rate
+// (as dz of a plain product: in FP16 past 65504 an infinity, as in any 16-bit gradient),
+// and their column sums before that.  Then
 //   dX = dg Wg^T + du Wu^T   one product with an inner size of 2 N
 //   dWg = X^T dg, dWu = X^T du   the tiles of both in one launch
 //
 // Measured (one MI355X).  4096 x 4096 x 4096 bf16, gelu, both biases: 207 us and more for
 // 275 GFLOP (1.33 PFLOP/s, the plain product's rate; 569 on small tiles).  Its
-// backward pass from checkpoints: dg and du 29, dX 210, both dW 240.  1 x 4096 x
-// 4096 bf16, both W N x K: 13 (67 MB, again and again; 16 from memory, 4.2 TB/s).
+// backward pass from checkpoints: dg and du 33 (silu 29), dX 210 (both W N x K 229), both
+// dW 240.  1 x 4096 x 4096 bf16, both W N x K: 13 (67 MB, again and again; 16 from
+// memory, 4.2 TB/s).
 #ifndef MMAOPS_GATED_H
 #define MMAOPS_GATED_H
 
@@ -76,7 +79,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void two_kernel(TwoArgs p) {
 // A small backward pass's second launch: the tiles of dg Wg^T + du Wu^T, those of
 // both weight gradients, then the column sums of both biases, 64 columns a
 // workgroup; all need only the first launch's results.  Launches bound such a
-// pass (fp16, silu, 299 x 260 x 640, on the GPU: four launches 27 us, two 14.5).
+// pass (fp16, gelu, 299 x 260 x 640, on the GPU: four launches 27 us, two 14.5).
 struct SmallArgs {
   LongArgs dx;
   TwoArgs dw;
@@ -258,8 +261,9 @@ __device__ __forceinline__ void act_both(const float (&z)[V], const int act, flo
 // dg, du and their column sums over the workgroup's run of rows: 64 lanes of
 // 8 columns, four waves over the rows, the waves' sums added in wave order.  The
 // activation is the kernel's own: with a switch in it, it held the registers
-// of the largest.  Bound by memory (4096 x 4096 bf16 from both checkpoints: 26.3
-// to 28.6 us for 135 MB, 5 TB/s), so dg and du leave in one pass.
+// of the largest.  Bound by memory (4096 x 4096 bf16 from both checkpoints: silu 26.3
+// to 28.6 us for 135 MB, 5 TB/s; gelu's arithmetic 30 to 35), so dg and du leave in one
+// pass.
 template <int DT, int ACT, bool SAVED>
 __global__ __launch_bounds__(256, 4) void gate_dz_kernel(GateDzArgs a) {
   constexpr int V = 8;

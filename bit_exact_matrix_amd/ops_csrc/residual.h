@@ -18,7 +18,15 @@
 // (one MI355X, 8192 x 4096 bf16, both rms norms, gate, dropout): forward 53 us for
 // 268 MB, 5.0 TB/s (197 where a row is read for each of its sums), backward 81 for
 // 403 MB, 5.0 TB/s, and 6.4 for the sums of the workgroups' partial rows (239 and 71).
-// Layer norms: 57, and 87 and 9.
+// Layer norms: 57, and 87 and 9.  FP32 (537 and 805 MB): forward 105, backward 148 and 5.
+//
+// What does not fit the registers.  A CU's 16 waves have 128 a lane each.  FP32
+// vectors beside 16-bit matrices, in rows of two vectors a lane forward, take 80 for the
+// vectors alone (2048 x 16384 177 us; vectors in 16 bits 62; one vector a lane, 4096 x
+// 8192, 69 and 62), and backward rows of 9 to 16 waves with biases hold four sums beside
+// their four matrices (4096 x 8192 bf16 169 us, without biases 82; 3276 x 5120 FP32, 8
+// elements a lane, 180 and 122).  There the compiler spills up to 101 registers, whose
+// loads the waits for a row's loads then count too.
 #ifndef MMAOPS_RESIDUAL_H
 #define MMAOPS_RESIDUAL_H
 
@@ -62,9 +70,10 @@ __device__ __forceinline__ void param(const void* p, int c, int n, float fill, f
 }
 
 // --------------------------------------------------- rows of any length
-// One workgroup a row, the row read again for each of its sums (backward of 2048 x
-// 16384 bf16: 161 us for both inputs' gradients, 66 for the vectors', 1.9 TB/s of
-// what has to be read and written once).
+// One workgroup a row, the row read again for each of its sums.  2048 x 16384, what
+// has to be read and written once: backward bf16 161 us for both inputs' gradients and
+// 66 for the vectors', 1.8 TB/s, FP32 271 and 126; forward FP32 213, 2.5 TB/s (1024 x
+// 32768 bf16 120).
 
 // Mean and rstd of a row whose elements fn(c, n, v) gives, 0 past its end.
 template <int GT, int V, typename FN>
@@ -451,7 +460,8 @@ __device__ __forceinline__ void held_stats(float (&v)[NV][V], int lane, int lane
 
 // A lane has NV vectors of 16 bytes of each matrix's row; a workgroup works on
 // G rows at a time (several only where a row is a wave) and walks the matrices,
-// the next rows' loads under way.
+// the next rows' loads under way.  (FP32 vectors beside 16-bit matrices: see above
+// for what they take.)
 template <int DT, int PDT, int W, int NV, int G>
 __global__ __launch_bounds__(W * 64 * G, NV == 1 ? 5 : 4) void join_kernel(JoinArgs a) {
   constexpr int V = kVec<DT>;
